@@ -140,20 +140,20 @@ class HipEvents:
 # Stages grouped by the kernel that runs them, with the sources that kernel is
 # built from (a counter summary is valid only for those sources).
 KERNELS = {
-    "gemm_fwd": (("fc1", "fc2"), ("fq_gemm.hip",)),
-    "gemm_dgrad": (("fc2_dgrad", "fc1_dgrad"), ("fq_gemm.hip",)),
-    "gemm_wgrad": (("fc2_wgrad", "fc1_wgrad"), ("fq_gemm.hip",)),
+    "gemm_fwd": (("fc1", "fc2"), ("fq_gemm.hip", "fq_mfma.h")),
+    "gemm_dgrad": (("fc2_dgrad", "fc1_dgrad"), ("fq_gemm.hip", "fq_mfma.h")),
+    "gemm_wgrad": (("fc2_wgrad", "fc1_wgrad"), ("fq_gemm.hip", "fq_mfma.h")),
     "tensor_fwd": (("w1_fq", "w2_fq"), ("fq_tensor.hip",)),
     # nvfp4: nothing (formed in gemm_wgrad's epilogue); INT/FP8: sums of its partials
-    "weight_scale_grad": (("w1_scale_grad", "w2_scale_grad"), ("fq_gemm.hip", "fq_tensor.hip")),
-    "route": (("route",), ("fq_layer.hip",)),
-    "permute_a1": (("permute_a1",), ("fq_layer.hip",)),
-    "swiglu_a2": (("swiglu_a2",), ("fq_layer.hip",)),
-    "combine": (("combine",), ("fq_layer.hip",)),
-    "permute_dy": (("permute_dy",), ("fq_layer.hip",)),
-    "swiglu_bwd": (("swiglu_bwd",), ("fq_layer.hip",)),
-    "segment_sum": (("a2_sum", "a1_sum"), ("fq_layer.hip",)),
-    "unpermute_a1": (("unpermute_a1",), ("fq_layer.hip",)),
+    "weight_scale_grad": (("w1_scale_grad", "w2_scale_grad"), ("fq_gemm.hip", "fq_mfma.h", "fq_tensor.hip")),
+    "route": (("route",), ("fq_layer.hip", "fq_act.h")),
+    "permute_a1": (("permute_a1",), ("fq_layer.hip", "fq_act.h")),
+    "swiglu_a2": (("swiglu_a2",), ("fq_layer.hip", "fq_act.h")),
+    "combine": (("combine",), ("fq_layer.hip", "fq_act.h")),
+    "permute_dy": (("permute_dy",), ("fq_layer.hip", "fq_act.h")),
+    "swiglu_bwd": (("swiglu_bwd",), ("fq_layer.hip", "fq_act.h")),
+    "segment_sum": (("a2_sum", "a1_sum"), ("fq_layer.hip", "fq_act.h")),
+    "unpermute_a1": (("unpermute_a1",), ("fq_layer.hip", "fq_act.h")),
 }
 COMMON_SOURCES = ("fq_common.h", "fq_internal.h")
 
