@@ -391,6 +391,47 @@ int fq_distill_loss(const fq_distill_desc* d, int64_t tokens, int64_t vocab, con
                     const int32_t* teacher_topk_ids, const int32_t* labels, float* loss, float* row_loss,
                     void* grad, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- RMS norm ----------------------------------------------------------------
+ * The norm in front of the expert layer and of the output layer, with the
+ * residual stream's addition, and for a served model its output in 8 bits:
+ *     s = bf16(x + residual)   (s = x without a residual)
+ *     r = 1 / sqrt(mean(s^2) + eps),   y = bf16(fl32(s gamma r))
+ * The statistic is formed in fp64 and y correctly rounded, so y does not
+ * depend on the order of the sum.  codes and scale are what fq_tensor gives on
+ * y: INT (8-bit ranges) or FP8 E4M3, one dynamic scale per row or group
+ * (scale receives [rows] or [rows, cols/group]), or one given scale for the
+ * tensor (FQ_PER_TENSOR, learnable or static: scale is read, [1]).
+ *
+ *   q         host; NULL or FQ_NONE: no codes (codes and scale are then NULL).
+ *   x         device bf16 [rows, cols], cols % 8 == 0, cols <= 65536, 16-B aligned.
+ *   residual  device bf16, shape of x, NULL for none; with it `sum` is written
+ *             (device bf16, shape of x; may be x or residual itself).
+ *   gamma     device bf16 [cols].
+ *   y         device bf16, shape of x, NULL to skip (may be x where no sum is written).
+ *   rstd      device fp32 [rows], r for the backward, NULL to skip.
+ *   codes     device u8, shape of x, 8-B aligned.
+ * Errors: FQ_E_INVALID (nulls, eps negative or not finite, sum without residual
+ * or the reverse, codes without q, nothing to write), FQ_E_SHAPE, FQ_E_UNSUPPORTED
+ * (4-bit formats, learnable or static scales per row or group, cols > 65536),
+ * FQ_E_ALIGN, FQ_E_HIP.  Zero rows are a no-op. */
+int fq_rms_norm_fwd(const fq_qdesc* q, int64_t rows, int64_t cols, double eps,
+                    const void* x, const void* residual, const void* gamma,
+                    void* sum, void* y, float* rstd, uint8_t* codes, float* scale, void* stream);
+
+/* Gradient of y = s gamma r (codes pass it straight through), fp32 arithmetic:
+ *     dx = bf16(dsum + r (gamma dy - s r^2 mean(gamma dy s))),  dgamma = sum over rows of dy s r
+ * dx is the gradient of x and of residual alike.
+ *   s       device bf16 [rows, cols]: the forward's sum (or x); rstd its rstd.
+ *   dy      device bf16; dsum: nullable device bf16, the gradient that reaches
+ *           s past the norm.  dx: device bf16 (may be dy or dsum).
+ *   dgamma  device fp32 [cols], NULL to skip (a frozen gamma); needs the workspace
+ *           (16-B aligned; zero rows write zeros).
+ * Errors: FQ_E_INVALID, FQ_E_SHAPE, FQ_E_UNSUPPORTED, FQ_E_ALIGN, FQ_E_WORKSPACE, FQ_E_HIP. */
+size_t fq_rms_norm_bwd_workspace_size(int64_t rows, int64_t cols);
+int fq_rms_norm_bwd(int64_t rows, int64_t cols, const void* s, const void* gamma, const float* rstd,
+                    const void* dy, const void* dsum, void* dx, float* dgamma,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- diagnostics ----------------------------------------------------------- */
 const char* fq_status_string(int32_t status);   /* static string                */
 const char* fq_last_hip_error(void);            /* thread-local; after FQ_E_HIP */

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, Structure, c_char_p, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, Structure, c_char_p, c_double, c_int32, c_int64, c_size_t, c_void_p
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # FQ_LIB selects another build of the same library (e.g. a tuning variant)
@@ -121,6 +121,11 @@ def _load():
         "fq_distill_loss": (c_int32, [POINTER(DistillDesc), c_int64, c_int64, c_void_p, c_void_p, c_void_p,
                                       c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                       c_void_p]),
+        "fq_rms_norm_fwd": (c_int32, [Q, c_int64, c_int64, c_double, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+        "fq_rms_norm_bwd_workspace_size": (c_size_t, [c_int64, c_int64]),
+        "fq_rms_norm_bwd": (c_int32, [c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -135,7 +140,8 @@ EXPORTS = ("fq_abi_version", "fq_status_string", "fq_last_hip_error", "fq_preset
            "fq_grouped_expert_workspace_size", "fq_grouped_expert_buffer",
            "fq_grouped_expert_fwd", "fq_grouped_expert_bwd", "fq_adamw_defaults",
            "fq_scale_adamw_workspace_size", "fq_scale_adamw", "fq_scale_adamw_noalloc",
-           "fq_distill_workspace_size", "fq_distill_loss")
+           "fq_distill_workspace_size", "fq_distill_loss", "fq_rms_norm_fwd",
+           "fq_rms_norm_bwd_workspace_size", "fq_rms_norm_bwd")
 
 
 def lib():
@@ -314,3 +320,91 @@ def distill_loss(d: DistillDesc, student, loss, teacher=None, top_v=None, top_i=
                               _ptr(labels), _ptr(loss), _ptr(row_loss), _ptr(grad), _ptr(workspace),
                               _nbytes(workspace), _stream(stream))
     _check(st, "fq_distill_loss")
+
+
+# ----------------------------------------------- operators around the layer --
+# These wrappers check what the C side cannot see of a tensor: its type, its
+# shape, that it is contiguous and on one GPU; they raise ValueError.  The work
+# goes to the tensors' own device and, unless `stream` is given, to the current
+# stream of that device.
+def _expect(where, name, t, dtype, shape, device):
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{where}: {name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def _scratch(where, t, device):
+    """(address, bytes) of a workspace tensor of any type."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{where}: the workspace must be a contiguous tensor on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _device_of(where, t):
+    if t.device.type != "cuda":
+        raise ValueError(f"{where}: the tensors must live on the GPU, got {t.device}")
+    return t.device
+
+
+def _call(where, fn, device, stream, *args):
+    """fn(*args, stream) with the tensors' device current; raises FqError on an error status."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, stream if stream is not None else torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream if stream is not None else torch.cuda.current_stream().cuda_stream)
+    if st != FQ_OK:
+        raise FqError(st, where)
+
+
+def rms_norm_fwd(x, gamma, eps, residual=None, sum=None, y=None, rstd=None, q: QDesc | None = None, codes=None,
+                 scale=None, stream=None):
+    """RMS norm of bf16 x [rows, cols] (fq_rms_norm_fwd): writes those of sum (bf16(x + residual)), y, rstd
+    [rows] and, with the 8-bit quantiser q, codes (uint8) that are given.  scale is written for a dynamic q
+    ([rows] or [rows, cols/group]) and read ([1]) for a per-tensor one."""
+    import torch
+    w = "rms_norm_fwd"
+    dev = _device_of(w, x)
+    if x.dim() != 2:
+        raise ValueError(f"{w}: x must be [rows, cols], got {list(x.shape)}")
+    rows, cols = x.shape
+    bf, f32 = torch.bfloat16, torch.float32
+    sshape = None
+    if scale is not None:
+        if q is None:
+            raise ValueError(f"{w}: scale needs a quantiser")
+        sshape = {FQ_PER_TENSOR: (1,), FQ_PER_ROW: (rows,)}.get(q.gran) or (rows, cols // max(q.group, 1))
+    full = (rows, cols)
+    _call(w, _lib.fq_rms_norm_fwd, dev, stream, None if q is None else ctypes.byref(q), rows, cols, eps,
+          _expect(w, "x", x, bf, full, dev), _expect(w, "residual", residual, bf, full, dev),
+          _expect(w, "gamma", gamma, bf, (cols,), dev), _expect(w, "sum", sum, bf, full, dev),
+          _expect(w, "y", y, bf, full, dev), _expect(w, "rstd", rstd, f32, (rows,), dev),
+          _expect(w, "codes", codes, torch.uint8, full, dev), _expect(w, "scale", scale, f32, sshape, dev))
+
+
+def rms_norm_bwd_workspace_size(rows: int, cols: int) -> int:
+    return _lib.fq_rms_norm_bwd_workspace_size(rows, cols)
+
+
+def rms_norm_bwd(s, gamma, rstd, dy, dx, dsum=None, dgamma=None, workspace=None, stream=None):
+    """Gradient of the norm of s (the forward's sum, or x): dx, and with dgamma (fp32 [cols], needs the
+    workspace) the gradient of gamma; dsum is the gradient that reaches s past the norm."""
+    import torch
+    w = "rms_norm_bwd"
+    dev = _device_of(w, s)
+    if s.dim() != 2:
+        raise ValueError(f"{w}: s must be [rows, cols], got {list(s.shape)}")
+    rows, cols = full = tuple(s.shape)
+    bf, f32 = torch.bfloat16, torch.float32
+    ws, nb = _scratch(w, workspace, dev)
+    _call(w, _lib.fq_rms_norm_bwd, dev, stream, rows, cols, _expect(w, "s", s, bf, full, dev),
+          _expect(w, "gamma", gamma, bf, (cols,), dev), _expect(w, "rstd", rstd, f32, (rows,), dev),
+          _expect(w, "dy", dy, bf, full, dev), _expect(w, "dsum", dsum, bf, full, dev),
+          _expect(w, "dx", dx, bf, full, dev), _expect(w, "dgamma", dgamma, f32, (cols,), dev), ws, nb)

@@ -1,0 +1,92 @@
+"""Refusals of the operators around the expert layer: every invalid call is
+answered with its status before any HIP call (no GPU needed: no pointer passed
+here is ever dereferenced), and the Python wrappers refuse tensors that the C
+side cannot see to be wrong."""
+import ctypes
+
+import pytest
+
+F = pytest.importorskip("scale_only_quantization_amd.fqlib")
+torch = pytest.importorskip("torch")
+
+FAKE = 0x100000
+MIS = 0x100002
+FP8_ROW = F.qdesc(F.FQ_FP8E4M3, F.FQ_PER_ROW, 0, F.FQ_DYNAMIC)
+
+
+def _nf(q=None, R=4, C=64, eps=1e-6, x=FAKE, res=None, g=FAKE, sum=None, y=FAKE, rstd=None, codes=None, scale=None):
+    return F.lib().fq_rms_norm_fwd(None if q is None else ctypes.byref(q), R, C, eps, x, res, g, sum, y, rstd, codes,
+                                   scale, None)
+
+
+def test_rms_norm_fwd_refusals():
+    assert _nf(R=-1) == F.FQ_E_SHAPE
+    assert _nf(R=1 << 31) == F.FQ_E_SHAPE
+    assert _nf(C=60) == F.FQ_E_SHAPE
+    assert _nf(C=0) == F.FQ_E_SHAPE
+    assert _nf(C=65544) == F.FQ_E_UNSUPPORTED
+    for e in (-1.0, float("nan"), float("inf")):
+        assert _nf(eps=e) == F.FQ_E_INVALID
+    assert _nf(x=None) == F.FQ_E_INVALID
+    assert _nf(g=None) == F.FQ_E_INVALID
+    assert _nf(y=None) == F.FQ_E_INVALID                         # nothing to write
+    assert _nf(res=FAKE) == F.FQ_E_INVALID                       # residual without sum
+    assert _nf(sum=FAKE) == F.FQ_E_INVALID
+    assert _nf(codes=FAKE) == F.FQ_E_INVALID                     # codes without a quantiser
+    assert _nf(scale=FAKE) == F.FQ_E_INVALID
+    assert _nf(q=FP8_ROW) == F.FQ_E_INVALID                      # quantiser without codes
+    assert _nf(q=FP8_ROW, codes=FAKE) == F.FQ_E_INVALID
+    for q in (F.qdesc(F.FQ_NVFP4, F.FQ_PER_GROUP, 16, F.FQ_DYNAMIC),
+              F.qdesc(F.FQ_INT, F.FQ_PER_ROW, 0, F.FQ_DYNAMIC, -8, 7),
+              F.qdesc(F.FQ_FP8E4M3, F.FQ_PER_ROW, 0, F.FQ_STATIC),
+              F.qdesc(F.FQ_FP8E4M3, F.FQ_PER_TENSOR, 0, F.FQ_DYNAMIC)):
+        assert _nf(q=q, codes=FAKE, scale=FAKE) == F.FQ_E_UNSUPPORTED, q
+    assert _nf(q=F.qdesc(F.FQ_FP8E4M3, F.FQ_PER_GROUP, 128, F.FQ_DYNAMIC), codes=FAKE, scale=FAKE) == F.FQ_E_SHAPE
+    assert _nf(q=F.qdesc(kind=9), codes=FAKE, scale=FAKE) == F.FQ_E_INVALID
+    for kw in (dict(x=MIS), dict(g=MIS), dict(y=MIS), dict(res=MIS, sum=FAKE), dict(res=FAKE, sum=MIS),
+               dict(rstd=MIS), dict(q=FP8_ROW, codes=FAKE + 4, scale=FAKE), dict(q=FP8_ROW, codes=FAKE, scale=MIS)):
+        assert _nf(**kw) == F.FQ_E_ALIGN, kw
+    assert _nf(R=0, x=None, g=None, y=None) == F.FQ_OK
+
+
+def _nb(R=4, C=64, s=FAKE, g=FAKE, r=FAKE, dy=FAKE, ds=None, dx=FAKE, dg=None, ws=None, wsb=0):
+    return F.lib().fq_rms_norm_bwd(R, C, s, g, r, dy, ds, dx, dg, ws, wsb, None)
+
+
+def test_rms_norm_bwd_refusals():
+    assert _nb(R=-1) == F.FQ_E_SHAPE
+    assert _nb(C=12) == F.FQ_E_SHAPE
+    assert _nb(C=1 << 20) == F.FQ_E_UNSUPPORTED
+    for n in ("s", "g", "r", "dy", "dx"):
+        assert _nb(**{n: None}) == F.FQ_E_INVALID, n
+        assert _nb(**{n: MIS}) == F.FQ_E_ALIGN, n
+    assert _nb(ds=MIS) == F.FQ_E_ALIGN
+    need = F.rms_norm_bwd_workspace_size(4, 64)
+    assert need == 4 * 64 * 4
+    assert F.rms_norm_bwd_workspace_size(4, 60) == 0
+    assert _nb(dg=FAKE, wsb=need) == F.FQ_E_WORKSPACE
+    assert _nb(dg=FAKE, ws=FAKE, wsb=need - 1) == F.FQ_E_WORKSPACE
+    assert _nb(dg=FAKE, ws=FAKE + 8, wsb=need) == F.FQ_E_ALIGN
+    assert _nb(R=0, s=None, g=None, r=None, dy=None, dx=None) == F.FQ_OK
+
+
+def test_wrappers_refuse_tensors():
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    g = torch.zeros(64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        F.rms_norm_fwd(x, g, 1e-6, y=x)
+    with pytest.raises(ValueError, match="GPU"):
+        F.rms_norm_bwd(x, g, torch.zeros(4), x, x)
+
+
+def test_expect_checks_type_shape_layout_and_device():
+    # the wrappers' one check, on CPU tensors
+    dev = torch.device("cpu")
+    t = torch.zeros((4, 6), dtype=torch.bfloat16)
+    assert F._expect("f", "t", t, torch.bfloat16, (4, 6), dev) == t.data_ptr()
+    assert F._expect("f", "t", None, torch.bfloat16, (4, 6), dev) is None
+    for bad, dt, shape, d in ((t, torch.float32, (4, 6), dev), (t, torch.bfloat16, (6, 4), dev),
+                              (t.t(), torch.bfloat16, (6, 4), dev), (t[:, :3], torch.bfloat16, (4, 3), dev),
+                              (t, torch.bfloat16, (4, 6), torch.device("cuda", 0))):
+        with pytest.raises(ValueError, match="contiguous"):
+            F._expect("f", "t", bad, dt, shape, d)
