@@ -432,6 +432,52 @@ int fq_rms_norm_bwd(int64_t rows, int64_t cols, const void* s, const void* gamma
                     const void* dy, const void* dsum, void* dx, float* dgamma,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- the output layer's loss from hidden states -------------------------------
+ * fq_distill_loss's cross entropy and top-k KL without logits: from the final
+ * hidden states h and the frozen output weight w, in pieces of the vocabulary,
+ * with the gradient on h (the output layer stays in high precision and frozen:
+ * the nxmr.cn article, section 二.3; the KL over the teacher's top-k tokens, so
+ * that no [tokens, vocab] tensor exists: section 二.5).
+ *     z = h w^T,   row = lm_weight (lse(z) - z[label])
+ *                      + distill_weight sum_j p_j (log p_j - z[id_j] + lse(z))
+ *     loss = sum of the rows that count / their number,  grad = d loss / d h
+ * with p the softmax of the teacher's topk logits.  A row counts if its label
+ * lies in [0, vocab), or always without labels; one that does not count
+ * (padding, e.g. a label of -1) has row loss 0 and gradient 0; where none
+ * counts the loss is 0.  Teacher ids outside [0, vocab) are absent, also from
+ * the teacher's softmax; a logit of -inf has p = 0; a row with no id left has
+ * no distillation term.  Ids may repeat.
+ * Logits and sums are fp32; probabilities enter the gradient's product rounded
+ * to bf16, except the label's and the teacher's ids', which are added in fp32.
+ * Bitwise deterministic. */
+typedef struct {
+    int64_t tokens;            /* >= 0, < 2^24                                        */
+    int64_t hidden;            /* a multiple of 64, 64 .. 16384                       */
+    int64_t vocab;             /* >= 1, < 2^31                                        */
+    int32_t topk;              /* teacher ids per token, 0 (no distillation) .. 64    */
+    float lm_weight;           /* weight of the cross entropy (needs labels)          */
+    float distill_weight;      /* weight of the top-k KL                              */
+} fq_head_desc;
+/* Bytes of device workspace (256-B aligned): with the gradient, at most about
+ * 512 MB for a piece's probabilities (never the logits), fp32 sums of the
+ * gradient and 8 bytes per token and 64 vocabulary entries of a piece.  0 on a
+ * bad descriptor. */
+size_t fq_head_loss_workspace_size(const fq_head_desc* d, int32_t with_grad);
+/* h: device bf16 [tokens, hidden]; w: device bf16 [vocab, hidden]; both 16-B
+ *   aligned.
+ * teacher_topk_logits / teacher_topk_ids: device fp32 / int32 [tokens, topk];
+ *   NULL with topk == 0.
+ * labels: nullable device int32 [tokens] (needed with topk == 0).
+ * loss: device fp32 [1].  row_loss: nullable device fp32 [tokens].
+ * grad: nullable device bf16 [tokens, hidden] (may be h).
+ * With tokens == 0 loss receives 0 and the other pointers may be NULL.
+ * Errors: FQ_E_INVALID (nulls, topk outside 0 .. min(64, vocab), weights not
+ * finite, neither labels nor teacher), FQ_E_SHAPE, FQ_E_UNSUPPORTED (hidden >
+ * 16384), FQ_E_ALIGN, FQ_E_WORKSPACE, FQ_E_HIP. */
+int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const float* teacher_topk_logits,
+                 const int32_t* teacher_topk_ids, const int32_t* labels, float* loss, float* row_loss,
+                 void* grad, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- diagnostics ----------------------------------------------------------- */
 const char* fq_status_string(int32_t status);   /* static string                */
 const char* fq_last_hip_error(void);            /* thread-local; after FQ_E_HIP */

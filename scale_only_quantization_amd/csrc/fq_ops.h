@@ -42,4 +42,38 @@ int norm_bwd_parts(int64_t rows, int64_t cols);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t st);
 constexpr int NORM_MAX_COLS = 65536;
 
+// ------------------------------------------------- the output layer's loss ---
+struct HeadPlan {
+    int pieces, vc;        // pieces of the vocabulary, entries per piece (a multiple of 256)
+    int splits, ksplit;    // splits of a piece in the gradient's product, entries per split (of 64)
+};
+HeadPlan head_plan(int64_t T, int64_t H, int64_t V);
+struct HeadArgs {
+    int64_t T;
+    int H;                 // a multiple of 64
+    int64_t V;
+    int k;                 // the teacher's ids per token, <= 64
+    float lm_w, dist_w;
+    const uint16_t* h;     // [T, H]
+    const uint16_t* w;     // [V, H]
+    const float* top_v;    // [T, k]
+    const int32_t* top_i;
+    const int32_t* labels; // nullable [T]
+    float* row_loss;       // [T]
+    uint16_t* grad;        // nullable [T, H]
+    // workspace
+    float* inv_n;          // [1]
+    float* frame;          // [T]
+    float* sum;            // [T]
+    float* step;           // [T] power of two the last piece moved the frame by
+    float* zs;             // [T, k + 1] logits of the teacher's ids and the label
+    float2* stats;         // [vc / 64, T] sum and frame of each strip
+    uint16_t* p;           // with grad: [T, vc]
+    float* g;              // with grad: [splits, T, H]
+    // filled per launch
+    int64_t c0;
+    int vc, splits, ksplit, first;
+};
+hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t st);
+
 }  // namespace fq

@@ -82,4 +82,92 @@ int fq_rms_norm_bwd(int64_t rows, int64_t cols, const void* s, const void* gamma
     return FQ_OK;
 }
 
+// ---------------------------------------------------- the output layer's loss --
+namespace {
+
+struct HeadLayout {
+    size_t inv_n, frame, sum, step, zs, rows, stats, p, g, total;
+};
+
+HeadLayout head_layout(const fq_head_desc* d, const HeadPlan& pl, bool grad) {
+    HeadLayout y{};
+    const size_t T = (size_t)d->tokens;
+    size_t c = 0;
+    auto place = [&](size_t& at, size_t bytes) {
+        at = c;
+        c = round_up(c + bytes, 256);
+    };
+    place(y.inv_n, 4);
+    place(y.frame, T * 4);
+    place(y.sum, T * 4);
+    place(y.step, T * 4);
+    place(y.zs, T * (size_t)(d->topk + 1) * 4);
+    place(y.rows, T * 4);
+    place(y.stats, (size_t)(pl.vc / 64) * T * 8);
+    place(y.p, grad ? T * (size_t)pl.vc * 2 : 0);
+    place(y.g, grad ? (size_t)pl.splits * T * (size_t)d->hidden * 4 : 0);
+    y.total = c;
+    return y;
+}
+
+int check_head(const fq_head_desc* d) {
+    if (!d || !std::isfinite(d->lm_weight) || !std::isfinite(d->distill_weight)) return FQ_E_INVALID;
+    if (d->topk < 0 || d->topk > 64 || d->topk > d->vocab) return FQ_E_INVALID;
+    if (d->tokens < 0 || d->tokens >= (int64_t)1 << 24 || d->hidden < 64 || d->hidden % 64 || d->vocab < 1 ||
+        d->vocab >= (int64_t)1 << 31)
+        return FQ_E_SHAPE;
+    return d->hidden > 16384 ? FQ_E_UNSUPPORTED : FQ_OK;
+}
+
+}  // namespace
+
+size_t fq_head_loss_workspace_size(const fq_head_desc* d, int32_t with_grad) {
+    if (check_head(d) != FQ_OK) return 0;
+    return head_layout(d, head_plan(d->tokens, d->hidden, d->vocab), with_grad != 0).total;
+}
+
+int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const float* teacher_topk_logits,
+                 const int32_t* teacher_topk_ids, const int32_t* labels, float* loss, float* row_loss, void* grad,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+    const int s = check_head(d);
+    if (s != FQ_OK) return s;
+    if (!loss || (d->tokens > 0 && (!h || !w))) return FQ_E_INVALID;
+    if (d->tokens > 0 && d->topk == 0 && !labels) return FQ_E_INVALID;        // no loss at all
+    if (d->topk > 0 ? (d->tokens > 0 && (!teacher_topk_logits || !teacher_topk_ids))
+                    : (teacher_topk_logits || teacher_topk_ids))
+        return FQ_E_INVALID;
+    if (!aligned(h, 16) || !aligned(w, 16) || !aligned(teacher_topk_logits, 4) || !aligned(teacher_topk_ids, 4) ||
+        !aligned(labels, 4) || !aligned(loss, 4) || !aligned(row_loss, 4) || !aligned(grad, 16) ||
+        !aligned(workspace, 256))
+        return FQ_E_ALIGN;
+    const HeadPlan pl = head_plan(d->tokens, d->hidden, d->vocab);
+    const HeadLayout y = head_layout(d, pl, grad != nullptr);
+    if (!workspace || workspace_bytes < y.total) return FQ_E_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    HeadArgs a{};
+    a.T = d->tokens;
+    a.H = (int)d->hidden;
+    a.V = d->vocab;
+    a.k = d->topk;
+    a.lm_w = d->lm_weight;
+    a.dist_w = d->distill_weight;
+    a.h = static_cast<const uint16_t*>(h);
+    a.w = static_cast<const uint16_t*>(w);
+    a.top_v = teacher_topk_logits;
+    a.top_i = teacher_topk_ids;
+    a.labels = labels;
+    a.row_loss = row_loss ? row_loss : reinterpret_cast<float*>(ws + y.rows);
+    a.grad = static_cast<uint16_t*>(grad);
+    a.inv_n = reinterpret_cast<float*>(ws + y.inv_n);
+    a.frame = reinterpret_cast<float*>(ws + y.frame);
+    a.sum = reinterpret_cast<float*>(ws + y.sum);
+    a.step = reinterpret_cast<float*>(ws + y.step);
+    a.zs = reinterpret_cast<float*>(ws + y.zs);
+    a.stats = reinterpret_cast<float2*>(ws + y.stats);
+    a.p = grad ? reinterpret_cast<uint16_t*>(ws + y.p) : nullptr;
+    a.g = grad ? reinterpret_cast<float*>(ws + y.g) : nullptr;
+    FQ_TRY(launch_head(a, pl, loss, static_cast<hipStream_t>(stream)));
+    return FQ_OK;
+}
+
 }  // extern "C"

@@ -68,6 +68,11 @@ class AdamWHparams(Structure):
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("max_grad_norm", ctypes.c_float)]
 
 
+class HeadDesc(Structure):
+    _fields_ = [("tokens", c_int64), ("hidden", c_int64), ("vocab", c_int64), ("topk", c_int32),
+                ("lm_weight", ctypes.c_float), ("distill_weight", ctypes.c_float)]
+
+
 class DistillDesc(Structure):
     _fields_ = [("type", c_int32), ("topk", c_int32), ("lm_weight", ctypes.c_float),
                 ("distill_weight", ctypes.c_float)]
@@ -126,6 +131,9 @@ def _load():
         "fq_rms_norm_bwd_workspace_size": (c_size_t, [c_int64, c_int64]),
         "fq_rms_norm_bwd": (c_int32, [c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                       c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "fq_head_loss_workspace_size": (c_size_t, [POINTER(HeadDesc), c_int32]),
+        "fq_head_loss": (c_int32, [POINTER(HeadDesc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -141,7 +149,8 @@ EXPORTS = ("fq_abi_version", "fq_status_string", "fq_last_hip_error", "fq_preset
            "fq_grouped_expert_fwd", "fq_grouped_expert_bwd", "fq_adamw_defaults",
            "fq_scale_adamw_workspace_size", "fq_scale_adamw", "fq_scale_adamw_noalloc",
            "fq_distill_workspace_size", "fq_distill_loss", "fq_rms_norm_fwd",
-           "fq_rms_norm_bwd_workspace_size", "fq_rms_norm_bwd")
+           "fq_rms_norm_bwd_workspace_size", "fq_rms_norm_bwd", "fq_head_loss_workspace_size",
+           "fq_head_loss")
 
 
 def lib():
@@ -408,3 +417,30 @@ def rms_norm_bwd(s, gamma, rstd, dy, dx, dsum=None, dgamma=None, workspace=None,
           _expect(w, "gamma", gamma, bf, (cols,), dev), _expect(w, "rstd", rstd, f32, (rows,), dev),
           _expect(w, "dy", dy, bf, full, dev), _expect(w, "dsum", dsum, bf, full, dev),
           _expect(w, "dx", dx, bf, full, dev), _expect(w, "dgamma", dgamma, f32, (cols,), dev), ws, nb)
+
+
+def head_desc(tokens: int, hidden: int, vocab: int, topk: int = 0, lm_weight: float = 1.0,
+              distill_weight: float = 1.0) -> HeadDesc:
+    return HeadDesc(tokens, hidden, vocab, topk, lm_weight, distill_weight)
+
+
+def head_loss_workspace_size(d: HeadDesc, grad: bool = True) -> int:
+    return _lib.fq_head_loss_workspace_size(ctypes.byref(d), 1 if grad else 0)
+
+
+def head_loss(d: HeadDesc, h, w, loss, top_v=None, top_i=None, labels=None, row_loss=None, grad=None, workspace=None,
+              stream=None):
+    """Cross entropy and top-k distillation of bf16 hidden states h [tokens, hidden] under the frozen output
+    weight w [vocab, hidden] (fq_head_loss): the mean loss into loss[0], each token's into row_loss, d loss / d h
+    into grad.  Logits are never stored."""
+    import torch
+    n = "head_loss"
+    dev = _device_of(n, h)
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    T, k = d.tokens, d.topk
+    ws, nb = _scratch(n, workspace, dev)
+    _call(n, _lib.fq_head_loss, dev, stream, ctypes.byref(d), _expect(n, "h", h, bf, (T, d.hidden), dev),
+          _expect(n, "w", w, bf, (d.vocab, d.hidden), dev), _expect(n, "top_v", top_v, f32, (T, k), dev),
+          _expect(n, "top_i", top_i, i32, (T, k), dev), _expect(n, "labels", labels, i32, (T,), dev),
+          _expect(n, "loss", loss, f32, (1,), dev), _expect(n, "row_loss", row_loss, f32, (T,), dev),
+          _expect(n, "grad", grad, bf, (T, d.hidden), dev), ws, nb)

@@ -90,3 +90,38 @@ def test_expect_checks_type_shape_layout_and_device():
                               (t, torch.bfloat16, (4, 6), torch.device("cuda", 0))):
         with pytest.raises(ValueError, match="contiguous"):
             F._expect("f", "t", bad, dt, shape, d)
+
+
+def _hl(T=4, H=64, V=100, k=0, lm=1.0, dist=1.0, h=FAKE, w=FAKE, tv=None, ti=None, lab=FAKE, loss=FAKE, rows=None,
+        grad=None, ws=FAKE, wsb=1 << 40, d=True):
+    desc = F.head_desc(T, H, V, k, lm, dist)
+    return F.lib().fq_head_loss(ctypes.byref(desc) if d else None, h, w, tv, ti, lab, loss, rows, grad, ws, wsb, None)
+
+
+def test_head_loss_refusals():
+    assert _hl(d=False) == F.FQ_E_INVALID
+    for kw in (dict(T=-1), dict(T=1 << 24), dict(H=0), dict(H=96), dict(H=32), dict(V=0), dict(V=1 << 31)):
+        assert _hl(**kw) == F.FQ_E_SHAPE, kw
+        assert F.head_loss_workspace_size(F.head_desc(kw.get("T", 4), kw.get("H", 64), kw.get("V", 100))) == 0
+    assert _hl(H=16448) == F.FQ_E_UNSUPPORTED
+    for kw in (dict(k=-1), dict(k=65), dict(k=9, V=8), dict(lm=float("nan")), dict(dist=float("inf")), dict(h=None),
+               dict(w=None), dict(loss=None), dict(lab=None), dict(k=4), dict(k=4, tv=FAKE), dict(k=4, ti=FAKE),
+               dict(tv=FAKE), dict(ti=FAKE)):
+        assert _hl(**kw) == F.FQ_E_INVALID, kw
+    for kw in (dict(h=MIS), dict(w=MIS), dict(lab=MIS), dict(loss=MIS), dict(rows=MIS), dict(grad=MIS),
+               dict(ws=FAKE + 128), dict(k=4, tv=MIS, ti=FAKE), dict(k=4, tv=FAKE, ti=MIS)):
+        assert _hl(**kw) == F.FQ_E_ALIGN, kw
+    need = F.head_loss_workspace_size(F.head_desc(4, 64, 100))
+    alone = F.head_loss_workspace_size(F.head_desc(4, 64, 100), grad=False)
+    assert 0 < alone < need
+    assert _hl(grad=FAKE, wsb=need - 1) == F.FQ_E_WORKSPACE
+    assert _hl(wsb=alone - 1) == F.FQ_E_WORKSPACE
+    assert _hl(ws=None) == F.FQ_E_WORKSPACE
+
+
+def test_head_loss_workspace_stays_small():
+    # at the largest batch the workspace holds no [tokens, vocab] tensor: 15360 of 151936 entries at a time
+    d = F.head_desc(16384, 2048, 151936, 64)
+    assert F.head_loss_workspace_size(d) < 16384 * 151936 * 2 / 6
+    # and a long vocabulary over few tokens stays within a buffer's reach
+    assert F.head_loss_workspace_size(F.head_desc(1, 16384, 2 ** 31 - 1)) < 1 << 30
