@@ -478,6 +478,61 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
                  const int32_t* teacher_topk_ids, const int32_t* labels, float* loss, float* row_loss,
                  void* grad, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- products of packed 4-bit weights --------------------------------------------
+ * For a served model: the weights as fq_tensor's packed codes with their
+ * scales, a few rows of activations.
+ *     y[m, n] = bf16(sum_k x[m, k] W[n, k]),
+ *     W = q s (INT4: scale s per row or per group of columns)
+ *     W = q d t (NVFP4: d the block code's E4M3 value, t the tensor scale)
+ * with exact products and fp32 sums; W is not rounded to bf16 first, as the
+ * fake-quantised weights of training are.  Deterministic, and a row's result
+ * does not depend on the other rows.
+ *
+ *   q            host; INT with a 4-bit range and scales per row or per group
+ *                (32 .. 512), or NVFP4; the source does not matter.
+ *   codes        device u8 [batch, rows, cols/2], 16-B aligned; cols % 32 == 0,
+ *                cols <= 65536.
+ *   block_codes  device u8 [batch, rows, cols/16], 2-B aligned, NVFP4 only, else NULL.
+ *   scale        device fp32 [batch, rows] or [batch, rows, cols/group], INT only.
+ *   tensor_scale device fp32 [batch], NVFP4 only.
+ *   m            rows of x, 0 .. 1024.
+ *   which        device int32 [m]: the matrix of each row of x; needed if batch > 1,
+ *                else nullable.  A row whose entry is outside [0, batch) gets zeros.
+ *   x            device bf16 [m, cols], 16-B aligned; y: device bf16 [m, rows].
+ * Errors: FQ_E_INVALID, FQ_E_SHAPE, FQ_E_UNSUPPORTED (other formats, m > 1024),
+ * FQ_E_ALIGN, FQ_E_HIP. */
+int fq_packed_matvec(const fq_qdesc* q, int64_t batch, int64_t rows, int64_t cols, const uint8_t* codes,
+                     const uint8_t* block_codes, const float* scale, const float* tensor_scale, int64_t m,
+                     const int32_t* which, const void* x, void* y, void* stream);
+
+/* The expert layer of fq_grouped_expert_fwd for a few tokens, from packed
+ * 4-bit weights: the single-token form of a served model.  Of the descriptor,
+ * w1 and w2 are formats of fq_packed_matvec, a1 and a2 are FQ_NONE, NVFP4 with
+ * dynamic blocks, or INT/FP8 with one scale per expert (the presets nvfp4,
+ * nvfp4a16, w4a16 and w4afp8), and T * topk <= 1024.
+ *     x^ = fq_a1,e(x[t]),  z1 = x^ W1[e]^T (fp32),  h^ = fq_a2,e(bf16(silu(g) u))
+ *     y[t] = bf16(sum_j topk_w[t, j] h^ W2[e]^T)
+ * as in training, except that W, z1 and the experts' outputs are not rounded
+ * to bf16 on the way. */
+typedef struct {
+    const uint8_t* w1_codes;        /* device u8 [E, 2I, H/2]                            */
+    const uint8_t* w1_block_codes;  /* device u8 [E, 2I, H/16], NVFP4, else NULL         */
+    const float* s_w1;              /* device fp32, INT: [E, 2I] or [E, 2I, H/group]     */
+    const float* t_w1;              /* device fp32 [E], NVFP4                            */
+    const uint8_t* w2_codes;        /* [E, H, I/2]                                       */
+    const uint8_t* w2_block_codes;
+    const float* s_w2;
+    const float* t_w2;
+    const float* s_a1;              /* device fp32 [E], with an input quantiser, else NULL */
+    const float* s_a2;
+} fq_packed_experts;
+/* Bytes of device workspace (256-B aligned), 0 on a descriptor that is not supported. */
+size_t fq_packed_expert_workspace_size(const fq_layer_desc* L);
+/* x device bf16 [T, H]; topk_ids device int32 [T, topk]; topk_w device fp32
+ * [T, topk]; y device bf16 [T, H], not x.  Errors as fq_grouped_expert_fwd. */
+int fq_packed_expert_fwd(const fq_layer_desc* L, const fq_packed_experts* P, const void* x, const int32_t* topk_ids,
+                         const float* topk_w, void* y, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- diagnostics ----------------------------------------------------------- */
 const char* fq_status_string(int32_t status);   /* static string                */
 const char* fq_last_hip_error(void);            /* thread-local; after FQ_E_HIP */

@@ -76,4 +76,42 @@ struct HeadArgs {
 };
 hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t st);
 
+// ------------------------------------------------- packed 4-bit weights ---
+constexpr int PACKED_MAX_ROWS = 1024;
+struct PackedW {           // a stack of matrices as fq_tensor's codes
+    const uint8_t* codes;  // two per byte, rows of K/2
+    const uint8_t* bcodes; // NVFP4: E4M3 bytes per 16 columns, else null
+    const float* scale;    // INT: spr per row
+    const float* tscale;   // NVFP4: per matrix
+    int K;                 // a multiple of 32
+    int group;             // INT: columns per scale (K where one per row)
+    int spr;               // INT: scales per row
+};
+struct MatvecArgs {
+    PackedW w;
+    int64_t N;             // rows of a matrix
+    int E, M;
+    const int32_t* which;  // nullable [M]: the matrix of each row of x
+    const uint16_t* x;     // [M, K]
+    uint16_t* y;           // [M, N]
+};
+hipError_t launch_matvec(const MatvecArgs& a, hipStream_t st);
+
+struct PackedExpertArgs {
+    PackedW w1, w2;        // [E, 2I, H], [E, H, I]
+    ActQ a1, a2;
+    int E, H, I, k, R;     // R = tokens * k <= PACKED_MAX_ROWS
+    const uint16_t* x;     // [T, H]
+    const int32_t* ids;    // [R]
+    const float* tw;       // [R]
+    uint16_t* y;           // [T, H]
+    uint16_t* xhat;        // with an input quantiser: workspace [R, H], else null
+    uint16_t* h;           // workspace [R, I]
+    float* yr;             // workspace [R, H]
+    int32_t* order;        // workspace [R]: rows by expert; null where every row is its own group
+    int32_t* start;        // [R]
+    int32_t* count;        // [R]
+};
+hipError_t launch_packed_expert(const PackedExpertArgs& a, hipStream_t st);
+
 }  // namespace fq

@@ -170,4 +170,139 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
     return FQ_OK;
 }
 
+// ------------------------------------------------------ packed 4-bit weights --
+namespace {
+
+// The packed form of `batch` matrices [rows, cols] under quantiser d.
+int check_packed(const fq_qdesc* d, int64_t cols, const uint8_t* codes, const uint8_t* block_codes, const float* scale,
+                 const float* tensor_scale, PackedW* w) {
+    QParams q;
+    const int s = check_qdesc(d, &q);
+    if (s != FQ_OK) return s;
+    if (!four_bit(q)) return FQ_E_UNSUPPORTED;
+    if (q.kind == FQ_INT && (q.qmin < -8.0f || q.qmax > 7.0f || q.gran == FQ_PER_TENSOR ||
+                             (q.gran == FQ_PER_GROUP && q.group < 32)))
+        return FQ_E_UNSUPPORTED;
+    if (cols < 32 || cols % 32 || (q.gran == FQ_PER_GROUP && cols % q.group)) return FQ_E_SHAPE;
+    if (cols > 65536) return FQ_E_UNSUPPORTED;
+    if (!codes) return FQ_E_INVALID;
+    if (q.kind == FQ_NVFP4 ? (!block_codes || !tensor_scale || scale) : (!scale || block_codes || tensor_scale))
+        return FQ_E_INVALID;
+    if (!aligned(codes, 16) || !aligned(block_codes, 2) || !aligned(scale, 4) || !aligned(tensor_scale, 4))
+        return FQ_E_ALIGN;
+    w->codes = codes;
+    w->bcodes = block_codes;
+    w->scale = scale;
+    w->tscale = tensor_scale;
+    w->K = (int)cols;
+    w->group = q.gran == FQ_PER_GROUP ? q.group : (int)(cols > 128 ? cols : 128);
+    w->spr = q.gran == FQ_PER_GROUP ? (int)(cols / q.group) : 1;
+    return FQ_OK;
+}
+
+struct PackedLayout {
+    size_t xhat, h, yr, order, start, count, total;
+};
+
+// an input quantiser the packed layer has: none, NVFP4 with dynamic blocks, or one scale per expert
+bool packed_act(const QParams& a) {
+    return a.kind == FQ_NONE || a.kind == FQ_NVFP4 || (a.gran == FQ_PER_TENSOR && a.source != FQ_DYNAMIC);
+}
+
+int check_packed_layer(const fq_layer_desc* L, LayerQ* q) {
+    const int s = check_layer(L, q);
+    if (s != FQ_OK) return s;
+    if (!packed_act(q->a1) || !packed_act(q->a2) || L->T * L->topk > PACKED_MAX_ROWS) return FQ_E_UNSUPPORTED;
+    return FQ_OK;
+}
+
+PackedLayout packed_layout(const fq_layer_desc* L, const LayerQ& q) {
+    PackedLayout y{};
+    const size_t R = (size_t)(L->T * L->topk);
+    size_t c = 0;
+    auto place = [&](size_t& at, size_t bytes) {
+        at = c;
+        c = round_up(c + bytes, 256);
+    };
+    place(y.xhat, q.a1.kind != FQ_NONE ? R * (size_t)L->H * 2 : 0);
+    place(y.h, R * (size_t)L->I * 2);
+    place(y.yr, R * (size_t)L->H * 4);
+    place(y.order, R * 4);
+    place(y.start, R * 4);
+    place(y.count, R * 4);
+    y.total = c;
+    return y;
+}
+
+}  // namespace
+
+int fq_packed_matvec(const fq_qdesc* d, int64_t batch, int64_t rows, int64_t cols, const uint8_t* codes,
+                     const uint8_t* block_codes, const float* scale, const float* tensor_scale, int64_t m,
+                     const int32_t* which, const void* x, void* y, void* stream) {
+    MatvecArgs a{};
+    if (batch < 1 || batch >= (int64_t)1 << 31 || rows < 1 || rows >= (int64_t)1 << 31 || m < 0) return FQ_E_SHAPE;
+    const int s = check_packed(d, cols, codes, block_codes, scale, tensor_scale, &a.w);
+    if (s != FQ_OK) return s;
+    if (m > PACKED_MAX_ROWS) return FQ_E_UNSUPPORTED;
+    if ((batch > 1 && m > 0 && !which) || (m > 0 && (!x || !y))) return FQ_E_INVALID;
+    if (!aligned(x, 16) || !aligned(y, 2) || !aligned(which, 4)) return FQ_E_ALIGN;
+    if (m == 0) return FQ_OK;
+    a.N = rows;
+    a.E = (int)batch;
+    a.M = (int)m;
+    a.which = which;
+    a.x = static_cast<const uint16_t*>(x);
+    a.y = static_cast<uint16_t*>(y);
+    FQ_TRY(launch_matvec(a, static_cast<hipStream_t>(stream)));
+    return FQ_OK;
+}
+
+size_t fq_packed_expert_workspace_size(const fq_layer_desc* L) {
+    LayerQ q;
+    if (check_packed_layer(L, &q) != FQ_OK) return 0;
+    return packed_layout(L, q).total;
+}
+
+int fq_packed_expert_fwd(const fq_layer_desc* L, const fq_packed_experts* P, const void* x, const int32_t* topk_ids,
+                         const float* topk_w, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+    LayerQ q;
+    int s = check_packed_layer(L, &q);
+    if (s != FQ_OK) return s;
+    if (!P) return FQ_E_INVALID;
+    PackedExpertArgs a{};
+    if ((s = check_packed(&L->w1, L->H, P->w1_codes, P->w1_block_codes, P->s_w1, P->t_w1, &a.w1)) != FQ_OK) return s;
+    if ((s = check_packed(&L->w2, L->I, P->w2_codes, P->w2_block_codes, P->s_w2, P->t_w2, &a.w2)) != FQ_OK) return s;
+    if ((q.a1.kind != FQ_NONE) != (P->s_a1 != nullptr) || (q.a2.kind != FQ_NONE) != (P->s_a2 != nullptr))
+        return FQ_E_INVALID;
+    if (L->T > 0 && (!x || !topk_ids || !topk_w || !y)) return FQ_E_INVALID;
+    if (!aligned(P->s_a1, 4) || !aligned(P->s_a2, 4) || !aligned(x, 16) || !aligned(topk_ids, 4) ||
+        !aligned(topk_w, 4) || !aligned(y, 16) || !aligned(workspace, 256))
+        return FQ_E_ALIGN;
+    const PackedLayout lay = packed_layout(L, q);
+    if (L->T > 0 && (!workspace || workspace_bytes < lay.total)) return FQ_E_WORKSPACE;
+    if (L->T == 0) return FQ_OK;
+    char* ws = static_cast<char*>(workspace);
+    a.a1 = ActQ{q.a1, P->s_a1};
+    a.a2 = ActQ{q.a2, P->s_a2};
+    a.E = (int)L->E;
+    a.H = (int)L->H;
+    a.I = (int)L->I;
+    a.k = (int)L->topk;
+    a.R = (int)(L->T * L->topk);
+    a.x = static_cast<const uint16_t*>(x);
+    a.ids = topk_ids;
+    a.tw = topk_w;
+    a.y = static_cast<uint16_t*>(y);
+    a.xhat = q.a1.kind != FQ_NONE ? reinterpret_cast<uint16_t*>(ws + lay.xhat) : nullptr;
+    a.h = reinterpret_cast<uint16_t*>(ws + lay.h);
+    a.yr = reinterpret_cast<float*>(ws + lay.yr);
+    if (L->T > 1) {
+        a.order = reinterpret_cast<int32_t*>(ws + lay.order);
+        a.start = reinterpret_cast<int32_t*>(ws + lay.start);
+        a.count = reinterpret_cast<int32_t*>(ws + lay.count);
+    }
+    FQ_TRY(launch_packed_expert(a, static_cast<hipStream_t>(stream)));
+    return FQ_OK;
+}
+
 }  // extern "C"

@@ -68,6 +68,11 @@ class AdamWHparams(Structure):
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("max_grad_norm", ctypes.c_float)]
 
 
+class PackedExperts(Structure):
+    _fields_ = [(n, c_void_p) for n in ("w1_codes", "w1_block_codes", "s_w1", "t_w1", "w2_codes", "w2_block_codes",
+                                        "s_w2", "t_w2", "s_a1", "s_a2")]
+
+
 class HeadDesc(Structure):
     _fields_ = [("tokens", c_int64), ("hidden", c_int64), ("vocab", c_int64), ("topk", c_int32),
                 ("lm_weight", ctypes.c_float), ("distill_weight", ctypes.c_float)]
@@ -134,6 +139,11 @@ def _load():
         "fq_head_loss_workspace_size": (c_size_t, [POINTER(HeadDesc), c_int32]),
         "fq_head_loss": (c_int32, [POINTER(HeadDesc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                    c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "fq_packed_matvec": (c_int32, [Q, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
+                                       c_void_p, c_void_p, c_void_p, c_void_p]),
+        "fq_packed_expert_workspace_size": (c_size_t, [L]),
+        "fq_packed_expert_fwd": (c_int32, [L, POINTER(PackedExperts), c_void_p, c_void_p, c_void_p, c_void_p,
+                                           c_void_p, c_size_t, c_void_p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -150,7 +160,7 @@ EXPORTS = ("fq_abi_version", "fq_status_string", "fq_last_hip_error", "fq_preset
            "fq_scale_adamw_workspace_size", "fq_scale_adamw", "fq_scale_adamw_noalloc",
            "fq_distill_workspace_size", "fq_distill_loss", "fq_rms_norm_fwd",
            "fq_rms_norm_bwd_workspace_size", "fq_rms_norm_bwd", "fq_head_loss_workspace_size",
-           "fq_head_loss")
+           "fq_head_loss", "fq_packed_matvec", "fq_packed_expert_workspace_size", "fq_packed_expert_fwd")
 
 
 def lib():
@@ -444,3 +454,67 @@ def head_loss(d: HeadDesc, h, w, loss, top_v=None, top_i=None, labels=None, row_
           _expect(n, "top_i", top_i, i32, (T, k), dev), _expect(n, "labels", labels, i32, (T,), dev),
           _expect(n, "loss", loss, f32, (1,), dev), _expect(n, "row_loss", row_loss, f32, (T,), dev),
           _expect(n, "grad", grad, bf, (T, d.hidden), dev), ws, nb)
+
+
+def _scale_shape(q: QDesc, E, N, K):
+    return (E, N) if q.gran == FQ_PER_ROW else (E, N, K // max(q.group, 1))
+
+
+def packed_matvec(q: QDesc, codes, x, y, scale=None, block_codes=None, tensor_scale=None, which=None, stream=None):
+    """y [m, N] = x [m, K] times packed 4-bit weights (fq_packed_matvec): codes uint8 [E, N, K/2] as fq_tensor
+    gives them, with scale (INT) or block_codes and tensor_scale (NVFP4); which [m] names each row's matrix."""
+    import torch
+    n = "packed_matvec"
+    dev = _device_of(n, x)
+    if codes.dim() != 3 or x.dim() != 2:
+        raise ValueError(f"{n}: codes must be [batch, rows, cols/2] and x [m, cols], got {list(codes.shape)} and "
+                         f"{list(x.shape)}")
+    E, N, K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
+    M = x.shape[0]
+    u8, f32, bf = torch.uint8, torch.float32, torch.bfloat16
+    _call(n, _lib.fq_packed_matvec, dev, stream, ctypes.byref(q), E, N, K,
+          _expect(n, "codes", codes, u8, (E, N, K // 2), dev),
+          _expect(n, "block_codes", block_codes, u8, (E, N, K // 16), dev),
+          _expect(n, "scale", scale, f32, _scale_shape(q, E, N, K), dev),
+          _expect(n, "tensor_scale", tensor_scale, f32, (E,), dev), M,
+          _expect(n, "which", which, torch.int32, (M,), dev), _expect(n, "x", x, bf, (M, K), dev),
+          _expect(n, "y", y, bf, (M, N), dev))
+
+
+def packed_experts(w1: dict, w2: dict, s_a1=None, s_a2=None) -> PackedExperts:
+    """The packed weights of an expert layer: w1 and w2 hold "codes" and "scale" (INT) or "block_codes" and
+    "tensor_scale" (NVFP4), s_a1 / s_a2 the activation quantisers' scales [E].  The result keeps the tensors."""
+    t = [w.get(n) for w in (w1, w2) for n in ("codes", "block_codes", "scale", "tensor_scale")] + [s_a1, s_a2]
+    P = PackedExperts(*[None if x is None else x.data_ptr() for x in t])
+    P.tensors = t
+    P.checked = None
+    return P
+
+
+def packed_expert_workspace_size(L: LayerDesc) -> int:
+    return _lib.fq_packed_expert_workspace_size(ctypes.byref(L))
+
+
+def packed_expert_fwd(L: LayerDesc, P: PackedExperts, x, topk_ids, topk_w, y, workspace, stream=None):
+    """The expert layer on packed weights for the T tokens of L (fq_packed_expert_fwd)."""
+    import torch
+    n = "packed_expert_fwd"
+    dev = _device_of(n, x)
+    f32, bf, u8 = torch.float32, torch.bfloat16, torch.uint8
+    T, H, k = L.T, L.H, L.topk
+    sizes = (L.E, H, L.I, dev)
+    if P.checked != sizes:                               # the weights' shapes, once per layer
+        E, I = L.E, L.I
+        for i, (q, N, K) in enumerate(((L.w1, 2 * I, H), (L.w2, H, I))):
+            c, b, s, t = P.tensors[4 * i:4 * i + 4]
+            _expect(n, "codes", c, u8, (E, N, K // 2), dev)
+            _expect(n, "block_codes", b, u8, (E, N, K // 16), dev)
+            _expect(n, "scale", s, f32, _scale_shape(q, E, N, K), dev)
+            _expect(n, "tensor_scale", t, f32, (E,), dev)
+        for s in P.tensors[8:]:
+            _expect(n, "activation scale", s, f32, (E,), dev)
+        P.checked = sizes
+    ws, nb = _scratch(n, workspace, dev)
+    _call(n, _lib.fq_packed_expert_fwd, dev, stream, ctypes.byref(L), ctypes.byref(P),
+          _expect(n, "x", x, bf, (T, H), dev), _expect(n, "topk_ids", topk_ids, torch.int32, (T, k), dev),
+          _expect(n, "topk_w", topk_w, f32, (T, k), dev), _expect(n, "y", y, bf, (T, H), dev), ws, nb)

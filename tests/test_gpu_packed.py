@@ -1,0 +1,245 @@
+"""GPU parity of the products of packed 4-bit weights (fq_packed_matvec) and of
+the expert layer on them (fq_packed_expert_fwd) with the oracle."""
+import numpy as np
+import pytest
+
+from oracle import packed as OPK
+from oracle import presets as OP
+from oracle.numerics import bf16_rne
+from tests.fq_testutil import check_gemm, from_dev, to_dev, to_dev_bf16, torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _F():
+    from scale_only_quantization_amd import fqlib
+    return fqlib
+
+
+def _weights(seed, fmt, E, N, K):
+    """Random codes of every value and positive scales; (descriptor, numpy arrays by name, W [E, N, K] float64)."""
+    F = _F()
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 256, (E, N, K // 2)).astype(np.uint8)
+    if fmt == "nvfp4":
+        d = dict(block_codes=rng.integers(0, 127, (E, N, K // 16)).astype(np.uint8),
+                 tensor_scale=(rng.random(E) * 1e-3 + 1e-4).astype(np.float32))
+        q = F.qdesc(F.FQ_NVFP4, F.FQ_PER_GROUP, 16, F.FQ_LEARNABLE)
+    elif fmt == "row":
+        d = dict(scale=(rng.random((E, N)) * 0.01 + 1e-3).astype(np.float32))
+        q = F.qdesc(F.FQ_INT, F.FQ_PER_ROW, 0, F.FQ_LEARNABLE, -8, 7)
+    else:
+        g = int(fmt[1:])
+        d = dict(scale=(rng.random((E, N, K // g)) * 0.01 + 1e-3).astype(np.float32))
+        q = F.qdesc(F.FQ_INT, F.FQ_PER_GROUP, g, F.FQ_STATIC, -8, 7)
+    return q, dict(codes=codes, **d), OPK.dequant(codes, **d)
+
+
+def _matvec(q, w, x, which=None, N=None):
+    F, T = _F(), torch()
+    y = T.full((x.shape[0] + 1, N), 7.0, dtype=T.bfloat16, device="cuda")   # one row more than is written
+    dev = {n: to_dev(v) for n, v in w.items()}
+    F.packed_matvec(q, dev.pop("codes"), to_dev_bf16(x), y[:-1], which=None if which is None else to_dev(which), **dev)
+    T.cuda.synchronize()
+    assert bool((y[-1] == 7).all()), "written past the last row"
+    return from_dev(y[:-1])
+
+
+def _check(got, ref, x, W, fmt, what):
+    # bf16 of an fp32 sum: exact products, K/32 products' sums and 8 steps more
+    # per term; INT4 codes enter as 136 + q, and the 136 comes off again: terms
+    # up to 272 times the scale
+    K = W.shape[-1]
+    if fmt == "nvfp4":
+        terms = np.abs(x.astype(np.float64)) @ np.abs(W).T
+    else:
+        s = np.abs(W).max(-1) / 7.0 + 1e-9
+        # the scale of each group is at least its largest |code| over 8: bounded by the row's largest
+        terms = np.abs(x.astype(np.float64)).sum(-1, keepdims=True) * (np.maximum(s, np.abs(W).max(-1)) * 280)[None]
+    tol = 2.0 ** -8 * np.abs(ref) + (K / 32 + 8) * 2.0 ** -24 * terms + 1e-30
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size}, worst {(np.abs(got - ref) / tol).max():.2f}"
+
+
+FMTS = ["nvfp4", "row", "g32", "g64", "g128", "g512"]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("N,K,M", [(1, 32, 1), (16, 128, 1), (40, 96, 3), (33, 2048, 16), (257, 544, 17), (129, 1024, 33),
+                                   (65, 8192, 13), (48, 256, 64), (20, 512, 65), (17, 128, 200)])
+def test_matvec(fmt, N, K, M):
+    g = int(fmt[1:]) if fmt[0] == "g" else 32
+    K = -(-K // g) * g                                   # a whole number of groups
+    q, w, W = _weights(N + K + M, fmt, 1, N, K)
+    rng = np.random.default_rng(M)
+    x = bf16_rne((rng.standard_normal((M, K)) + 0.3).astype(np.float32))
+    got = _matvec(q, w, x, N=N)
+    _check(got, x.astype(np.float64) @ W[0].T, x, W[0], fmt, f"{fmt} {N}x{K} m={M}")
+    # a row alone gives the same bits
+    np.testing.assert_array_equal(_matvec(q, w, x[M // 2:M // 2 + 1], N=N)[0], got[M // 2])
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "g128", "g32"])
+@pytest.mark.parametrize("M", [1, 5, 70])
+def test_matvec_by_matrix(fmt, M):
+    E, N, K = 5, 50, 256
+    q, w, W = _weights(7, fmt, E, N, K)
+    rng = np.random.default_rng(M)
+    x = bf16_rne(rng.standard_normal((M, K)).astype(np.float32))
+    which = rng.integers(0, E, M).astype(np.int32)
+    if M > 4:
+        which[[1, 3]] = -1, E                            # no such matrix: zeros
+        which[M // 2:] = which[M // 2]                   # more rows of one matrix than a tile holds
+    got = _matvec(q, w, x, which, N)
+    for m in range(M):
+        e = which[m]
+        if e < 0 or e >= E:
+            assert not got[m].any()
+        else:
+            _check(got[m:m + 1], x[m:m + 1].astype(np.float64) @ W[e].T, x[m:m + 1], W[e], fmt, f"row {m}")
+
+
+def test_matvec_of_nothing_and_of_fq_tensors_codes():
+    F, T = _F(), torch()
+    q, w, W = _weights(3, "nvfp4", 1, 16, 64)
+    assert _matvec(q, w, np.zeros((0, 64), np.float32), N=16).shape == (0, 16)
+    # codes as fq_tensor packs them, against its own fake-quantised weights
+    rng = np.random.default_rng(4)
+    Wf = bf16_rne((rng.standard_normal((2, 32, 256)) * 0.02).astype(np.float32))
+    x = bf16_rne(rng.standard_normal((3, 256)).astype(np.float32))
+    which = np.array([1, 0, 1], np.int32)
+    for fmt in ("nvfp4", "w4a16"):
+        q = F.preset(fmt)[0]
+        c = T.empty((2, 32, 128), dtype=T.uint8, device="cuda")
+        kw, out = {}, {}
+        if fmt == "nvfp4":
+            s = to_dev((np.abs(Wf).reshape(2, 32, 16, 16).max(-1) / 6).astype(np.float32))
+            t = to_dev((np.abs(Wf).max((1, 2)) / 2688).astype(np.float32))
+            b = T.empty((2, 32, 16), dtype=T.uint8, device="cuda")
+            kw, out = dict(tensor_scale=t, block_codes=b), dict(block_codes=b, tensor_scale=t)
+        else:
+            s = to_dev((np.abs(Wf).reshape(2, 32, 2, 128).max(-1) / 7).astype(np.float32))
+            out = dict(scale=s)
+        yq = T.empty((2, 32, 256), dtype=T.bfloat16, device="cuda")
+        F.fq_tensor(q, to_dev_bf16(Wf), s, y=yq, codes=c, **kw)
+        y = T.empty((3, 32), dtype=T.bfloat16, device="cuda")
+        F.packed_matvec(q, c, to_dev_bf16(x), y, which=to_dev(which), **out)
+        T.cuda.synchronize()
+        ref = np.stack([from_dev(yq)[which[m]].astype(np.float64) @ x[m] for m in range(3)])
+        check_gemm(from_dev(y), ref, fmt)
+
+
+def _layer(seed, fmt, E, H, I, T, k, ids=None):
+    F = _F()
+    wf = "nvfp4" if fmt.startswith("nvfp4") else "g128"
+    q1, w1, W1 = _weights(seed, wf, E, 2 * I, H)
+    q2, w2, W2 = _weights(seed + 1, wf, E, H, I)
+    # weights' sizes as in a layer: z of order one
+    for w, W, n in ((w1, W1, H), (w2, W2, I)):
+        f = np.float32(1.0 / (np.sqrt(np.mean(W ** 2)) * np.sqrt(n)))
+        w["tensor_scale" if wf == "nvfp4" else "scale"] *= f
+    W1, W2 = (OPK.dequant(**w) for w in (w1, w2))
+    rng = np.random.default_rng(seed + 2)
+    x = bf16_rne(rng.standard_normal((T, H)).astype(np.float32))
+    if ids is None:
+        ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    tw = rng.random((T, k)).astype(np.float32)
+    s1 = s2 = None
+    if fmt in ("nvfp4", "w4afp8"):
+        div = 2688.0 if fmt == "nvfp4" else 448.0
+        s1 = ((4 + rng.random(E)) / div).astype(np.float32)
+        s2 = ((3 + rng.random(E)) / div).astype(np.float32)
+    return dict(L=F.layer_desc(E, H, I, T, k, *F.preset(fmt)), w1=w1, w2=w2, W1=W1, W2=W2, x=x, ids=ids, tw=tw, s1=s1,
+                s2=s2, fmt=fmt)
+
+
+def _run(d, rows=slice(None)):
+    F, T = _F(), torch()
+    x, ids, tw = d["x"][rows], d["ids"][rows], d["tw"][rows]
+    L = F.layer_desc(d["L"].E, d["L"].H, d["L"].I, x.shape[0], ids.shape[1], *F.preset(d["fmt"]))
+    dev = [{n: to_dev(v) for n, v in w.items()} for w in (d["w1"], d["w2"])]
+    P = F.packed_experts(*dev, *(None if s is None else to_dev(s) for s in (d["s1"], d["s2"])))
+    y = T.full((x.shape[0], L.H), 7.0, dtype=T.bfloat16, device="cuda")
+    ws = T.full((F.packed_expert_workspace_size(L),), 255, dtype=T.uint8, device="cuda")
+    F.packed_expert_fwd(L, P, to_dev_bf16(x), to_dev(ids), to_dev(tw), y, ws)
+    T.cuda.synchronize()
+    return from_dev(y)
+
+
+def _check_layer(d, got, what):
+    _, _, a1, a2 = OP.PRESETS[d["fmt"]]
+    ref = OPK.experts(d["W1"], d["W2"], d["x"], d["ids"], d["tw"], a1, d["s1"], a2, d["s2"])
+    check_gemm(got, ref, what)
+    # the output's bf16 rounding is at most 2^-8 of each value; a few elements
+    # of h on the other side of a bf16 (or activation code) border as much again
+    err = np.linalg.norm(got - ref) / np.linalg.norm(ref)
+    assert err <= 2.0 ** -7, f"{what}: {err:.2e}"
+
+
+@pytest.mark.parametrize("fmt", ["w4a16", "nvfp4", "nvfp4a16", "w4afp8"])
+@pytest.mark.parametrize("E,H,I,T,k", [(8, 256, 128, 1, 2), (8, 256, 128, 7, 4), (1, 128, 128, 3, 1),
+                                       (16, 2048, 768, 1, 8), (4, 384, 256, 40, 3)])
+def test_experts(fmt, E, H, I, T, k):
+    d = _layer(E + H + T, fmt, E, H, I, T, k)
+    got = _run(d)
+    _check_layer(d, got, f"{fmt} E={E} H={H} I={I} T={T} k={k}")
+    # a token alone gives the same bits
+    np.testing.assert_array_equal(_run(d, slice(T // 2, T // 2 + 1))[0], got[T // 2])
+
+
+def test_experts_crowded_and_at_the_limit():
+    # every token to the same experts (64 rows each, four tiles), some never hit
+    ids = np.tile(np.array([[5, 2]], np.int32), (64, 1))
+    d = _layer(1, "nvfp4", 8, 256, 128, 64, 2, ids)
+    _check_layer(d, _run(d), "crowded")
+    d = _layer(2, "w4a16", 8, 128, 128, 128, 8)          # 1024 routed rows
+    _check_layer(d, _run(d), "limit")
+    # no tokens
+    F, T = _F(), torch()
+    L = F.layer_desc(8, 128, 128, 0, 8, *F.preset("w4a16"))
+    z = T.empty((0, 128), dtype=T.bfloat16, device="cuda")
+    dev = [{n: to_dev(v) for n, v in w.items()} for w in (d["w1"], d["w2"])]
+    F.packed_expert_fwd(L, F.packed_experts(*dev), z, T.empty((0, 8), dtype=T.int32, device="cuda"),
+                        T.empty((0, 8), device="cuda"), z, None)
+
+
+def test_experts_match_the_training_layer():
+    # the same layer through fq_grouped_expert_fwd, its weights packed by
+    # fq_tensor: W^ there is rounded to bf16, the packed one is not
+    import synth
+    from scale_only_quantization_amd.layer import ExpertLayer, LayerDims
+    F, T = _F(), torch()
+    case = synth.CASES["tiny"]
+    data = synth.make_layer(case, T=24)
+    for fmt in ("nvfp4", "w4a16"):
+        p = synth.layer_params(data, fmt)
+        dl = ExpertLayer(LayerDims(case.E, case.H, case.I, 24, case.k), fmt, data["W1"], data["W2"], data["X"],
+                         data["ids"], data["w"], data["dY"], p)
+        dl.forward()
+        ws = []
+        for n, W in (("1", dl.d["W1"]), ("2", dl.d["W2"])):
+            E, N, K = W.shape
+            c = T.empty((E, N, K // 2), dtype=T.uint8, device="cuda")
+            b = T.empty((E, N, K // 16), dtype=T.uint8, device="cuda") if fmt == "nvfp4" else None
+            F.fq_tensor(dl.q["w" + n], W, dl.d["s_w" + n], dl.d["t_w" + n], codes=c, block_codes=b)
+            ws.append(dict(codes=c, block_codes=b, tensor_scale=dl.d["t_w" + n]) if fmt == "nvfp4"
+                      else dict(codes=c, scale=dl.d["s_w" + n]))
+        P = F.packed_experts(*ws, dl.d["s_a1"], dl.d["s_a2"])
+        y = T.empty_like(dl.y)
+        F.packed_expert_fwd(dl.desc, P, dl.d["X"], dl.d["ids"], dl.d["w"], y,
+                            T.empty(F.packed_expert_workspace_size(dl.desc), dtype=T.uint8, device="cuda"))
+        T.cuda.synchronize()
+        got, ref = from_dev(y).astype(np.float64), from_dev(dl.y).astype(np.float64)
+        if fmt == "w4a16":
+            # the roundings that differ (W^ twice, gate, up, y_r) and the two of
+            # h and y: 8 of 1.6e-3 rms each give 4.5e-3, 4 sigma of that 1.8e-2
+            check_gemm(got, ref, fmt, rel=2e-2)
+        else:
+            # h differs by about 2^-8 of itself before its second quantiser,
+            # whose steps are a quarter to a half of a value: of the codes
+            # 2 * 2^-8 / (1/3), about 2.5 in 100, fall on the other side of a
+            # border and move by up to half of the value, which is
+            # sqrt(0.025) * 0.5 = 0.08 of h^'s norm, and so of y's
+            err = np.linalg.norm(got - ref) / np.linalg.norm(ref)
+            print(f"[packed] nvfp4 against the training layer: {err:.3e}", flush=True)
+            assert err <= 0.08

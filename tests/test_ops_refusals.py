@@ -125,3 +125,70 @@ def test_head_loss_workspace_stays_small():
     assert F.head_loss_workspace_size(d) < 16384 * 151936 * 2 / 6
     # and a long vocabulary over few tokens stays within a buffer's reach
     assert F.head_loss_workspace_size(F.head_desc(1, 16384, 2 ** 31 - 1)) < 1 << 30
+
+
+I4 = F.qdesc(F.FQ_INT, F.FQ_PER_GROUP, 128, F.FQ_LEARNABLE, -8, 7)
+NV = F.qdesc(F.FQ_NVFP4, F.FQ_PER_GROUP, 16, F.FQ_LEARNABLE)
+
+
+def _mv(q=I4, E=1, N=16, K=256, c=FAKE, b=None, s=FAKE, t=None, M=2, which=None, x=FAKE, y=FAKE):
+    return F.lib().fq_packed_matvec(ctypes.byref(q), E, N, K, c, b, s, t, M, which, x, y, None)
+
+
+def test_packed_matvec_refusals():
+    for kw in (dict(E=0), dict(N=0), dict(N=1 << 31), dict(M=-1), dict(K=0), dict(K=48), dict(K=192),
+               dict(q=NV, K=40, s=None, b=FAKE, t=FAKE)):
+        assert _mv(**kw) == F.FQ_E_SHAPE, kw
+    for q in (F.qdesc(F.FQ_INT, F.FQ_PER_ROW, 0, F.FQ_LEARNABLE, -128, 127), F.qdesc(F.FQ_FP8E4M3, F.FQ_PER_ROW),
+              F.qdesc(F.FQ_INT, F.FQ_PER_GROUP, 16, F.FQ_LEARNABLE, -8, 7),
+              F.qdesc(F.FQ_INT, F.FQ_PER_TENSOR, 0, F.FQ_LEARNABLE, -8, 7),
+              F.qdesc(F.FQ_INT, F.FQ_PER_ROW, 0, F.FQ_LEARNABLE, -9, 5), F.qdesc()):
+        assert _mv(q=q) == F.FQ_E_UNSUPPORTED, q
+    assert _mv(K=1 << 17) == F.FQ_E_UNSUPPORTED
+    assert _mv(M=1025) == F.FQ_E_UNSUPPORTED
+    assert _mv(q=F.qdesc(kind=7)) == F.FQ_E_INVALID
+    for kw in (dict(c=None), dict(s=None), dict(b=FAKE), dict(t=FAKE), dict(x=None), dict(y=None), dict(E=2),
+               dict(q=NV, s=None, b=FAKE), dict(q=NV, s=None, t=FAKE), dict(q=NV, b=FAKE, t=FAKE)):
+        assert _mv(**kw) == F.FQ_E_INVALID, kw
+    for kw in (dict(c=FAKE + 8), dict(s=MIS), dict(x=FAKE + 8), dict(y=FAKE + 1), dict(E=2, which=MIS),
+               dict(q=NV, s=None, b=FAKE + 1, t=FAKE), dict(q=NV, s=None, b=FAKE, t=MIS)):
+        assert _mv(**kw) == F.FQ_E_ALIGN, kw
+    assert _mv(M=0, x=None, y=None) == F.FQ_OK
+
+
+def _pe(fmt="w4a16", E=8, H=256, I=128, T=4, k=2, P=None, x=FAKE, ids=FAKE, w=FAKE, y=FAKE, ws=FAKE, wsb=1 << 30,
+        quants=None, **over):
+    L = F.layer_desc(E, H, I, T, k, *(quants or F.preset(fmt)))
+    if P is None:
+        nv = fmt.startswith("nvfp4")
+        act = fmt in ("nvfp4", "w4afp8")
+        d = dict(w1_codes=FAKE, w2_codes=FAKE, s_a1=FAKE if act else None, s_a2=FAKE if act else None)
+        for n in ("1", "2"):
+            d.update({f"w{n}_block_codes": FAKE if nv else None, "t_w" + n: FAKE if nv else None,
+                      "s_w" + n: None if nv else FAKE})
+        d.update(over)
+        P = F.PackedExperts(**d)
+    return F.lib().fq_packed_expert_fwd(ctypes.byref(L), ctypes.byref(P), x, ids, w, y, ws, wsb, None)
+
+
+def test_packed_expert_refusals():
+    w1, w2, a1, a2 = F.preset("w4a16")
+    tok = F.qdesc(F.FQ_INT, F.FQ_PER_ROW, 0, F.FQ_DYNAMIC, -128, 127)
+    for kw in (dict(fmt="w8a8"), dict(fmt="fp8"), dict(T=513), dict(quants=(w1, w2, tok, a2)),
+               dict(quants=(w1, w2, a1, tok)), dict(H=8320)):
+        assert _pe(**kw) == F.FQ_E_UNSUPPORTED, kw
+    assert F.packed_expert_workspace_size(F.layer_desc(8, 256, 128, 513, 2, w1, w2, a1, a2)) == 0
+    for kw in (dict(H=192), dict(T=-1), dict(k=9), dict(E=0)):
+        assert _pe(**kw) == F.FQ_E_SHAPE, kw
+    for kw in (dict(w1_codes=None), dict(w2_codes=None), dict(s_w1=None), dict(t_w1=FAKE), dict(w2_block_codes=FAKE),
+               dict(s_a1=FAKE), dict(fmt="nvfp4", s_a1=None), dict(fmt="nvfp4", s_a2=None), dict(fmt="nvfp4", t_w2=None),
+               dict(x=None), dict(ids=None), dict(w=None), dict(y=None)):
+        assert _pe(**kw) == F.FQ_E_INVALID, kw
+    for kw in (dict(x=FAKE + 8), dict(ids=MIS), dict(w=MIS), dict(y=FAKE + 8), dict(ws=FAKE + 16),
+               dict(w1_codes=FAKE + 4), dict(s_w2=MIS), dict(fmt="nvfp4", s_a1=MIS)):
+        assert _pe(**kw) == F.FQ_E_ALIGN, kw
+    need = F.packed_expert_workspace_size(F.layer_desc(8, 256, 128, 4, 2, w1, w2, a1, a2))
+    assert need >= 8 * (128 * 2 + 256 * 4)
+    assert _pe(wsb=need - 1) == F.FQ_E_WORKSPACE
+    assert _pe(ws=None) == F.FQ_E_WORKSPACE
+    assert _pe(T=0, x=None, ids=None, w=None, y=None, ws=None) == F.FQ_OK
