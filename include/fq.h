@@ -459,7 +459,7 @@ typedef struct {
     float distill_weight;      /* weight of the top-k KL                              */
 } fq_head_desc;
 /* Bytes of device workspace (256-B aligned): with the gradient, at most about
- * 512 MB for a piece's probabilities (never the logits), fp32 sums of the
+ * 640 MB for a piece's probabilities (never the logits), fp32 sums of the
  * gradient and 8 bytes per token and 64 vocabulary entries of a piece.  0 on a
  * bad descriptor. */
 size_t fq_head_loss_workspace_size(const fq_head_desc* d, int32_t with_grad);

@@ -147,13 +147,29 @@ __device__ __forceinline__ void tile_of(int t, int mt, int nt, int* m, int* n) {
 }
 
 // --------------------------------------------------------------- sparse ---
+// Rows that count: those with a label in the vocabulary, or all without labels.
+__device__ __forceinline__ bool counts(const HeadArgs& a, int64_t t) {
+    return !a.labels || (a.labels[t] >= 0 && a.labels[t] < a.V);
+}
+
 // Logits of the label and the teacher's ids: a block per token, its waves
 // take the slots in turn (slot k is the label).  Slots outside the vocabulary
-// are absent (-inf).
+// are absent (-inf).  One block more forms 1 / (rows that count, at least one).
 __global__ __launch_bounds__(256) void k_head_sparse(HeadArgs a) {
     __shared__ float sz[65];
+    __shared__ int red[4];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    if (t == a.T) {
+        int n = 0;
+        for (int64_t r = threadIdx.x; r < a.T; r += 256) n += counts(a, r) ? 1 : 0;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) n += __shfl_xor(n, m);
+        if (lane == 0) red[w] = n;
+        __syncthreads();
+        if (threadIdx.x == 0) a.inv_n[0] = 1.0f / (float)max(red[0] + red[1] + red[2] + red[3], 1);
+        return;
+    }
     const int slots = a.k + 1, nvec = a.H >> 3;
     const uint4* hr = reinterpret_cast<const uint4*>(a.h + t * a.H);
     for (int j = w; j < slots; j += 4) {
@@ -284,28 +300,35 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
 }
 
 // ---------------------------------------------------------------- merge ---
-// 64 tokens per block, 16 threads per token taking every 16th strip; the
-// sums of the 16 are added in order.
+// 16 tokens per block, 64 threads per token taking every 64th strip; maxima
+// and sums combine in a fixed tree (lanes 16 apart, then the waves in order).
+// 64 tokens per block with 16 threads each left short batches on few CUs with
+// long chains of loads: 86 us against 7 for 333 tokens of 32003 entries.
 __global__ __launch_bounds__(1024) void k_head_merge(HeadArgs a) {
-    __shared__ float red_f[16][64], red_s[16][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * 64 + lane;
+    __shared__ float red_f[16][16], red_s[16][16];
+    const int tok = threadIdx.x & 15, sl = threadIdx.x >> 4, w = threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * 16 + tok;
     const bool live = t < a.T;
     const int strips = a.vc / 64;
     const float f0 = live ? a.frame[t] : 0.0f;
     float f = f0;
-    if (live)
-        for (int s = w; s < strips; s += 16) {
+    if (live) {
+#pragma unroll 4
+        for (int s = sl; s < strips; s += 64) {
             const float2 v = a.stats[(int64_t)s * a.T + t];
             if (v.x != 0.0f) f = fmaxf(f, v.y);
         }
-    red_f[w][lane] = f;
+    }
+    f = fmaxf(f, __shfl_xor(f, 16));
+    f = fmaxf(f, __shfl_xor(f, 32));
+    if ((threadIdx.x & 63) < 16) red_f[w][tok] = f;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f = fmaxf(f, red_f[i][lane]);
+    for (int i = 0; i < 16; ++i) f = fmaxf(f, red_f[i][tok]);
     float sum = 0.0f;
-    if (live)
-        for (int s = w; s < strips; s += 16) {
+    if (live) {
+#pragma unroll 4
+        for (int s = sl; s < strips; s += 64) {
             const float2 v = a.stats[(int64_t)s * a.T + t];
             if (v.y == f) {
                 sum += v.x;
@@ -324,21 +347,24 @@ __global__ __launch_bounds__(1024) void k_head_merge(HeadArgs a) {
                 }
             }
         }
-    red_s[w][lane] = sum;
+    }
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if ((threadIdx.x & 63) < 16) red_s[w][tok] = sum;
     __syncthreads();                                   // also: the strips are in the common frame
-    if (w == 0 && live) {
+    if (threadIdx.x < 16 && live) {
         const float step = f0 == f ? 1.0f : exp2_hw(f0 - f);
         sum = a.sum[t] == 0.0f ? 0.0f : a.sum[t] * step;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum += red_s[i][lane];
+        for (int i = 0; i < 16; ++i) sum += red_s[i][tok];
         a.sum[t] = sum;
         a.frame[t] = f;
         a.step[t] = step;
     }
     if (a.p) {
         const int slots = a.k + 1;
-        const int64_t t0 = (int64_t)blockIdx.x * 64;
-        const int n = (int)min((int64_t)64, a.T - t0) * slots;
+        const int64_t t0 = (int64_t)blockIdx.x * 16;
+        const int n = (int)min((int64_t)16, a.T - t0) * slots;
         for (int i = threadIdx.x; i < n; i += 1024) {
             const int64_t r = t0 + i / slots;
             const int j = i % slots;
@@ -407,27 +433,6 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
 }
 
 // ------------------------------------------------------------------ out ---
-// Rows that count: those with a label in the vocabulary, or all without labels.
-__device__ __forceinline__ bool counts(const HeadArgs& a, int64_t t) {
-    return !a.labels || (a.labels[t] >= 0 && a.labels[t] < a.V);
-}
-
-// 1 / (rows that count), at least one
-__global__ __launch_bounds__(1024) void k_head_count(HeadArgs a) {
-    __shared__ int red[16];
-    int n = 0;
-    for (int64_t t = threadIdx.x; t < a.T; t += 1024) n += counts(a, t) ? 1 : 0;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) n += __shfl_xor(n, m);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = n;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int tot = 0;
-        for (int i = 0; i < 16; ++i) tot += red[i];
-        a.inv_n[0] = 1.0f / (float)max(tot, 1);
-    }
-}
-
 // A block per token: loss and coefficients by the first wave (lane j is slot
 // j, k <= 64; the label is lane 0's second slot), then 8 columns per thread.
 __global__ __launch_bounds__(256) void k_head_out(HeadArgs a) {
@@ -524,21 +529,29 @@ __global__ __launch_bounds__(1024) void k_head_mean(HeadArgs a, float* loss) {
 
 }  // namespace
 
-// The vocabulary's pieces and the second product's splits: P of a piece takes
-// at most 512 MB (and a piece of the weight 2 GB, the reach of a buffer
-// resource's offsets), pieces of equal size; where the gradient's tiles are
-// fewer than the CUs the piece is split until they are about as many.
+// The vocabulary's pieces and the second product's splits.  P of a piece takes
+// at most 640 MB (and a piece of the weight 2 GB, the reach of a buffer
+// resource's offsets); of the numbers of equal pieces from the least on, up to
+// half as many again, the one whose first products fill the 256 CUs in the
+// fewest rounds of tiles.  Where the gradient's tiles are fewer than the CUs
+// the piece is split until they are about as many.
 HeadPlan head_plan(int64_t T, int64_t H, int64_t V) {
     HeadPlan p{};
     const int64_t mt = (T + BM - 1) / BM, nt = (H + BN - 1) / BN;
-    int64_t most = ((int64_t)512 << 20) / (2 * (T > 0 ? T : 1));
+    int64_t most = ((int64_t)640 << 20) / (2 * (T > 0 ? T : 1));
     if (most > ((int64_t)1 << 30) / H) most = ((int64_t)1 << 30) / H;
     most = most / BN * BN;
     if (most < BN) most = BN;
-    p.pieces = (int)((V + most - 1) / most);
-    const int64_t vc = (V + p.pieces - 1) / p.pieces;
-    p.vc = (int)((vc + BN - 1) / BN * BN);
-    p.pieces = (int)((V + p.vc - 1) / p.vc);
+    const int64_t least = (V + most - 1) / most;
+    int64_t best = -1;
+    for (int64_t n = least; n <= least + least / 2 && n <= least + 32; ++n) {
+        const int64_t vc = ((V + n - 1) / n + BN - 1) / BN * BN, pieces = (V + vc - 1) / vc;
+        const int64_t rounds = pieces * ((mt * (vc / BN) + 255) / 256);
+        if (best >= 0 && rounds >= best) continue;
+        best = rounds;
+        p.vc = (int)vc;
+        p.pieces = (int)pieces;
+    }
     const int64_t tiles = mt * nt > 0 ? mt * nt : 1;
     int64_t sp = 256 / tiles;
     if (sp > p.vc / (8 * BK)) sp = p.vc / (8 * BK);
@@ -554,8 +567,7 @@ hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t 
         a.vc = pl.vc;
         a.splits = pl.splits;
         a.ksplit = pl.ksplit;
-        hipLaunchKernelGGL(k_head_count, dim3(1), dim3(1024), 0, st, a);
-        hipLaunchKernelGGL(k_head_sparse, dim3((unsigned)a.T), dim3(256), 0, st, a);
+        hipLaunchKernelGGL(k_head_sparse, dim3((unsigned)a.T + 1), dim3(256), 0, st, a);
         hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
         for (int i = 0; i < pl.pieces; ++i) {
@@ -564,7 +576,7 @@ hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t 
             const unsigned g1 = (unsigned)((mt * (pl.vc / BN) + 7) / 8 * 8);
             if (a.grad) hipLaunchKernelGGL(k_head_probs<true>, dim3(g1), dim3(512), 0, st, a);
             else hipLaunchKernelGGL(k_head_probs<false>, dim3(g1), dim3(512), 0, st, a);
-            hipLaunchKernelGGL(k_head_merge, dim3((unsigned)((a.T + 63) / 64)), dim3(1024), 0, st, a);
+            hipLaunchKernelGGL(k_head_merge, dim3((unsigned)((a.T + 15) / 16)), dim3(1024), 0, st, a);
             if (a.grad)
                 hipLaunchKernelGGL(k_head_grad, dim3((unsigned)((mt * nt * pl.splits + 7) / 8 * 8)), dim3(512), 0, st,
                                    a);

@@ -345,12 +345,22 @@ def distill_loss(d: DistillDesc, student, loss, teacher=None, top_v=None, top_i=
 # These wrappers check what the C side cannot see of a tensor: its type, its
 # shape, that it is contiguous and on one GPU; they raise ValueError.  The work
 # goes to the tensors' own device and, unless `stream` is given, to the current
-# stream of that device.
+# stream of that device.  They stand in front of kernels of a few microseconds,
+# so they are kept short: 0.25 us a tensor, 0.1 us for the stream (the handle
+# itself; torch.cuda.current_stream() takes 2.7 us to wrap it).
+try:
+    import torch as _torch
+    _BF16, _F32, _I32, _U8 = _torch.bfloat16, _torch.float32, _torch.int32, _torch.uint8
+except ImportError:
+    _torch = None
+
+
 def _expect(where, name, t, dtype, shape, device):
+    """Address of tensor t (None: none), which must have this type, shape and device index (-1: the CPU)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{where}: {name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}, "
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{where}: {name} must be a contiguous {dtype} tensor of shape {list(shape)} on GPU {device}, "
                          f"got {t.dtype} {list(t.shape)} on {t.device}"
                          f"{'' if t.is_contiguous() else ', not contiguous'}")
     return t.data_ptr()
@@ -360,25 +370,30 @@ def _scratch(where, t, device):
     """(address, bytes) of a workspace tensor of any type."""
     if t is None:
         return None, 0
-    if not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{where}: the workspace must be a contiguous tensor on {device}")
+    if not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{where}: the workspace must be a contiguous tensor on GPU {device}")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _device_of(where, t):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{where}: the tensors must live on the GPU, got {t.device}")
-    return t.device
+    return t.get_device()
+
+
+_raw_stream = getattr(getattr(_torch, "_C", None), "_cuda_getCurrentRawStream", None) or (
+    lambda device: _torch.cuda.current_stream(device).cuda_stream)
 
 
 def _call(where, fn, device, stream, *args):
     """fn(*args, stream) with the tensors' device current; raises FqError on an error status."""
-    import torch
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, stream if stream is not None else torch.cuda.current_stream().cuda_stream)
+    if stream is None:
+        stream = _raw_stream(device)
+    if _torch.cuda.current_device() == device:
+        st = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, stream if stream is not None else torch.cuda.current_stream().cuda_stream)
+        with _torch.cuda.device(device):
+            st = fn(*args, stream)
     if st != FQ_OK:
         raise FqError(st, where)
 
@@ -388,24 +403,22 @@ def rms_norm_fwd(x, gamma, eps, residual=None, sum=None, y=None, rstd=None, q: Q
     """RMS norm of bf16 x [rows, cols] (fq_rms_norm_fwd): writes those of sum (bf16(x + residual)), y, rstd
     [rows] and, with the 8-bit quantiser q, codes (uint8) that are given.  scale is written for a dynamic q
     ([rows] or [rows, cols/group]) and read ([1]) for a per-tensor one."""
-    import torch
     w = "rms_norm_fwd"
     dev = _device_of(w, x)
     if x.dim() != 2:
         raise ValueError(f"{w}: x must be [rows, cols], got {list(x.shape)}")
-    rows, cols = x.shape
-    bf, f32 = torch.bfloat16, torch.float32
+    rows, cols = full = x.shape
+    bf, f32 = _BF16, _F32
     sshape = None
     if scale is not None:
         if q is None:
             raise ValueError(f"{w}: scale needs a quantiser")
         sshape = {FQ_PER_TENSOR: (1,), FQ_PER_ROW: (rows,)}.get(q.gran) or (rows, cols // max(q.group, 1))
-    full = (rows, cols)
     _call(w, _lib.fq_rms_norm_fwd, dev, stream, None if q is None else ctypes.byref(q), rows, cols, eps,
           _expect(w, "x", x, bf, full, dev), _expect(w, "residual", residual, bf, full, dev),
           _expect(w, "gamma", gamma, bf, (cols,), dev), _expect(w, "sum", sum, bf, full, dev),
           _expect(w, "y", y, bf, full, dev), _expect(w, "rstd", rstd, f32, (rows,), dev),
-          _expect(w, "codes", codes, torch.uint8, full, dev), _expect(w, "scale", scale, f32, sshape, dev))
+          _expect(w, "codes", codes, _U8, full, dev), _expect(w, "scale", scale, f32, sshape, dev))
 
 
 def rms_norm_bwd_workspace_size(rows: int, cols: int) -> int:
@@ -415,13 +428,12 @@ def rms_norm_bwd_workspace_size(rows: int, cols: int) -> int:
 def rms_norm_bwd(s, gamma, rstd, dy, dx, dsum=None, dgamma=None, workspace=None, stream=None):
     """Gradient of the norm of s (the forward's sum, or x): dx, and with dgamma (fp32 [cols], needs the
     workspace) the gradient of gamma; dsum is the gradient that reaches s past the norm."""
-    import torch
     w = "rms_norm_bwd"
     dev = _device_of(w, s)
     if s.dim() != 2:
         raise ValueError(f"{w}: s must be [rows, cols], got {list(s.shape)}")
-    rows, cols = full = tuple(s.shape)
-    bf, f32 = torch.bfloat16, torch.float32
+    rows, cols = full = s.shape
+    bf, f32 = _BF16, _F32
     ws, nb = _scratch(w, workspace, dev)
     _call(w, _lib.fq_rms_norm_bwd, dev, stream, rows, cols, _expect(w, "s", s, bf, full, dev),
           _expect(w, "gamma", gamma, bf, (cols,), dev), _expect(w, "rstd", rstd, f32, (rows,), dev),
@@ -443,10 +455,9 @@ def head_loss(d: HeadDesc, h, w, loss, top_v=None, top_i=None, labels=None, row_
     """Cross entropy and top-k distillation of bf16 hidden states h [tokens, hidden] under the frozen output
     weight w [vocab, hidden] (fq_head_loss): the mean loss into loss[0], each token's into row_loss, d loss / d h
     into grad.  Logits are never stored."""
-    import torch
     n = "head_loss"
     dev = _device_of(n, h)
-    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    bf, f32, i32 = _BF16, _F32, _I32
     T, k = d.tokens, d.topk
     ws, nb = _scratch(n, workspace, dev)
     _call(n, _lib.fq_head_loss, dev, stream, ctypes.byref(d), _expect(n, "h", h, bf, (T, d.hidden), dev),
@@ -463,7 +474,6 @@ def _scale_shape(q: QDesc, E, N, K):
 def packed_matvec(q: QDesc, codes, x, y, scale=None, block_codes=None, tensor_scale=None, which=None, stream=None):
     """y [m, N] = x [m, K] times packed 4-bit weights (fq_packed_matvec): codes uint8 [E, N, K/2] as fq_tensor
     gives them, with scale (INT) or block_codes and tensor_scale (NVFP4); which [m] names each row's matrix."""
-    import torch
     n = "packed_matvec"
     dev = _device_of(n, x)
     if codes.dim() != 3 or x.dim() != 2:
@@ -471,13 +481,13 @@ def packed_matvec(q: QDesc, codes, x, y, scale=None, block_codes=None, tensor_sc
                          f"{list(x.shape)}")
     E, N, K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
     M = x.shape[0]
-    u8, f32, bf = torch.uint8, torch.float32, torch.bfloat16
+    u8, f32, bf = _U8, _F32, _BF16
     _call(n, _lib.fq_packed_matvec, dev, stream, ctypes.byref(q), E, N, K,
           _expect(n, "codes", codes, u8, (E, N, K // 2), dev),
           _expect(n, "block_codes", block_codes, u8, (E, N, K // 16), dev),
           _expect(n, "scale", scale, f32, _scale_shape(q, E, N, K), dev),
           _expect(n, "tensor_scale", tensor_scale, f32, (E,), dev), M,
-          _expect(n, "which", which, torch.int32, (M,), dev), _expect(n, "x", x, bf, (M, K), dev),
+          _expect(n, "which", which, _I32, (M,), dev), _expect(n, "x", x, bf, (M, K), dev),
           _expect(n, "y", y, bf, (M, N), dev))
 
 
@@ -497,10 +507,9 @@ def packed_expert_workspace_size(L: LayerDesc) -> int:
 
 def packed_expert_fwd(L: LayerDesc, P: PackedExperts, x, topk_ids, topk_w, y, workspace, stream=None):
     """The expert layer on packed weights for the T tokens of L (fq_packed_expert_fwd)."""
-    import torch
     n = "packed_expert_fwd"
     dev = _device_of(n, x)
-    f32, bf, u8 = torch.float32, torch.bfloat16, torch.uint8
+    f32, bf, u8 = _F32, _BF16, _U8
     T, H, k = L.T, L.H, L.topk
     sizes = (L.E, H, L.I, dev)
     if P.checked != sizes:                               # the weights' shapes, once per layer
@@ -516,5 +525,5 @@ def packed_expert_fwd(L: LayerDesc, P: PackedExperts, x, topk_ids, topk_w, y, wo
         P.checked = sizes
     ws, nb = _scratch(n, workspace, dev)
     _call(n, _lib.fq_packed_expert_fwd, dev, stream, ctypes.byref(L), ctypes.byref(P),
-          _expect(n, "x", x, bf, (T, H), dev), _expect(n, "topk_ids", topk_ids, torch.int32, (T, k), dev),
+          _expect(n, "x", x, bf, (T, H), dev), _expect(n, "topk_ids", topk_ids, _I32, (T, k), dev),
           _expect(n, "topk_w", topk_w, f32, (T, k), dev), _expect(n, "y", y, bf, (T, H), dev), ws, nb)

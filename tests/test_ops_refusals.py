@@ -81,13 +81,13 @@ def test_wrappers_refuse_tensors():
 
 def test_expect_checks_type_shape_layout_and_device():
     # the wrappers' one check, on CPU tensors
-    dev = torch.device("cpu")
+    dev = -1
     t = torch.zeros((4, 6), dtype=torch.bfloat16)
     assert F._expect("f", "t", t, torch.bfloat16, (4, 6), dev) == t.data_ptr()
     assert F._expect("f", "t", None, torch.bfloat16, (4, 6), dev) is None
     for bad, dt, shape, d in ((t, torch.float32, (4, 6), dev), (t, torch.bfloat16, (6, 4), dev),
                               (t.t(), torch.bfloat16, (6, 4), dev), (t[:, :3], torch.bfloat16, (4, 3), dev),
-                              (t, torch.bfloat16, (4, 6), torch.device("cuda", 0))):
+                              (t, torch.bfloat16, (4, 6), 0)):
         with pytest.raises(ValueError, match="contiguous"):
             F._expect("f", "t", bad, dt, shape, d)
 
