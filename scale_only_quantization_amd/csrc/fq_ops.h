@@ -84,8 +84,9 @@ struct PackedW {           // a stack of matrices as fq_tensor's codes
     const float* scale;    // INT: spr per row
     const float* tscale;   // NVFP4: per matrix
     int K;                 // a multiple of 32
-    int group;             // INT: columns per scale (K where one per row)
+    int group;             // INT: columns per scale (at least 128 where one per row)
     int spr;               // INT: scales per row
+    int gshift;            // INT: chunk >> gshift (groups from 128), 32-column segment >> gshift (below) is its scale
 };
 struct MatvecArgs {
     PackedW w;

@@ -15,27 +15,32 @@
 //          again in fp32.  The scale multiplies the sum of its group.
 //   NVFP4  q d is exact in bf16 (2 + 4 significant bits): two conversions and
 //          two products per pair of codes; t multiplies the end.
-// A lane loads 16 bytes, 32 codes, of one weight row.  Which k a lane holds is
-// free as long as x agrees: with a scale per row or per 128 and more a lane's
-// four words are four products' operands as they are; with groups of 32 or 64
-// the words are transposed between the four lane groups first (four lane
-// swaps), so that one product covers one 32-code segment of all 16 rows.
-// The waves of a block split k and add their sums in order.
+// A lane loads 16 bytes, 32 codes, of one weight row; the four words of the
+// four lanes that hold a row's 128 columns (a chunk) are then transposed
+// between them (four lane swaps), so that product i covers columns 32 i ..
+// 32 i + 31 and its operand of x is 64 consecutive bytes of each row.
+// KW waves of a block share a tile's columns and add their sums in order.  A
+// wave holds x of a slab of four chunks in registers while NT tiles of weight
+// rows pass, the next tile's codes in flight.  Reading x again for every tile
+// cost more than the codes (13 rows by 12289 x 8192 in NVFP4: 37 us, of which
+// 22 were x through the L2, against 15 for codes and scales alone); and the
+// scales of a slab are one load, a lane group per chunk, spread by lane swaps
+// (a load per chunk touches 16 cache lines for 128 bytes: 6 us of those 15).
+// All loads go through buffer resources: a lane's constant plus a scalar, and
+// rows past the end read as zero without a branch.
 #include <type_traits>
 
 #include "fq_act.h"
+#include "fq_mfma.h"
 #include "fq_ops.h"
 
 namespace fq {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 enum Fmt { INT_WIDE = 0, INT_NARROW = 1, NVFP4 = 2 };
-
-constexpr int NW = 4;                     // waves of a block
 
 __device__ __forceinline__ f32x4 mfma(u32x4 x, u32x4 w, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), c, 0,
@@ -87,179 +92,339 @@ __device__ __forceinline__ void transpose4(u32x4& w) {
     w.w = d[1];
 }
 
-// Sums over the 128-column chunks [c0, c1) of 16 MT rows of x with NT tiles of
-// 16 weight rows: acc[mt][nt][i] is row 16 mt + 4 (lane/16) + i of x and weight
-// row lane%16 of tile nt.  row: this lane's weight row of each tile (in the
-// whole stack); xr: this lane's row lane%16 of each tile of x, or null
-// (zeros).  U chunks' loads are in flight at once; columns past K have x = 0
-// and read the row's last codes again.
-template <int FMT, int MT, int NT, int U>
-__device__ __forceinline__ void dot_rows(const PackedW& w, const int64_t (&row)[NT], int c0, int c1,
-                                         const uint16_t* const (&xr)[MT], f32x4 (&acc)[MT][NT]) {
-    const int g = (threadIdx.x & 63) >> 4;
-    const int nseg = w.K >> 5;
-    const u32x4 zero = {0, 0, 0, 0}, minus136 = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};
-    for (int c = c0; c < c1; c += U) {
-        u32x4 q[U][NT], x[U][MT][4];
-        float s[U][NT][FMT == INT_NARROW ? 4 : 1];
-        uint32_t d[U][NT];
+constexpr int WV = 4;                     // waves of a block of the expert layer
+constexpr int XC = 4;                     // chunks of a slab: one per lane group in the scales' load
+
+// A run of weight rows as buffer resources; rows past its end read as zero.
+template <int FMT>
+struct Rows {
+    __amdgpu_buffer_rsrc_t codes, scale;             // scale: INT scales or NVFP4 block codes
+    uint32_t vc, vs;                                 // this lane's offsets: row lane%16, its quarter of a chunk
+    uint32_t cb, sb;                                 // bytes per row
+    __device__ __forceinline__ Rows(const PackedW& w, int64_t row0, int64_t rows) {
+        const int lane = threadIdx.x & 63;
+        cb = (uint32_t)w.K >> 1;
+        sb = FMT == NVFP4 ? (uint32_t)w.K >> 4 : (uint32_t)w.spr * 4;
+        codes = make_rsrc(w.codes + row0 * cb, rows * cb);
+        scale = FMT == NVFP4 ? make_rsrc(w.bcodes + row0 * sb, rows * sb) : make_rsrc(w.scale + row0 * w.spr, rows * sb);
+        vc = (lane & 15) * cb + (lane >> 4) * 16;
+        vs = (lane & 15) * sb;
+    }
+};
+
+// The value that each lane group (16 lanes) g holds, given to all lanes: o[g].
+__device__ __forceinline__ void spread4(uint32_t v, uint32_t (&o)[4]) {
+    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);         // groups 0 1 0 1 and 2 3 2 3
+    const auto a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+    o[0] = a[0];
+    o[1] = a[1];
+    o[2] = b[0];
+    o[3] = b[1];
+}
+
+// A slab of a tile's codes and scales, as loaded.
+template <int FMT>
+struct Slab {
+    static constexpr int NS = FMT == NVFP4 ? 2 : FMT == INT_WIDE ? 1 : 4;        // scale words of a chunk
+    u32x4 q[XC];
+    uint32_t s[NS];                                  // of chunk c + lane group
+    __device__ __forceinline__ void load(const PackedW& w, const Rows<FMT>& r, int row, int c) {
+        const uint32_t oc = row * r.cb + c * 64, os = row * r.sb;
+        const int cg = c + ((threadIdx.x & 63) >> 4);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int seg = (c + u) * 4 + g, sg = min(seg, nseg - 1);
+        for (int u = 0; u < XC; ++u) q[u] = __builtin_amdgcn_raw_buffer_load_b128(r.codes, r.vc, oc + u * 64, 0);
+        if (FMT == NVFP4) {
+            if ((w.K & 127) == 0) {
+                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r.scale, r.vs + cg * 8, os, 0);
+                s[0] = v.x;
+                s[1] = v.y;
+            } else {                                  // rows of any even number of block codes
+                uint32_t h[4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                q[u][n] = *reinterpret_cast<const u32x4*>(w.codes + row[n] * (w.K >> 1) + sg * 16);
-                if (FMT == NVFP4)
-                    d[u][n] = *reinterpret_cast<const uint16_t*>(w.bcodes + row[n] * (w.K >> 4) + sg * 2);
-                else if (FMT == INT_WIDE)
-                    s[u][n][0] = w.scale[row[n] * w.spr + min((c + u) * 128, w.K - 1) / w.group];
-                else
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        s[u][n][i] = w.scale[row[n] * w.spr + min((c + u) * 4 + i, nseg - 1) * 32 / w.group];
+                for (int i = 0; i < 4; ++i) h[i] = __builtin_amdgcn_raw_buffer_load_b16(r.scale, r.vs + cg * 8 + 2 * i, os, 0);
+                s[0] = h[0] | h[1] << 16;
+                s[1] = h[2] | h[3] << 16;
             }
+        } else {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = FMT == INT_NARROW ? ((c + u) * 4 + i) * 32 + 8 * g : seg * 32 + 8 * i;
-                    x[u][m][i] = xr[m] && c + u < c1 && k < w.K ? *reinterpret_cast<const u32x4*>(xr[m] + k) : zero;
-                }
+            for (int i = 0; i < NS; ++i)
+                s[i] = __builtin_amdgcn_raw_buffer_load_b32(r.scale, r.vs + ((cg * NS + i) >> w.gshift) * 4, os, 0);
         }
+    }
+};
+
+// acc[n][m] += 16 rows m of x times tile n's slab of chunks c .. c + 3:
+// acc[n][m][v] is row 16 m + 4 (lane/16) + v of x, weight row lane%16.  x(u, o)
+// fills o[m][i] with the operands of chunk u's products i (columns 32 i + 8
+// (lane/16) .. + 7; INT: in int_order).  base(o, u, m): INT_WIDE, the chunk's
+// sum of x times -136.
+template <int FMT, int MT, int NT, typename X, typename B>
+__device__ __forceinline__ void add_slab(Slab<FMT> (&k)[NT], int c, int nseg, X&& x, B&& base, f32x4 (&acc)[NT][MT]) {
+    const int g = (threadIdx.x & 63) >> 4;
+    const f32x4 z = {0, 0, 0, 0};
+    const u32x4 minus136 = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};
+    uint32_t sc[NT][Slab<FMT>::NS][4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            f32x4 base[MT][FMT == INT_NARROW ? 4 : 1];
-            if (FMT != NVFP4)
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < Slab<FMT>::NS; ++i) spread4(k[n].s[i], sc[n][i]);
+#pragma unroll
+    for (int u = 0; u < XC; ++u) {
+        if ((c + u) * 4 >= nseg) continue;            // past the row's end
+        u32x4 xu[MT][4];
+        x(u, xu);
+        f32x4 b[MT];
+        if (FMT == INT_WIDE)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) b[m] = base(xu[m], u, m);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            transpose4(k[n].q[u]);
+            float dd[4];
+            if (FMT == NVFP4) {                       // word i is the g-th quarter of segment i: block 2 i + g/2
+                const int sh = 4 * (g & 2);
+                const int d0 = (int)(sc[n][0][u] >> sh), d1 = (int)(sc[n][1 % Slab<FMT>::NS][u] >> sh);
+                dd[0] = __builtin_amdgcn_cvt_f32_fp8(d0, 0);
+                dd[1] = __builtin_amdgcn_cvt_f32_fp8(d0, 2);
+                dd[2] = __builtin_amdgcn_cvt_f32_fp8(d1, 0);
+                dd[3] = __builtin_amdgcn_cvt_f32_fp8(d1, 2);
+                if ((c + u) * 4 + 4 > nseg)           // another row's factors: zero, not a NaN for zero times it
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) dd[i] = (c + u) * 4 + i < nseg ? dd[i] : 0.0f;
+            }
+            f32x4 part[MT];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const u32x4 wv = FMT == NVFP4 ? fp4_words(k[n].q[u][i], dd[i]) : int_words(k[n].q[u][i]);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
+                    if (FMT == NVFP4) {
+                        acc[n][m] = mfma(xu[m][i], wv, acc[n][m]);
+                    } else if (FMT == INT_WIDE) {
+                        part[m] = mfma(xu[m][i], wv, i == 0 ? b[m] : part[m]);
+                    } else {
+                        part[m] = mfma(xu[m][i], wv, mfma(xu[m][i], minus136, z));
+                        const float s = __uint_as_float(sc[n][i % Slab<FMT>::NS][u]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[u][m][i] = int_order(x[u][m][i]);
-                        const f32x4 z = {0, 0, 0, 0};
-                        if (FMT == INT_NARROW) base[m][i] = mfma(x[u][m][i], minus136, z);
-                        else base[m][0] = mfma(x[u][m][i], minus136, i == 0 ? z : base[m][0]);
+                        for (int v = 0; v < 4; ++v) acc[n][m][v] = __builtin_fmaf(part[m][v], s, acc[n][m][v]);
                     }
                 }
+            }
+            if (FMT == INT_WIDE) {
+                const float s = __uint_as_float(sc[n][0][u]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (FMT == INT_NARROW) transpose4(q[u][n]);
-                float dd[2];
-                if (FMT == NVFP4) {
-                    dd[0] = __builtin_amdgcn_cvt_f32_fp8((int)d[u][n], 0);
-                    dd[1] = __builtin_amdgcn_cvt_f32_fp8((int)d[u][n], 1);
-                }
-                f32x4 part[MT];
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const u32x4 wv = FMT == NVFP4 ? fp4_words(q[u][n][i], dd[i >> 1]) : int_words(q[u][n][i]);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        if (FMT == NVFP4) {
-                            acc[m][n] = mfma(x[u][m][i], wv, acc[m][n]);
-                        } else if (FMT == INT_WIDE) {
-                            part[m] = mfma(x[u][m][i], wv, i == 0 ? base[m][0] : part[m]);
-                        } else {
-                            part[m] = mfma(x[u][m][i], wv, base[m][i]);
-#pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                acc[m][n][v] = __builtin_fmaf(part[m][v], s[u][n][i], acc[m][n][v]);
-                        }
-                    }
-                }
-                if (FMT == INT_WIDE)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            acc[m][n][v] = __builtin_fmaf(part[m][v], s[u][n][0], acc[m][n][v]);
+                    for (int v = 0; v < 4; ++v) acc[n][m][v] = __builtin_fmaf(part[m][v], s, acc[n][m][v]);
             }
         }
     }
 }
 
-// chunks in flight: the loads' registers
-constexpr int flight(int mt, int nt) { return mt * nt <= 2 ? 4 / nt : mt <= 2 ? 2 : 1; }
+// 16 MT rows of x (resource xs, this lane's row lane%16 of tile m at vx[m])
+// times NT tiles of 16 weight rows that start at rows row(n) of r, over this
+// wave's slabs kp, kp + KW, ... of the columns, x of a slab in registers.  The
+// order of a row's sum does not depend on MT or NT.
+template <int FMT, int MT, int NT, int KW, typename R>
+__device__ __forceinline__ void dot_rows(const PackedW& w, const Rows<FMT>& r, R&& row, int kp,
+                                         __amdgpu_buffer_rsrc_t xs, const uint32_t (&vx)[MT], f32x4 (&acc)[NT][MT]) {
+    const int nseg = w.K >> 5, nch = (nseg + 3) >> 2;
+    const f32x4 z = {0, 0, 0, 0};
+    const u32x4 zero = {0, 0, 0, 0}, minus136 = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[n][m] = z;
+    Slab<FMT> sl[2][1];
+    if (kp * XC < nch) sl[0][0].load(w, r, row(0), kp * XC);
+    for (int c = kp * XC; c < nch; c += KW * XC) {
+        u32x4 x[MT][XC][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int u = 0; u < XC; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[m][u][i] = __builtin_amdgcn_raw_buffer_load_b128(xs, vx[m], c * 256 + u * 256 + i * 64, 0);
+        if ((c + XC) * 4 > nseg)                      // the row ends inside the slab
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int u = 0; u < XC; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if ((c + u) * 4 + i >= nseg) x[m][u][i] = zero;
+        f32x4 base[MT][XC];
+        if (FMT != NVFP4)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int u = 0; u < XC; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[m][u][i] = int_order(x[m][u][i]);
+                        if (FMT == INT_WIDE) base[m][u] = mfma(x[m][u][i], minus136, i == 0 ? z : base[m][u]);
+                    }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (n + 1 < NT) sl[(n + 1) & 1][0].load(w, r, row(n + 1), c);
+            else if (c + KW * XC < nch) sl[(n + 1) & 1][0].load(w, r, row(0), c + KW * XC);
+            __builtin_amdgcn_sched_barrier(0);        // in flight before this tile's products
+            add_slab<FMT, MT, 1>(
+                sl[n & 1], c, nseg,
+                [&](int u, u32x4 (&o)[MT][4]) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[m][i] = x[m][u][i];
+                },
+                [&](const u32x4 (&)[4], int u, int m) { return base[m][u]; },
+                reinterpret_cast<f32x4 (&)[1][MT]>(acc[n]));
+        }
+        if (NT & 1) sl[0][0] = sl[1][0];              // the next slab's first tile
+    }
+}
 
-// The waves' sums of a block added in wave order through LDS: value (m, n, v)
-// of lane l at red[wave][(m NT + n) 4 + v][l]; afterwards thread (wave v,
-// lane l) calls f(m, n, row 16 m + 4 (l/16) + v of x, column l%16 of the tile, sum).
-template <int MT, int NT>
+// Rows of x in LDS, shared by a block's waves: K columns (a multiple of 128) at
+// a stride of K + 8, so that 16 rows of one column fall on distinct banks;
+// INT: each 8 columns in int_order.
+template <int FMT>
+struct XLds {
+    lds_t* p;
+    uint32_t stride;                                  // bytes
+    __device__ __forceinline__ static uint32_t bytes_per_row(int K) { return K * 2 + 16; }
+    // rows 0 .. n - 1 from src(i), by the whole block
+    template <typename S>
+    __device__ __forceinline__ void fill(int K, int n, S&& src) {
+        for (int m = 0; m < n; ++m) {
+            const uint16_t* row = src(m);             // uniform
+            for (int v = threadIdx.x; v < K >> 3; v += blockDim.x) {
+                u32x4 x = *reinterpret_cast<const u32x4*>(row + v * 8);
+                if (FMT != NVFP4) x = int_order(x);
+                *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(p + m * stride + v * 16) = x;
+            }
+        }
+    }
+};
+
+// Rows of x in LDS times two tiles of 16 weight rows that start at rows row0
+// and row1 of r, over this wave's slabs kp, kp + KW, ...  begin() sends the
+// first slab's loads, before the rows of x are there; run() takes this lane's
+// row at byte xo (its quarter of a 32-column segment included).  One slab is
+// in registers at a time: a second one (the next slab's loads during this
+// one's products) took the registers that hold a fourth wave per SIMD, and
+// the layer's blocks, short chains of dependent loads, need the waves more
+// (fc1 of 16 tokens in NVFP4: 45 us against 58).
+template <int FMT, int KW>
+struct DotLds {
+    const PackedW& w;
+    const Rows<FMT>& r;
+    int row0, row1, c;
+    Slab<FMT> sl[2];
+    __device__ __forceinline__ void load() {
+        sl[0].load(w, r, row0, c);
+        sl[1].load(w, r, row1, c);
+    }
+    __device__ __forceinline__ void begin(int kp) {
+        c = kp * XC;
+        if (c * 128 < w.K) load();
+    }
+    __device__ __forceinline__ void run(const lds_t* xp, uint32_t xo, f32x4 (&acc)[2][1]) {
+        const f32x4 z = {0, 0, 0, 0};
+        const u32x4 minus136 = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};
+        const int nseg = w.K >> 5, nch = (nseg + 3) >> 2;
+        acc[0][0] = acc[1][0] = z;
+        while (c < nch) {
+            add_slab<FMT, 1, 2>(
+                sl, c, nseg,
+                [&](int u, u32x4 (&o)[1][4]) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[0][i] = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(
+                            xp + xo + (c + u) * 256 + i * 64);
+                },
+                [&](const u32x4 (&v)[4], int, int) {
+                    f32x4 b = z;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) b = mfma(v[i], minus136, b);
+                    return b;
+                },
+                acc);
+            c += KW * XC;
+            if (c < nch) load();
+        }
+    }
+};
+
+// A barrier that waits for this wave's LDS accesses but not for its loads from memory.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The KW waves' sums of a block's tiles, added in wave order through LDS.  Of
+// tile n and 16 rows m of x, thread (lane, v) gets row 16 m + 4 (lane/16) + v
+// and weight row lane%16.
+template <int MT, int NT, int KW>
 struct Reduce {
-    float red[NW][MT * NT * 4][64];
-    __device__ __forceinline__ void put(const f32x4 (&acc)[MT][NT]) {
+    float red[KW][MT * NT * 4][64];
+    __device__ __forceinline__ void put(const f32x4 (&acc)[NT][MT]) {
         const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) red[w][(m * NT + n) * 4 + v][lane] = acc[m][n][v];
+                for (int v = 0; v < 4; ++v) red[w][(m * NT + n) * 4 + v][lane] = acc[n][m][v];
         __syncthreads();
     }
-    __device__ __forceinline__ float get(int m, int n) const {
-        const int lane = threadIdx.x & 63, v = threadIdx.x >> 6;
+    __device__ __forceinline__ float get(int m, int n, int v) const {
+        const int lane = threadIdx.x & 63;
         float s = red[0][(m * NT + n) * 4 + v][lane];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) s += red[w][(m * NT + n) * 4 + v][lane];
+        for (int w = 1; w < KW; ++w) s += red[w][(m * NT + n) * 4 + v][lane];
         return s;
     }
 };
 
 __device__ __forceinline__ uint16_t bf16_of(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
-// this wave's share of the 128-column chunks
-__device__ __forceinline__ void wave_chunks(int K, int w, int* c0, int* c1) {
-    const int n = (K + 127) >> 7, per = (n + NW - 1) / NW;
-    *c0 = w * per;
-    *c1 = min(n, *c0 + per);
-}
-
 // --------------------------------------------------------------- matvec ---
-// 16 NT weight rows and 16 MT rows of x per block.  With `which` a block
-// belongs to row r of x: it does nothing if an earlier row names the same
-// matrix, else it takes every row that does, 16 at a time.
-template <int FMT, int MT, int NT>
-__global__ __launch_bounds__(64 * NW) void k_matvec(MatvecArgs a) {
-    __shared__ Reduce<MT, NT> red;
+// 16 NT weight rows and 16 MT rows of x per block.
+template <int FMT, int MT, int NT, int KW>
+__global__ __launch_bounds__(64 * KW) void k_matvec(MatvecArgs a) {
+    __shared__ Reduce<MT, NT, KW> red;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int n0 = blockIdx.x * 16 * NT;
-    int c0, c1;
-    wave_chunks(a.w.K, w, &c0, &c1);
-    int64_t row[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) row[n] = min((int64_t)n0 + 16 * n + (lane & 15), a.N - 1);
+    const int64_t n0 = (int64_t)blockIdx.x * 16 * NT;
     const int m0 = blockIdx.y * 16 * MT;
-    const uint16_t* xr[MT];
-    f32x4 acc[MT][NT];
+    uint32_t vx[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int r = m0 + 16 * m + (lane & 15);
-        xr[m] = r < a.M ? a.x + (int64_t)r * a.w.K : nullptr;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0, 0, 0, 0};
-    }
-    dot_rows<FMT, MT, NT, flight(MT, NT)>(a.w, row, c0, c1, xr, acc);
+    for (int m = 0; m < MT; ++m) vx[m] = (16 * m + (lane & 15)) * (uint32_t)a.w.K * 2 + (lane >> 4) * 16;
+    f32x4 acc[NT][MT];
+    dot_rows<FMT, MT, NT, KW>(
+        a.w, Rows<FMT>(a.w, n0, min((int64_t)16 * NT, a.N - n0)), [](int n) { return 16 * n; }, w,
+        make_rsrc(a.x + (int64_t)m0 * a.w.K, (int64_t)(a.M - m0) * a.w.K * 2), vx, acc);
     red.put(acc);
     const float t = FMT == NVFP4 ? a.w.tscale[0] : 1.0f;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int r = m0 + 16 * m + 4 * (lane >> 4) + w;
-            const int64_t c = (int64_t)n0 + 16 * n + (lane & 15);
-            const float s = red.get(m, n);
-            if (r < a.M && c < a.N) a.y[(int64_t)r * a.N + c] = bf16_of(FMT == NVFP4 ? s * t : s);
-        }
+    for (int i = w; i < MT * NT * 4; i += KW) {
+        const int m = (i >> 2) / NT, n = (i >> 2) % NT, v = i & 3;
+        const int r = m0 + 16 * m + 4 * (lane >> 4) + v;
+        const int64_t c = n0 + 16 * n + (lane & 15);
+        const float s = red.get(m, n, v);
+        if (r < a.M && c < a.N) a.y[(int64_t)r * a.N + c] = bf16_of(FMT == NVFP4 ? s * t : s);
+    }
 }
 
-template <int FMT>
-__global__ __launch_bounds__(64 * NW) void k_matvec_which(MatvecArgs a) {
-    __shared__ Reduce<1, 1> red;
+// With `which`: a block belongs to row r of x.  It does nothing if an earlier
+// row names the same matrix, else it takes every row that does, 16 at a time.
+template <int FMT, int KW>
+__global__ __launch_bounds__(64 * KW) void k_matvec_which(MatvecArgs a) {
+    __shared__ Reduce<1, 1, KW> red;
     __shared__ int ids[PACKED_MAX_ROWS], list[PACKED_MAX_ROWS];
     __shared__ int count;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int n0 = blockIdx.x * 16, r0 = blockIdx.y;
-    for (int i = threadIdx.x; i < a.M; i += 64 * NW) ids[i] = a.which[i];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r0 = blockIdx.y;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    for (int i = threadIdx.x; i < a.M; i += 64 * KW) ids[i] = a.which[i];
     __syncthreads();
     const int e = ids[r0];
     const bool bad = e < 0 || e >= a.E;               // no such matrix: the row is zero
@@ -275,21 +440,21 @@ __global__ __launch_bounds__(64 * NW) void k_matvec_which(MatvecArgs a) {
     }
     __syncthreads();
     if (list[0] != r0) return;                        // an earlier row has this matrix
-    int c0, c1;
-    wave_chunks(a.w.K, w, &c0, &c1);
-    const int64_t row[1] = {(int64_t)(bad ? 0 : e) * a.N + min((int64_t)n0 + (lane & 15), a.N - 1)};
-    const float t = FMT == NVFP4 ? a.w.tscale[bad ? 0 : e] : 1.0f;
+    const float t = bad ? 0.0f : FMT == NVFP4 ? a.w.tscale[e] : 1.0f;
+    const Rows<FMT> rows(a.w, (int64_t)(bad ? 0 : e) * a.N + n0, min((int64_t)16, a.N - n0));
+    const __amdgpu_buffer_rsrc_t xs = make_rsrc(a.x, (int64_t)a.M * a.w.K * 2);
     for (int b = 0; b < count; b += 16) {
-        const uint16_t* xr[1] = {
-            b + (lane & 15) < count ? a.x + (int64_t)list[b + (lane & 15)] * a.w.K : nullptr};
-        f32x4 acc[1][1] = {{f32x4{0, 0, 0, 0}}};
-        if (!bad) dot_rows<FMT, 1, 1, flight(1, 1)>(a.w, row, c0, c1, xr, acc);
-        __syncthreads();                              // the last group's sums have been read
+        const uint32_t vx[1] = {(uint32_t)list[min(b + (lane & 15), count - 1)] * (uint32_t)a.w.K * 2 + (lane >> 4) * 16};
+        f32x4 acc[1][1];
+        dot_rows<FMT, 1, 1, KW>(a.w, rows, [](int) { return 0; }, w, xs, vx, acc);
         red.put(acc);
-        const int m = b + 4 * (lane >> 4) + w;
-        const int64_t c = (int64_t)n0 + (lane & 15);
-        const float s = red.get(0, 0);
-        if (m < count && c < a.N) a.y[(int64_t)list[m] * a.N + c] = bf16_of(FMT == NVFP4 ? s * t : s);
+        for (int v = w; v < 4; v += KW) {
+            const int m = b + 4 * (lane >> 4) + v;
+            const int64_t c = n0 + (lane & 15);
+            const float s = bad ? 0.0f : red.get(0, 0, v);
+            if (m < count && c < a.N) a.y[(int64_t)list[m] * a.N + c] = bf16_of(FMT == NVFP4 ? s * t : s);
+        }
+        __syncthreads();                              // read before the next rows' sums
     }
 }
 
@@ -353,38 +518,64 @@ struct Group {
         start = order ? sload(a.start, r_) : 0;
     }
     __device__ __forceinline__ int at(int i) const { return order ? order[start + i] : r; }
+    __device__ __forceinline__ int at_uniform(int i) const { return order ? sload(order, start + i) : r; }
 };
 
-// fc1 and SwiGLU: 16 gate rows and their 16 up rows per block; the tile of h
-// goes through the second activation quantiser on the way (a 16-block of
-// NVFP4 is the tile's row)
+// The sums of a team of KW waves for two tiles: value i = 4 tile + v of lane l
+// at red[wave][i][l], added in wave order.
+template <int KW>
+__device__ __forceinline__ void team_put(float (*red)[8][64], const f32x4 (&acc)[2][1]) {
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        red[w][v][lane] = acc[0][0][v];
+        red[w][4 + v][lane] = acc[1][0][v];
+    }
+    lds_barrier();
+}
+template <int KW>
+__device__ __forceinline__ float team_get(float (*red)[8][64], int i) {
+    const int lane = threadIdx.x & 63, w0 = (threadIdx.x >> 6) / KW * KW;
+    float s = red[w0][i][lane];
+#pragma unroll
+    for (int o = 1; o < KW; ++o) s += red[w0 + o][i][lane];
+    return s;
+}
+
+// fc1 and SwiGLU of one group of rows: 16 gate rows and their 16 up rows per
+// block, the waves splitting the columns.  `cap` rows of x at a time are in
+// LDS.  The tile of h goes through the second activation quantiser on the way
+// (a 16-block of NVFP4 is the tile's row).
 template <int FMT>
-__global__ __launch_bounds__(64 * NW) void k_packed_fc1(PackedExpertArgs a) {
-    __shared__ Reduce<1, 2> red;
+__global__ __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(4))) void k_packed_fc1(PackedExpertArgs a,
+                                                                                                int cap) {
+    extern __shared__ __attribute__((aligned(16))) char dyn[];
+    __shared__ float red[WV][8][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int r0 = blockIdx.y, i0 = blockIdx.x * 16;
     const Group gr(a, r0);
     if (gr.count == 0) return;
     const int e = clamp_id(sload(a.ids, r0), a.E);
-    int c0, c1;
-    wave_chunks(a.H, w, &c0, &c1);
-    const int64_t base = (int64_t)e * 2 * a.I + i0 + (lane & 15);
-    const int64_t row[2] = {base, base + a.I};
+    const Rows<FMT> rows(a.w1, (int64_t)e * 2 * a.I, 2 * a.I);
     const float t1 = FMT == NVFP4 ? sload(a.w1.tscale, e) : 1.0f;
     const int kind2 = a.a2.q.kind;
     const float s2 = kind2 != K_NONE ? sload(a.a2.s, e) : 0.0f;
-    for (int b = 0; b < gr.count; b += 16) {
-        const uint16_t* xr[1] = {nullptr};
-        if (b + (lane & 15) < gr.count) {
-            const int r = gr.at(b + (lane & 15));
-            xr[0] = a.xhat ? a.xhat + (int64_t)r * a.H : a.x + (int64_t)(r / a.k) * a.H;
-        }
-        f32x4 acc[1][2] = {{f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}};
-        dot_rows<FMT, 1, 2, flight(1, 2)>(a.w1, row, c0, c1, xr, acc);
-        __syncthreads();                               // the last group's sums have been read
-        red.put(acc);
-        const int m = b + 4 * (lane >> 4) + w;
-        float gate = red.get(0, 0), up = red.get(0, 1), sig;
+    XLds<FMT> x{(lds_t*)dyn, XLds<FMT>::bytes_per_row(a.H)};
+    DotLds<FMT, WV> dot{a.w1, rows, i0, i0 + a.I};
+    for (int b = 0; b < gr.count; b += cap) {
+        const int n = min(cap, gr.count - b);
+        dot.begin(w);
+        if (b > 0) lds_barrier();                      // the last rows and sums have been read
+        x.fill(a.H, n, [&](int m) {
+            const int r = gr.at_uniform(b + m);
+            return a.xhat ? a.xhat + (int64_t)r * a.H : a.x + (int64_t)(r / a.k) * a.H;
+        });
+        lds_barrier();
+        f32x4 acc[2][1];
+        dot.run(x.p, (uint32_t)min(lane & 15, n - 1) * x.stride + (lane >> 4) * 16, acc);
+        team_put<WV>(red, acc);
+        const int m = 4 * (lane >> 4) + w;             // wave w takes the w-th row of each lane group
+        float gate = team_get<WV>(red, w), up = team_get<WV>(red, 4 + w), sig;
         if (FMT == NVFP4) {
             gate *= t1;
             up *= t1;
@@ -404,33 +595,43 @@ __global__ __launch_bounds__(64 * NW) void k_packed_fc1(PackedExpertArgs a) {
                 hb = bf16_of(q.q * s2);
             }
         }
-        if (m < gr.count) a.h[(int64_t)gr.at(m) * a.I + i0 + (lane & 15)] = hb;
+        if (m < n) a.h[(int64_t)gr.at(b + m) * a.I + i0 + (lane & 15)] = hb;
     }
 }
 
-// fc2 of one group of rows: y_r in fp32, one row per routed row
+// fc2 of one group of rows: y_r in fp32, one row per routed row; 32 columns of
+// y per pair of waves
 template <int FMT>
-__global__ __launch_bounds__(64 * NW) void k_packed_fc2(PackedExpertArgs a) {
-    __shared__ Reduce<1, 1> red;
+__global__ __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(4))) void k_packed_fc2(PackedExpertArgs a,
+                                                                                                int cap) {
+    constexpr int KW = 2;
+    extern __shared__ __attribute__((aligned(16))) char dyn[];
+    __shared__ float red[WV][8][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int r0 = blockIdx.y, n0 = blockIdx.x * 16;
+    const int r0 = blockIdx.y, n0 = (blockIdx.x * (WV / KW) + w / KW) * 32;      // H is a multiple of 128
     const Group gr(a, r0);
     if (gr.count == 0) return;
     const int e = clamp_id(sload(a.ids, r0), a.E);
-    int c0, c1;
-    wave_chunks(a.I, w, &c0, &c1);
-    const int64_t row[1] = {(int64_t)e * a.H + n0 + (lane & 15)};
+    const Rows<FMT> rows(a.w2, (int64_t)e * a.H, a.H);
     const float t2 = FMT == NVFP4 ? sload(a.w2.tscale, e) : 1.0f;
-    for (int b = 0; b < gr.count; b += 16) {
-        const uint16_t* xr[1] = {
-            b + (lane & 15) < gr.count ? a.h + (int64_t)gr.at(b + (lane & 15)) * a.I : nullptr};
-        f32x4 acc[1][1] = {{f32x4{0, 0, 0, 0}}};
-        dot_rows<FMT, 1, 1, flight(1, 1)>(a.w2, row, c0, c1, xr, acc);
-        __syncthreads();
-        red.put(acc);
-        const int m = b + 4 * (lane >> 4) + w;
-        const float s = red.get(0, 0);
-        if (m < gr.count) a.yr[(int64_t)gr.at(m) * a.H + n0 + (lane & 15)] = FMT == NVFP4 ? s * t2 : s;
+    XLds<FMT> x{(lds_t*)dyn, XLds<FMT>::bytes_per_row(a.I)};
+    DotLds<FMT, KW> dot{a.w2, rows, n0, n0 + 16};
+    for (int b = 0; b < gr.count; b += cap) {
+        const int n = min(cap, gr.count - b);
+        dot.begin(w % KW);
+        if (b > 0) lds_barrier();
+        x.fill(a.I, n, [&](int m) { return a.h + (int64_t)gr.at_uniform(b + m) * a.I; });
+        lds_barrier();
+        f32x4 acc[2][1];
+        dot.run(x.p, (uint32_t)min(lane & 15, n - 1) * x.stride + (lane >> 4) * 16, acc);
+        team_put<KW>(red, acc);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = j * KW + w % KW, m = 4 * (lane >> 4) + (i & 3);
+            const float s = team_get<KW>(red, i);
+            if (m < n)
+                a.yr[(int64_t)gr.at(b + m) * a.H + n0 + 16 * (i >> 2) + (lane & 15)] = FMT == NVFP4 ? s * t2 : s;
+        }
     }
 }
 
@@ -443,29 +644,48 @@ __global__ __launch_bounds__(256) void k_packed_combine(PackedExpertArgs a) {
     a.y[(int64_t)t * a.H + c] = bf16_of(s);
 }
 
-template <int FMT>
+// Up to 2048 columns four waves split a tile's columns, above eight do (12289 x
+// 8192, 13 rows, NVFP4: 22 us against 27; 49152 x 2048: 22 against 19); by the
+// columns only, so that a row's bits do not depend on the other rows.  Four
+// tiles per block reuse x where that leaves blocks for most CUs, else one
+// (2048 x 2048, one row: 4.2 us against 6.3).
+template <int FMT, int KW>
 hipError_t run_matvec(const MatvecArgs& a, hipStream_t st) {
-    const unsigned nb = (unsigned)((a.N + 15) / 16);
-    if (a.which) {
-        hipLaunchKernelGGL(k_matvec_which<FMT>, dim3(nb, (unsigned)a.M), dim3(64 * NW), 0, st, a);
-    } else if (a.M <= 16) {
-        hipLaunchKernelGGL((k_matvec<FMT, 1, 1>), dim3(nb, 1), dim3(64 * NW), 0, st, a);
-    } else if (a.M <= 32) {
-        hipLaunchKernelGGL((k_matvec<FMT, 2, 1>), dim3(nb, 1), dim3(64 * NW), 0, st, a);
-    } else {
-        hipLaunchKernelGGL((k_matvec<FMT, 4, 1>), dim3(nb, (unsigned)((a.M + 63) / 64)), dim3(64 * NW), 0, st, a);
-    }
+    const unsigned tiles = (unsigned)((a.N + 15) / 16);
+    if (a.which)
+        hipLaunchKernelGGL((k_matvec_which<FMT, KW>), dim3(tiles, (unsigned)a.M), dim3(64 * KW), 0, st, a);
+    else if (a.M > 16)
+        hipLaunchKernelGGL((k_matvec<FMT, 2, 2, KW>), dim3((tiles + 1) / 2, (unsigned)((a.M + 31) / 32)), dim3(64 * KW),
+                           0, st, a);
+    else if (tiles >= 768)
+        hipLaunchKernelGGL((k_matvec<FMT, 1, 4, KW>), dim3((tiles + 3) / 4), dim3(64 * KW), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_matvec<FMT, 1, 1, KW>), dim3(tiles), dim3(64 * KW), 0, st, a);
     return hipGetLastError();
 }
+template <int FMT>
+hipError_t run_matvec(const MatvecArgs& a, hipStream_t st) {
+    return a.w.K > 2048 ? run_matvec<FMT, 8>(a, st) : run_matvec<FMT, 4>(a, st);
+}
 
+// Rows of x a block keeps in LDS at a time: as many as a group can have, up to
+// 16 and to 32 KB (four blocks to a CU).
+int lds_rows(int K, int T) {
+    const int fit = 32768 / (K * 2 + 16), most = T < 16 ? T : 16;
+    return fit < 1 ? 1 : fit < most ? fit : most;
+}
 template <int FMT>
 hipError_t run_fc1(const PackedExpertArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL(k_packed_fc1<FMT>, dim3((unsigned)(a.I / 16), (unsigned)a.R), dim3(64 * NW), 0, st, a);
+    const int cap = lds_rows(a.H, a.R / a.k);
+    hipLaunchKernelGGL(k_packed_fc1<FMT>, dim3((unsigned)(a.I / 16), (unsigned)a.R), dim3(64 * WV),
+                       (size_t)cap * (a.H * 2 + 16), st, a, cap);
     return hipGetLastError();
 }
 template <int FMT>
 hipError_t run_fc2(const PackedExpertArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL(k_packed_fc2<FMT>, dim3((unsigned)(a.H / 16), (unsigned)a.R), dim3(64 * NW), 0, st, a);
+    const int cap = lds_rows(a.I, a.R / a.k);
+    hipLaunchKernelGGL(k_packed_fc2<FMT>, dim3((unsigned)(a.H / 64), (unsigned)a.R), dim3(64 * WV),
+                       (size_t)cap * (a.I * 2 + 16), st, a, cap);
     return hipGetLastError();
 }
 
