@@ -92,6 +92,7 @@ __device__ __forceinline__ void transpose4(u32x4& w) {
     w.w = d[1];
 }
 
+constexpr int FC2_KW = 2;                 // waves that split fc2's columns
 constexpr int WV = 4;                     // waves of a block of the expert layer
 constexpr int XC = 4;                     // chunks of a slab: one per lane group in the scales' load
 
@@ -547,8 +548,8 @@ __device__ __forceinline__ float team_get(float (*red)[8][64], int i) {
 // LDS.  The tile of h goes through the second activation quantiser on the way
 // (a 16-block of NVFP4 is the tile's row).
 template <int FMT>
-__global__ __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(4))) void k_packed_fc1(PackedExpertArgs a,
-                                                                                                int cap) {
+__global__ __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(FMT == INT_NARROW ? 3 : 4))) void k_packed_fc1(
+    PackedExpertArgs a, int cap) {
     extern __shared__ __attribute__((aligned(16))) char dyn[];
     __shared__ float red[WV][8][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -602,9 +603,9 @@ __global__ __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(4))) vo
 // fc2 of one group of rows: y_r in fp32, one row per routed row; 32 columns of
 // y per pair of waves
 template <int FMT>
-__global__ __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(4))) void k_packed_fc2(PackedExpertArgs a,
-                                                                                                int cap) {
-    constexpr int KW = 2;
+__global__ __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(FMT == INT_NARROW ? 3 : 4))) void k_packed_fc2(
+    PackedExpertArgs a, int cap) {
+    constexpr int KW = FC2_KW;
     extern __shared__ __attribute__((aligned(16))) char dyn[];
     __shared__ float red[WV][8][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -635,7 +636,9 @@ __global__ __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(4))) vo
     }
 }
 
-// y[t] = sum over the slots of w y_r, ascending
+// y[t] = sum over the slots of w y_r, ascending.  (A launch less for one token,
+// with a token's slots side by side in blocks of sixteen waves, took 20.9 us
+// where the two take 17.8.)
 __global__ __launch_bounds__(256) void k_packed_combine(PackedExpertArgs a) {
     const int t = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
     if (c >= a.H) return;
