@@ -295,47 +295,61 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
 #pragma unroll
     for (int it = 0; it < NIT; ++it) {
         const int row = (it * NW + wave) * RPI + lane / CH, c = lane % CH;
-        __builtin_amdgcn_raw_buffer_store_b128(cv[it], prs, (uint32_t)row * (uint32_t)a.vc * 2u + c * 16, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(cv[it], prs, (uint32_t)row * (uint32_t)a.vc * 2u + c * 16, 0, 2);
     }
 }
 
 // ---------------------------------------------------------------- merge ---
-// 16 tokens per block, 64 threads per token taking every 64th strip; maxima
-// and sums combine in a fixed tree (lanes 16 apart, then the waves in order).
-// 64 tokens per block with 16 threads each left short batches on few CUs with
-// long chains of loads: 86 us against 7 for 333 tokens of 32003 entries.
+// TOK tokens per block, 1024 / TOK threads per token taking every so many-th
+// strip; sums and maxima combine in a fixed tree.  One pass over the strips
+// where all have the tokens' frames, as nearly always; else a second one in
+// the new frames.  16 tokens (128-byte pieces of the strips' rows) where they
+// fill the card, else 4 with the shorter chains of loads (333 tokens of 32003
+// entries: 14 us with 4, 28 with 16; 2048 of 151936: 36 and 21; 16384, a piece
+// of 15360: 41 and 20).
+template <int TOK>
 __global__ __launch_bounds__(1024) void k_head_merge(HeadArgs a) {
-    __shared__ float red_f[16][16], red_s[16][16];
-    const int tok = threadIdx.x & 15, sl = threadIdx.x >> 4, w = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * 16 + tok;
+    constexpr int PER = 1024 / TOK;
+    __shared__ float red_f[16][TOK], red_s[16][TOK];
+    const int tok = threadIdx.x % TOK, sl = threadIdx.x / TOK, w = threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * TOK + tok, tc = min(t, a.T - 1);
     const bool live = t < a.T;
     const int strips = a.vc / 64;
-    const float f0 = live ? a.frame[t] : 0.0f;
-    float f = f0;
-    if (live) {
-#pragma unroll 4
-        for (int s = sl; s < strips; s += 64) {
-            const float2 v = a.stats[(int64_t)s * a.T + t];
-            if (v.x != 0.0f) f = fmaxf(f, v.y);
-        }
-    }
-    f = fmaxf(f, __shfl_xor(f, 16));
-    f = fmaxf(f, __shfl_xor(f, 32));
-    if ((threadIdx.x & 63) < 16) red_f[w][tok] = f;
-    __syncthreads();
+    const float f0 = a.frame[tc];
+    auto over_token = [&](float v, bool max, float (*red)[TOK]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f = fmaxf(f, red_f[i][tok]);
-    float sum = 0.0f;
-    if (live) {
-#pragma unroll 4
-        for (int s = sl; s < strips; s += 64) {
-            const float2 v = a.stats[(int64_t)s * a.T + t];
+        for (int m = TOK; m < 64; m <<= 1) {
+            const float o = __shfl_xor(v, m);
+            v = max ? fmaxf(v, o) : v + o;
+        }
+        if ((threadIdx.x & 63) < TOK) red[w][tok] = v;
+        __syncthreads();
+        v = red[0][tok];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) v = max ? fmaxf(v, red[i][tok]) : v + red[i][tok];
+        return v;
+    };
+    float f = f0, sum = 0.0f;
+    bool moved = false;
+#pragma unroll 8
+    for (int s = sl; s < strips; s += PER) {
+        const float2 v = a.stats[(int64_t)s * a.T + tc];
+        const bool other = v.y != f0 && v.x != 0.0f;
+        moved |= other;
+        f = other ? fmaxf(f, v.y) : f;
+        sum += v.y == f0 ? v.x : 0.0f;
+    }
+    if (__syncthreads_or(moved && live)) {             // frames of their own: bring all to the common one
+        f = over_token(f, true, red_f);
+        sum = 0.0f;
+        for (int s = sl; s < strips; s += PER) {
+            const float2 v = a.stats[(int64_t)s * a.T + tc];
             if (v.y == f) {
                 sum += v.x;
-            } else if (v.x != 0.0f) {                  // a frame of its own: to the common one
+            } else if (v.x != 0.0f) {
                 const float k = exp2_hw(v.y - f);
                 sum += v.x * k;
-                if (a.p) {
+                if (a.p && live) {
                     uint4* p = reinterpret_cast<uint4*>(a.p + t * a.vc + s * 64);
                     for (int i = 0; i < 8; ++i) {
                         float e[8];
@@ -348,23 +362,17 @@ __global__ __launch_bounds__(1024) void k_head_merge(HeadArgs a) {
             }
         }
     }
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    if ((threadIdx.x & 63) < 16) red_s[w][tok] = sum;
-    __syncthreads();                                   // also: the strips are in the common frame
-    if (threadIdx.x < 16 && live) {
+    sum = over_token(sum, false, red_s);               // its barrier: the strips are in the common frame
+    if (threadIdx.x < TOK && live) {
         const float step = f0 == f ? 1.0f : exp2_hw(f0 - f);
-        sum = a.sum[t] == 0.0f ? 0.0f : a.sum[t] * step;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum += red_s[i][tok];
-        a.sum[t] = sum;
+        a.sum[t] = (a.sum[t] == 0.0f ? 0.0f : a.sum[t] * step) + sum;
         a.frame[t] = f;
         a.step[t] = step;
     }
     if (a.p) {
         const int slots = a.k + 1;
-        const int64_t t0 = (int64_t)blockIdx.x * 16;
-        const int n = (int)min((int64_t)16, a.T - t0) * slots;
+        const int64_t t0 = (int64_t)blockIdx.x * TOK;
+        const int n = (int)min((int64_t)TOK, a.T - t0) * slots;
         for (int i = threadIdx.x; i < n; i += 1024) {
             const int64_t r = t0 + i / slots;
             const int j = i % slots;
@@ -533,7 +541,8 @@ __global__ __launch_bounds__(1024) void k_head_mean(HeadArgs a, float* loss) {
 // at most 640 MB (and a piece of the weight 2 GB, the reach of a buffer
 // resource's offsets); of the numbers of equal pieces from the least on, up to
 // half as many again, the one whose first products fill the 256 CUs in the
-// fewest rounds of tiles.  Where the gradient's tiles are fewer than the CUs
+// fewest rounds of tiles.  (16384 tokens of 151936 entries: 18.0 ms; with 1300
+// MB 17.6, with 2600 17.4, half of what the logits take.)  Where the gradient's tiles are fewer than the CUs
 // the piece is split until they are about as many.
 HeadPlan head_plan(int64_t T, int64_t H, int64_t V) {
     HeadPlan p{};
@@ -576,7 +585,8 @@ hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t 
             const unsigned g1 = (unsigned)((mt * (pl.vc / BN) + 7) / 8 * 8);
             if (a.grad) hipLaunchKernelGGL(k_head_probs<true>, dim3(g1), dim3(512), 0, st, a);
             else hipLaunchKernelGGL(k_head_probs<false>, dim3(g1), dim3(512), 0, st, a);
-            hipLaunchKernelGGL(k_head_merge, dim3((unsigned)((a.T + 15) / 16)), dim3(1024), 0, st, a);
+            if (a.T >= 1024) hipLaunchKernelGGL(k_head_merge<16>, dim3((unsigned)((a.T + 15) / 16)), dim3(1024), 0, st, a);
+            else hipLaunchKernelGGL(k_head_merge<4>, dim3((unsigned)((a.T + 3) / 4)), dim3(1024), 0, st, a);
             if (a.grad)
                 hipLaunchKernelGGL(k_head_grad, dim3((unsigned)((mt * nt * pl.splits + 7) / 8 * 8)), dim3(512), 0, st,
                                    a);

@@ -13,7 +13,8 @@ EPS = 1e-6
 
 # one wave per row (with 1, 2 and 4 vectors a lane, ragged ends), one block per
 # row of every kind, the longest row, a single element vector
-SHAPES = [(1, 8), (1, 2048), (3, 1000), (1025, 64), (1030, 520), (1027, 1000), (2050, 2048), (77, 2056), (5, 8192),
+SHAPES = [(1, 8), (1, 2048), (3, 1000), (1025, 64), (1030, 520), (1027, 1000), (2047, 2048), (2049, 64), (2051, 520),
+          (2053, 1000), (2050, 2048), (77, 2056), (5, 8192),
           (3, 16384), (2, 65536)]
 
 
