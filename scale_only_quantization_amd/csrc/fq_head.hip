@@ -26,6 +26,8 @@
 // computed once, never stored, and rounded to bf16 only as a probability
 // beside fp32 sums (P's rounding, 2^-9 of each term, averages out over the
 // product's sum).  The two products carry the time.
+#include <algorithm>
+
 #include "fq_mfma.h"
 #include "fq_ops.h"
 
@@ -40,100 +42,118 @@ __device__ __forceinline__ float bf_from_bits(uint16_t b) { return __uint_as_flo
 
 constexpr int BM = 256, BN = 256, BK = 64, S = 2, NW = 8, WTM = 4, WTN = 2, WVN = 4;
 constexpr int KS = BK / 16;
+constexpr int CUS = 256;
 typedef KTile<BM, BK, NW> KT;             // a reduction-contiguous operand
 typedef MNTile<BN, BK, NW> MT;            // the weight as [vocabulary, hidden], reduced over the vocabulary
 constexpr int SMEM = S * (KT::BYTES + KT::BYTES);
 static_assert(KT::BYTES == MT::BYTES, "both products use one LDS layout");
-static_assert(BM * BN * 2 <= SMEM, "the output tile fits the stages");
 
-// acc = A B^T over nk steps of 64 on eight waves in two groups of four that
-// alternate between a memory phase (fragments of one step into registers, the
-// loads of a later step) and a compute phase (that step's MFMAs), one phase
-// apart: on each SIMD one wave issues MFMAs while the other reads.  Group 0
-// issues the loads of step k + 1 in its memory phase of step k, into the stage
-// both groups finished reading in the two phases before; group 1 issues those
-// of step k + 2 after its own reads of step k, which group 0 made one phase
-// earlier.  Each group waits for its loads of step k + 1 before the barrier
-// that opens group 0's memory phase of that step.  nti: this wave's 32-row
-// sub-tiles that hold rows; tail0 runs on group 0 while group 1 computes its
-// last step (LDS is free then).
-template <class AT, class BT, typename F>
-__device__ __forceinline__ void product(AT& la, BT& lb, f32x16 (&acc)[WTM][WTN], lds_t* smem, int nk, int nti,
-                                        F&& tail0) {
+// acc = A B^T, nk steps of 64 for each of n tiles (nk even where n > 1), on eight
+// waves in two groups of four that alternate between a memory phase (fragments
+// of one step into registers, the loads of a later step) and a compute phase
+// (that step's MFMAs), one phase apart: on each SIMD one wave issues MFMAs while
+// the other reads.  Group 0 issues its loads of step k + 1 as its memory phase of
+// step k opens, into the stage both groups finished reading in the two phases
+// before.  Group 1 issues its loads of step k + 2 in its memory phase of step k,
+// behind a barrier in the middle of group 0's compute phase: its other waves may
+// still be reading that stage before it (without a measurable cost there; in
+// group 1's own compute phase the loads cost a tenth).  Each group waits for its
+// loads of step k + 1 before the barrier that opens group 0's memory phase of
+// that step.  The steps run on from tile to tile: next(i) points la and lb at
+// tile i before a group's first load of it, and epi(i), which uses no stage,
+// opens the group's next memory phase, while the other group computes.  Wave row
+// wm (the group) has the rows from wm wr on, nti(i) sub-tiles of 32 of them.
+template <class AT, class BT, typename N, typename R, typename E>
+__device__ __forceinline__ void product(AT& la, BT& lb, f32x16 (&acc)[WTM][WTN], lds_t* smem, int n, int nk, int wr,
+                                        N&& next, R&& nti, E&& epi) {
     constexpr int LOADS = AT::PER_WAVE + BT::PER_WAVE;
     const int w = wave_id(), grp = w >> 2;
     typename AT::template Frags<WTM> fa;
     typename BT::template Frags<WTN> fb;
-    fa.prep((w / WVN) * 32 * WTM);
+    fa.prep((w / WVN) * wr);
     fb.prep((w % WVN) * 32 * WTN);
     bf16x8 af[KS][WTM], bfr[KS][WTN];
-    auto issue = [&](int kt) {
-        la.issue(smem + (kt % S) * AT::BYTES, kt * BK);
-        lb.issue(smem + S * AT::BYTES + (kt % S) * BT::BYTES, kt * BK);
+    // loads of step kt of tile i, or of step kt - nk of the tile after it; false if there is none
+    auto issue = [&](int i, int kt, int st) {
+        if (kt >= nk) {
+            if (i + 1 >= n) return false;
+            if (kt == nk) next(i + 1);
+            kt -= nk;
+        }
+        la.issue(smem + st * AT::BYTES, kt * BK);
+        lb.issue(smem + S * AT::BYTES + st * BT::BYTES, kt * BK);
+        return true;
     };
     auto bar = [&]() {
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("s_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
-#pragma unroll
-    for (int a = 0; a < WTM; ++a)
-#pragma unroll
-        for (int b = 0; b < WTN; ++b)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.0f;
-    const int last = grp == 0 ? S - 2 : S - 1;
-#pragma unroll
-    for (int p = 0; p < S; ++p)
-        if (p <= last && p < nk) issue(p);
-    wait_steps<LOADS>(min(last, nk - 1));
+    if (nk > 0) {
+        next(0);
+        issue(0, 0, 0);
+    }
+    vm_wait<0>();
     bar();
+    if (nk > 0) issue(0, 1, 1);
     if (grp == 1) bar();
-    auto phases = [&](int kt, int st, auto part_c) {
-        constexpr bool PART = decltype(part_c)::value;
-        if (grp == 0 && kt + S - 1 < nk) issue(kt + S - 1);
+    auto phases = [&](int i, int kt, int st, auto n_c) {
+        constexpr int NT = decltype(n_c)::value;
         const lds_t* sa = smem + st * AT::BYTES;
         const lds_t* sb = smem + S * AT::BYTES + st * BT::BYTES;
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
 #pragma unroll
-            for (int t = 0; t < WTM; ++t)
-                if (!PART || t < nti) af[kk][t] = fa.get(sa, t, kk);
-            if (!PART || nti > 0)
+            for (int t = 0; t < NT; ++t) af[kk][t] = fa.get(sa, t, kk);
+            if (NT > 0)
 #pragma unroll
                 for (int t = 0; t < WTN; ++t) bfr[kk][t] = fb.get(sb, t, kk);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         if (grp == 1) {
-            if (kt + S < nk) issue(kt + S);
-            wait_steps<LOADS>(min(S - 1, nk - 2 - kt));
+            bar();
+            const bool more = issue(i, kt + 2, st);
+            if (kt > 0 || i == 0) wait_steps<LOADS>(more ? 1 : 0);
         }
         bar();
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk)
+        for (int kk = 0; kk < KS; ++kk) {
 #pragma unroll
-            for (int ti = 0; ti < WTM; ++ti)
-                if (!PART || ti < nti)
+            for (int ti = 0; ti < NT; ++ti)
 #pragma unroll
-                    for (int tj = 0; tj < WTN; ++tj)
-                        acc[ti][tj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bfr[kk][tj], af[kk][ti], acc[ti][tj], 0,
-                                                                              0, 0);
-        if (grp == 0) wait_steps<LOADS>(min(S - 2, nk - 2 - kt));
+                for (int tj = 0; tj < WTN; ++tj)
+                    acc[ti][tj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bfr[kk][tj], af[kk][ti], acc[ti][tj], 0, 0, 0);
+            if (kk == 1 && grp == 0) bar();
+        }
+        if (grp == 0) vm_wait<0>();
         bar();
+        if (grp == 0) issue(i, kt + 2, st);
     };
-    auto steps = [&](auto part_c) {
+    auto steps = [&](int i, auto n_c) {
         for (int kt = 0; kt < nk; kt += S) {
 #pragma unroll
             for (int u = 0; u < S; ++u)
-                if (kt + u < nk) phases(kt + u, u, part_c);
+                if (kt + u < nk) phases(i, kt + u, u, n_c);
         }
     };
-    if (nti >= WTM) steps(std::false_type{});
-    else steps(std::true_type{});
-    if (grp == 0) {
-        tail0();
-        bar();
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+#pragma unroll
+        for (int a = 0; a < WTM; ++a)
+#pragma unroll
+            for (int b = 0; b < WTN; ++b)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.0f;
+        const int sub = nti(i);
+        if (sub == 4) steps(i, std::integral_constant<int, 4>{});
+        else if (sub == 3) steps(i, std::integral_constant<int, 3>{});
+        else if (sub == 2) steps(i, std::integral_constant<int, 2>{});
+        else if (sub == 1) steps(i, std::integral_constant<int, 1>{});
+        else steps(i, std::integral_constant<int, 0>{});
+        if (grp == 1) vm_wait<0>();                    // step 1 of the next tile, before the epilogue's stores
+        epi(i);
     }
+    if (grp == 0) bar();
 }
 
 // Tile t of mt x nt in the order that shares operands inside an XCD's L2:
@@ -203,39 +223,73 @@ __global__ __launch_bounds__(256) void k_head_sparse(HeadArgs a) {
 }
 
 // ---------------------------------------------------------------- probs ---
+// One block per CU (or fewer) takes tiles in turn; each XCD has a contiguous run
+// of them.  P goes from the registers to memory: the four stores of a wave's 64
+// columns fill whole 128-byte lines one after the other.  (A piece of 15360
+// entries for 16384 tokens: 815 us, 1265 TFLOP/s; a block per tile with P through
+// the stages 864; P through LDS of its own 828, past the caches then or not.)
 template <bool GRAD>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k_head_probs(HeadArgs a) {
-    __shared__ __attribute__((aligned(1024))) char smem_raw[SMEM];
+    __shared__ __attribute__((aligned(1024))) char smem_raw[SMEM + 2 * BM * 4];
     lds_t* smem = (lds_t*)smem_raw;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_id();
     const int wm = wave / WVN, wn = wave % WVN;
-    const int mt = (int)((a.T + BM - 1) / BM), nt = a.vc / BN;
-    const int tile = xcd_tile(blockIdx.x, gridDim.x, mt * nt);
-    if (tile < 0) return;
-    int tm, tn;
-    tile_of(tile, mt, nt, &tm, &tn);
-    const int64_t m0 = (int64_t)tm * BM;
-    const int rows = (int)min((int64_t)BM, a.T - m0);
-    const int64_t v0 = a.c0 + (int64_t)tn * BN;               // first vocabulary entry of the tile
-    const int cols = (int)min((int64_t)BN, a.V - v0);         // may be <= 0 in the last piece's padding
+    const int mt = (int)((a.T + a.bm - 1) / a.bm), nt = a.vc / BN;
+    const int wr = (a.bm / 2 + 31) / 32 * 32;                 // the first wave row's rows; the second has the rest
+    const int run = (mt * nt + 7) / 8, per = gridDim.x / 8;   // tiles of an XCD, its blocks
+    const int t0 = (blockIdx.x & 7) * run + (blockIdx.x >> 3), t1 = min(mt * nt, ((int)(blockIdx.x & 7) + 1) * run);
+    if (t0 >= t1) return;
+    auto at = [&](int i, int64_t* m0, int* tn) {              // tile i's first row, its rows, its column tile
+        int tm;
+        tile_of(t0 + i * per, mt, nt, &tm, tn);
+        *m0 = (int64_t)tm * a.bm;
+        return (int)min((int64_t)a.bm, a.T - *m0);
+    };
     KT la, lb;
-    la.init(make_rsrc_words(a.h + m0 * a.H, (int64_t)rows * a.H * 2), a.H);
-    lb.init(make_rsrc_words(a.w + (cols > 0 ? v0 : 0) * a.H, (int64_t)cols * a.H * 2), a.H);
+    la.init(u32x4{}, a.H);
+    lb.init(u32x4{}, a.H);
     f32x16 acc[WTM][WTN];
-    float frame[WTM];
-#pragma unroll
-    for (int ti = 0; ti < WTM; ++ti) {
-        const int64_t t = m0 + wm * 128 + ti * 32 + (lane & 31);
-        frame[ti] = t < a.T ? a.frame[t] : 0.0f;
-    }
-    constexpr int RB = BN * 2, CH = BN / 8;
+    auto next = [&](int i) {
+        int64_t m0;
+        int tn;
+        const int rows = at(i, &m0, &tn);
+        const int64_t v0 = a.c0 + (int64_t)tn * BN;           // first vocabulary entry of the tile
+        const int cols = (int)min((int64_t)BN, a.V - v0);     // may be <= 0 in the last piece's padding
+        la.rs = make_rsrc_words(a.h + m0 * a.H, (int64_t)rows * a.H * 2);
+        lb.rs = make_rsrc_words(a.w + (cols > 0 ? v0 : 0) * a.H, (int64_t)cols * a.H * 2);
+        // the tile's frames, ahead of its first step, in the other buffer than
+        // the tile's before
+        if (wave == 0) {
+            const uint32_t voff[1] = {(uint32_t)lane * 16};
+            stage_loads<1, 0>(make_rsrc_words(a.frame + m0, (int64_t)(rows + 3) / 4 * 16),
+                              smem + SMEM + (i & 1) * BM * 4, voff, 0);
+        }
+    };
+    auto nti = [&](int i) {
+        int64_t m0;
+        int tn;
+        const int rows = at(i, &m0, &tn);
+        return wm == 0 ? (min(rows, wr) + 31) / 32 : (max(rows - wr, 0) + 31) / 32;
+    };
     // lane holds z of token lane%32 and columns 8 (v/4) + 4 (lane/32) + v%4 of
     // each 32 x 32 sub-tile: a token's 64 columns of this wave are its own 32
     // and lane ^ 32's
-    auto epilogue = [&]() {
+    auto epilogue = [&](int i) {
+        int64_t m0;
+        int tn;
+        const int rows = at(i, &m0, &tn), sub = nti(i);
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));                        // what follows from it is not held through the steps
+        const int cols = (int)min((int64_t)BN, a.V - a.c0 - (int64_t)tn * BN);
+        const __amdgpu_buffer_rsrc_t prs = make_rsrc(GRAD ? a.p + m0 * a.vc + (int64_t)tn * BN : nullptr,
+                                                     (int64_t)(rows - 1) * a.vc * 2 + BN * 2);
+        const __attribute__((address_space(3))) float* frames =
+            reinterpret_cast<const __attribute__((address_space(3))) float*>(smem + SMEM + (i & 1) * BM * 4);
 #pragma unroll
         for (int ti = 0; ti < WTM; ++ti) {
-            const int row = wm * 128 + ti * 32 + (lane & 31);
+            if (ti >= sub) break;
+            const int row = wm * wr + ti * 32 + (lane & 31);
+            const float frame = frames[row];
             if (cols < BN) {
 #pragma unroll
                 for (int tj = 0; tj < WTN; ++tj)
@@ -250,7 +304,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
 #pragma unroll
                 for (int v = 0; v < 16; ++v) m = fmaxf(m, acc[ti][tj][v]);
             m = fmaxf(m, xor32(m)) * LOG2E;
-            float f = m <= frame[ti] + FRAME_SLACK ? frame[ti] : ceilf(m);
+            float f = m <= frame + FRAME_SLACK ? frame : ceilf(m);
             if (f == -INFINITY) f = 0.0f;                     // nothing in the strip: P = 0
             float s = 0.0f;
 #pragma unroll
@@ -268,35 +322,23 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
 #pragma unroll
                 for (int tj = 0; tj < WTN; ++tj)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int col = wn * 64 + tj * 32 + 8 * q + 4 * (lane >> 5);
-                        const int off = row * RB + (((col >> 3) ^ (row & 15)) << 4) + (col & 7) * 2;
-                        *reinterpret_cast<__attribute__((address_space(3))) uint64_t*>(smem + off) =
-                            (uint64_t)pack_bf16(acc[ti][tj][4 * q], acc[ti][tj][4 * q + 1]) |
-                            ((uint64_t)pack_bf16(acc[ti][tj][4 * q + 2], acc[ti][tj][4 * q + 3]) << 32);
+                    for (int q = 0; q < 4; q += 2) {
+                        // the halves trade, so that a lane has 8 columns in a row
+                        u32x4 c;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const auto r = __builtin_amdgcn_permlane32_swap(
+                                pack_bf16(acc[ti][tj][4 * q + 2 * j], acc[ti][tj][4 * q + 2 * j + 1]),
+                                pack_bf16(acc[ti][tj][4 * q + 4 + 2 * j], acc[ti][tj][4 * q + 5 + 2 * j]), false, false);
+                            c[j] = r[0];
+                            c[2 + j] = r[1];
+                        }
+                        const int col = wn * 64 + tj * 32 + 8 * (q + (lane >> 5));
+                        __builtin_amdgcn_raw_buffer_store_b128(c, prs, (uint32_t)row * (uint32_t)a.vc * 2u + col * 2, 0, 0);
                     }
         }
     };
-    const int nti = min(max((rows - wm * 128 + 31) / 32, 0), WTM);
-    product(la, lb, acc, smem, a.H / BK, nti, epilogue);
-    if (wave_id() >= 4) epilogue();
-    if (!GRAD) return;
-    __syncthreads();
-    constexpr int RPI = 64 / CH, NIT = BM / (RPI * NW);
-    u32x4 cv[NIT];
-#pragma unroll
-    for (int it = 0; it < NIT; ++it) {
-        const int row = (it * NW + wave) * RPI + lane / CH, c = lane % CH;
-        cv[it] = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(smem + row * RB +
-                                                                                   ((c ^ (row & 15)) << 4));
-    }
-    const __amdgpu_buffer_rsrc_t prs =
-        make_rsrc(a.p + m0 * a.vc + (int64_t)tn * BN, (int64_t)(rows - 1) * a.vc * 2 + BN * 2);
-#pragma unroll
-    for (int it = 0; it < NIT; ++it) {
-        const int row = (it * NW + wave) * RPI + lane / CH, c = lane % CH;
-        __builtin_amdgcn_raw_buffer_store_b128(cv[it], prs, (uint32_t)row * (uint32_t)a.vc * 2u + c * 16, 0, 2);
-    }
+    product(la, lb, acc, smem, (t1 - t0 + per - 1) / per, a.H / BK, wr, next, nti, epilogue);
 }
 
 // ---------------------------------------------------------------- merge ---
@@ -329,6 +371,17 @@ __global__ __launch_bounds__(1024) void k_head_merge(HeadArgs a) {
         for (int i = 1; i < 16; ++i) v = max ? fmaxf(v, red[i][tok]) : v + red[i][tok];
         return v;
     };
+    // read ahead of the strips: what the tail needs
+    const int slots = a.k + 1;
+    const int64_t t0 = (int64_t)blockIdx.x * TOK;
+    const int n = a.p ? (int)min((int64_t)TOK, a.T - t0) * slots : 0;
+    auto id_of = [&](int i) {
+        const int64_t r = t0 + i / slots;
+        const int j = i % slots;
+        return j < a.k ? a.top_i[r * a.k + j] : (a.labels ? a.labels[r] : -1);
+    };
+    const int id0 = (int)threadIdx.x < n ? id_of(threadIdx.x) : -1;
+    const float before = a.sum[tc];
     float f = f0, sum = 0.0f;
     bool moved = false;
 #pragma unroll 8
@@ -365,20 +418,13 @@ __global__ __launch_bounds__(1024) void k_head_merge(HeadArgs a) {
     sum = over_token(sum, false, red_s);               // its barrier: the strips are in the common frame
     if (threadIdx.x < TOK && live) {
         const float step = f0 == f ? 1.0f : exp2_hw(f0 - f);
-        a.sum[t] = (a.sum[t] == 0.0f ? 0.0f : a.sum[t] * step) + sum;
+        a.sum[t] = (before == 0.0f ? 0.0f : before * step) + sum;
         a.frame[t] = f;
         a.step[t] = step;
     }
-    if (a.p) {
-        const int slots = a.k + 1;
-        const int64_t t0 = (int64_t)blockIdx.x * TOK;
-        const int n = (int)min((int64_t)TOK, a.T - t0) * slots;
-        for (int i = threadIdx.x; i < n; i += 1024) {
-            const int64_t r = t0 + i / slots;
-            const int j = i % slots;
-            const int id = j < a.k ? a.top_i[r * a.k + j] : (a.labels ? a.labels[r] : -1);
-            if (id >= a.c0 && id < a.V && id - a.c0 < a.vc) a.p[r * a.vc + (id - a.c0)] = 0;
-        }
+    for (int i = threadIdx.x; i < n; i += 1024) {
+        const int id = i < 1024 ? id0 : id_of(i);
+        if (id >= a.c0 && id < a.V && id - a.c0 < a.vc) a.p[(t0 + i / slots) * a.vc + (id - a.c0)] = 0;
     }
 }
 
@@ -388,17 +434,19 @@ __global__ __launch_bounds__(1024) void k_head_merge(HeadArgs a) {
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k_head_grad(HeadArgs a) {
     __shared__ __attribute__((aligned(1024))) char smem_raw[SMEM];
     lds_t* smem = (lds_t*)smem_raw;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_id();
     const int wm = wave / WVN, wn = wave % WVN;
-    const int mt = (int)((a.T + BM - 1) / BM), nt = (a.H + BN - 1) / BN;
+    const int mt = (int)((a.T + a.bm - 1) / a.bm), nt = (a.H + BN - 1) / BN;
     int tile = xcd_tile(blockIdx.x, gridDim.x, mt * nt * a.splits);
     if (tile < 0) return;
     const int split = tile / (mt * nt);
     tile -= split * mt * nt;
     int tm, tn;
     tile_of(tile, mt, nt, &tm, &tn);
-    const int64_t m0 = (int64_t)tm * BM;
-    const int rows = (int)min((int64_t)BM, a.T - m0);
+    const int64_t m0 = (int64_t)tm * a.bm;
+    const int rows = (int)min((int64_t)a.bm, a.T - m0);
+    const int wr = (a.bm / 2 + 31) / 32 * 32;                 // the first wave row's; the second has the rest
+    const int nti = wm == 0 ? (min(rows, wr) + 31) / 32 : (max(rows - wr, 0) + 31) / 32;
     const int n0 = tn * BN;
     const int k0 = split * a.ksplit, kn = min(a.ksplit, a.vc - k0);     // multiples of 64; kn may be <= 0
     const int kv = (int)min((int64_t)kn, a.V - a.c0 - k0);              // of them inside the vocabulary
@@ -409,13 +457,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
                             kv > 0 ? ((int64_t)(kv - 1) * a.H + (a.H - n0)) * 2 : 0),
             a.H);
     f32x16 acc[WTM][WTN];
-    const int nti = min(max((rows - wm * 128 + 31) / 32, 0), WTM);
-    product(la, lb, acc, smem, max(kn, 0) / BK, nti, []() {});
+    product(la, lb, acc, smem, 1, max(kn, 0) / BK, wr, [](int) {}, [&](int) { return nti; }, [](int) {});
     float* G = a.g + (int64_t)split * a.T * a.H;
 #pragma unroll
     for (int ti = 0; ti < WTM; ++ti) {
-        const int row = wm * 128 + ti * 32 + (lane & 31);
-        if (row >= rows) continue;
+        const int row = wm * wr + ti * 32 + (lane & 31);
+        if (ti >= nti || row >= rows) continue;
         const int64_t t = m0 + row;
         const float f = a.first ? 0.0f : a.step[t];
         float* gr = G + t * a.H + n0;
@@ -442,7 +489,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
 
 // ------------------------------------------------------------------ out ---
 // A block per token: loss and coefficients by the first wave (lane j is slot
-// j, k <= 64; the label is lane 0's second slot), then 8 columns per thread.
+// j, k <= 64; the label is lane 0's second slot), then VEC columns per thread.
+template <int VEC>
 __global__ __launch_bounds__(256) void k_head_out(HeadArgs a) {
     __shared__ float s_coef[65];
     __shared__ int s_id[65];
@@ -495,29 +543,38 @@ __global__ __launch_bounds__(256) void k_head_out(HeadArgs a) {
     if (!a.grad) return;
     __syncthreads();
     const float cs = s_c;
-    for (int c = threadIdx.x; c < (a.H >> 3); c += 256) {
-        float o[8];
-        const int64_t at = t * a.H + 8 * c;
+    typedef uint32_t words __attribute__((ext_vector_type(VEC / 2)));
+    for (int c = threadIdx.x; c < a.H / VEC; c += 256) {
+        float o[VEC];
+        const int64_t at = t * a.H + VEC * c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+        for (int i = 0; i < VEC; ++i) o[i] = 0.0f;
+#pragma unroll 8
         for (int s = 0; s < a.splits; ++s) {
             const float4* g = reinterpret_cast<const float4*>(a.g + (int64_t)s * a.T * a.H + at);
-            const float4 x = g[0], y = g[1];
-            o[0] += x.x; o[1] += x.y; o[2] += x.z; o[3] += x.w;
-            o[4] += y.x; o[5] += y.y; o[6] += y.z; o[7] += y.w;
+#pragma unroll
+            for (int i = 0; i < VEC / 4; ++i) {
+                const float4 x = g[i];
+                o[4 * i] += x.x; o[4 * i + 1] += x.y; o[4 * i + 2] += x.z; o[4 * i + 3] += x.w;
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= cs;
+        for (int i = 0; i < VEC; ++i) o[i] *= cs;
 #pragma unroll 4
         for (int j = 0; j < slots; ++j) {
             const float k = s_coef[j];
             const int id = max(s_id[j], 0);              // an absent slot has k = 0
-            float x[8];
-            unpack8(reinterpret_cast<const uint4*>(a.w + (int64_t)id * a.H)[c], x);
+            const words x = reinterpret_cast<const words*>(a.w + (int64_t)id * a.H)[c];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __builtin_fmaf(k, x[i], o[i]);
+            for (int i = 0; i < VEC / 2; ++i) {
+                o[2 * i] = __builtin_fmaf(k, __uint_as_float(x[i] << 16), o[2 * i]);
+                o[2 * i + 1] = __builtin_fmaf(k, __uint_as_float(x[i] & 0xffff0000u), o[2 * i + 1]);
+            }
         }
-        reinterpret_cast<uint4*>(a.grad + at)[0] = pack8(o);
+        words r;
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) r[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
+        *reinterpret_cast<words*>(a.grad + at) = r;
     }
 }
 
@@ -542,8 +599,8 @@ __global__ __launch_bounds__(1024) void k_head_mean(HeadArgs a, float* loss) {
 // resource's offsets); of the numbers of equal pieces from the least on, up to
 // half as many again, the one whose first products fill the 256 CUs in the
 // fewest rounds of tiles.  (16384 tokens of 151936 entries: 18.0 ms; with 1300
-// MB 17.6, with 2600 17.4, half of what the logits take.)  Where the gradient's tiles are fewer than the CUs
-// the piece is split until they are about as many.
+// MB 17.6, with 2600 17.4, half of what the logits take.)  Where the gradient's
+// tiles are fewer than the CUs the piece is split until they are about as many.
 HeadPlan head_plan(int64_t T, int64_t H, int64_t V) {
     HeadPlan p{};
     const int64_t mt = (T + BM - 1) / BM, nt = (H + BN - 1) / BN;
@@ -572,7 +629,10 @@ HeadPlan head_plan(int64_t T, int64_t H, int64_t V) {
 
 hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t st) {
     if (a.T > 0) {
-        const int64_t mt = (a.T + BM - 1) / BM, nt = (a.H + BN - 1) / BN;
+        // Tiles of equally many rows, in whole sub-tiles: 333 tokens are 192 and
+        // 141, not 256 and 77, and a tile's time goes with its sub-tiles.
+        a.bm = (int)(((a.T + (a.T + BM - 1) / BM - 1) / ((a.T + BM - 1) / BM) + 31) / 32 * 32);
+        const int64_t mt = (a.T + a.bm - 1) / a.bm, nt = (a.H + BN - 1) / BN;
         a.vc = pl.vc;
         a.splits = pl.splits;
         a.ksplit = pl.ksplit;
@@ -582,7 +642,7 @@ hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t 
         for (int i = 0; i < pl.pieces; ++i) {
             a.c0 = (int64_t)i * pl.vc;
             a.first = i == 0;
-            const unsigned g1 = (unsigned)((mt * (pl.vc / BN) + 7) / 8 * 8);
+            const unsigned g1 = (unsigned)std::min<int64_t>((mt * (pl.vc / BN) + 7) / 8 * 8, a.H % (2 * BK) == 0 ? CUS : INT32_MAX);
             if (a.grad) hipLaunchKernelGGL(k_head_probs<true>, dim3(g1), dim3(512), 0, st, a);
             else hipLaunchKernelGGL(k_head_probs<false>, dim3(g1), dim3(512), 0, st, a);
             if (a.T >= 1024) hipLaunchKernelGGL(k_head_merge<16>, dim3((unsigned)((a.T + 15) / 16)), dim3(1024), 0, st, a);
@@ -593,7 +653,11 @@ hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t 
             err = hipGetLastError();
             if (err != hipSuccess) return err;
         }
-        hipLaunchKernelGGL(k_head_out, dim3((unsigned)a.T), dim3(256), 0, st, a);
+        // 4 columns a thread where the splits' sums are the most that is read,
+        // for more threads; 8 where the weight's rows are (333 tokens, 32 splits
+        // and no teacher: 9.6 us and 13.8; 2048, 4 splits and 65 rows: 111 and 96)
+        if (pl.splits > a.k + 1) hipLaunchKernelGGL(k_head_out<4>, dim3((unsigned)a.T), dim3(256), 0, st, a);
+        else hipLaunchKernelGGL(k_head_out<8>, dim3((unsigned)a.T), dim3(256), 0, st, a);
     }
     hipLaunchKernelGGL(k_head_mean, dim3(1), dim3(1024), 0, st, a, loss);
     return hipGetLastError();

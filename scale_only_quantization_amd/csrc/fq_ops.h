@@ -73,6 +73,7 @@ struct HeadArgs {
     // filled per launch
     int64_t c0;
     int vc, splits, ksplit, first;
+    int bm;                // tokens per tile of the two products, <= 256
 };
 hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t st);
 
