@@ -456,13 +456,16 @@ __global__ __launch_bounds__(64 * WVM * WVN) __attribute__((amdgpu_waves_per_eu(
     //     stage step kt-1 used, read by both groups in the two phases
     //     before), then its fragment reads of step kt; it waits for its loads
     //     of step kt+1 after its next compute phase.
-    //   group 1, memory phase of step kt: its fragment reads of step kt, then
-    //     (once they have returned) its loads of step kt+S into the same stage
-    //     (group 0 read it one phase earlier), then it waits for its loads of
-    //     step kt+1.
+    //   group 1, memory phase of step kt, three stages: the same, as step
+    //     kt-1's stage is free of readers here too.  Two stages: its fragment
+    //     reads of step kt, then, once every wave's have returned (a barrier,
+    //     which group 0 passes in the middle of its MFMAs; without it a wave's
+    //     loads could land in lines that another of the group is yet to read),
+    //     its loads of step kt+2 into the same stage, which group 0 read one
+    //     phase earlier.  It waits for its loads of step kt+1 in this phase.
     // Every load of step kt+1 has landed before the barrier that opens group
-    // 0's memory phase of step kt+1.  Prologue: group 0 has steps [0, S-2] in
-    // flight, group 1 steps [0, S-1]; pre: steps [0, pre) were issued by every
+    // 0's memory phase of step kt+1.  Prologue: steps [0, S-2] are in flight,
+    // with two stages step 1 of group 1 too; pre: steps [0, pre) were issued by every
     // wave before the call.
     // The weight gradient runs it with 32-deep steps and three stages: with
     // 64-deep steps a step's fragments (both operands read transposed) do not
@@ -482,7 +485,9 @@ __global__ __launch_bounds__(64 * WVM * WVN) __attribute__((amdgpu_waves_per_eu(
             __builtin_amdgcn_sched_barrier(0);
         };
         if (pre > 0) bar();
-        const int last = grp == 0 ? S - 2 : S - 1;
+        // three stages: one is free of readers in both groups' memory phases
+        constexpr bool FREE = S > 2;
+        const int last = FREE || grp == 0 ? S - 2 : S - 1;
         issue_steps(nk, pre, last);
         wait_steps<LOADS>(min(last, nk - 1));
         bar();
@@ -490,7 +495,7 @@ __global__ __launch_bounds__(64 * WVM * WVN) __attribute__((amdgpu_waves_per_eu(
         auto phases = [&](int kt, int st, auto part_c) {
             constexpr bool PART = decltype(part_c)::value;
             // memory phase
-            if (grp == 0 && kt + S - 1 < nk) issue(kt + S - 1);
+            if ((FREE || grp == 0) && kt + S - 1 < nk) issue(kt + S - 1);
             const lds_t* sa = smem + st * A_BYTES;
             const lds_t* sb = smem + S * A_BYTES + st * B_BYTES;
 #pragma unroll
@@ -503,14 +508,15 @@ __global__ __launch_bounds__(64 * WVM * WVN) __attribute__((amdgpu_waves_per_eu(
                     for (int t = 0; t < WTN; ++t) bfr[kk][t] = fb.get(sb, t, kk);
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            if (grp == 1) {
+            if (!FREE && grp == 1) {
+                bar();
                 if (kt + S < nk) issue(kt + S);
-                wait_steps<LOADS>(min(S - 1, nk - 2 - kt));
             }
+            if (grp == 1) wait_steps<LOADS>(min(FREE ? S - 2 : S - 1, nk - 2 - kt));
             bar();
             // compute phase
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk)
+            for (int kk = 0; kk < KS; ++kk) {
 #pragma unroll
                 for (int ti = 0; ti < WTM; ++ti)
                     if (!PART || ti < nti)
@@ -518,6 +524,8 @@ __global__ __launch_bounds__(64 * WVM * WVN) __attribute__((amdgpu_waves_per_eu(
                         for (int tj = 0; tj < WTN; ++tj)
                             acc[ti][tj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bfr[kk][tj], af[kk][ti],
                                                                                   acc[ti][tj], 0, 0, 0);
+                if (!FREE && kk == KS / 2 - 1 && grp == 0) bar();
+            }
             if (grp == 0) wait_steps<LOADS>(min(S - 2, nk - 2 - kt));
             bar();
         };
