@@ -459,9 +459,9 @@ typedef struct {
     float distill_weight;      /* weight of the top-k KL                              */
 } fq_head_desc;
 /* Bytes of device workspace (256-B aligned): with the gradient, at most about
- * 640 MB for a piece's probabilities (never the logits), fp32 sums of the
- * gradient and 8 bytes per token and 64 vocabulary entries of a piece.  0 on a
- * bad descriptor. */
+ * 640 MB (or 512 bytes a token, if that is more) for a piece's probabilities,
+ * never the logits, then fp32 sums of the gradient and 8 bytes per token and 64
+ * vocabulary entries of a piece.  0 on a bad descriptor. */
 size_t fq_head_loss_workspace_size(const fq_head_desc* d, int32_t with_grad);
 /* h: device bf16 [tokens, hidden]; w: device bf16 [vocab, hidden]; both 16-B
  *   aligned.
@@ -498,7 +498,7 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
  *   m            rows of x, 0 .. 1024.
  *   which        device int32 [m]: the matrix of each row of x; needed if batch > 1,
  *                else nullable.  A row whose entry is outside [0, batch) gets zeros.
- *   x            device bf16 [m, cols], 16-B aligned; y: device bf16 [m, rows].
+ *   x            device bf16 [m, cols], 16-B aligned; y: device bf16 [m, rows], not x.
  * Errors: FQ_E_INVALID, FQ_E_SHAPE, FQ_E_UNSUPPORTED (other formats, m > 1024),
  * FQ_E_ALIGN, FQ_E_HIP. */
 int fq_packed_matvec(const fq_qdesc* q, int64_t batch, int64_t rows, int64_t cols, const uint8_t* codes,

@@ -250,6 +250,7 @@ int fq_packed_matvec(const fq_qdesc* d, int64_t batch, int64_t rows, int64_t col
     if ((batch > 1 && m > 0 && !which) || (m > 0 && (!x || !y))) return FQ_E_INVALID;
     if (!aligned(x, 16) || !aligned(y, 2) || !aligned(which, 4)) return FQ_E_ALIGN;
     if (m == 0) return FQ_OK;
+    if (x == y) return FQ_E_INVALID;
     a.N = rows;
     a.E = (int)batch;
     a.M = (int)m;
@@ -284,6 +285,7 @@ int fq_packed_expert_fwd(const fq_layer_desc* L, const fq_packed_experts* P, con
     const PackedLayout lay = packed_layout(L, q);
     if (L->T > 0 && (!workspace || workspace_bytes < lay.total)) return FQ_E_WORKSPACE;
     if (L->T == 0) return FQ_OK;
+    if (x == y) return FQ_E_INVALID;
     char* ws = static_cast<char*>(workspace);
     a.a1 = ActQ{q.a1, P->s_a1};
     a.a2 = ActQ{q.a2, P->s_a2};

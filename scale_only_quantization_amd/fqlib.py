@@ -511,8 +511,8 @@ def packed_expert_fwd(L: LayerDesc, P: PackedExperts, x, topk_ids, topk_w, y, wo
     dev = _device_of(n, x)
     f32, bf, u8 = _F32, _BF16, _U8
     T, H, k = L.T, L.H, L.topk
-    sizes = (L.E, H, L.I, dev)
-    if P.checked != sizes:                               # the weights' shapes, once per layer
+    sizes = (L.E, H, L.I, dev, bytes(L.w1), bytes(L.w2))
+    if P.checked != sizes:                               # the weights' shapes, once per layer and formats
         E, I = L.E, L.I
         for i, (q, N, K) in enumerate(((L.w1, 2 * I, H), (L.w2, H, I))):
             c, b, s, t = P.tensors[4 * i:4 * i + 4]

@@ -276,3 +276,38 @@ def test_tensors_of_another_device_or_type_are_refused():
     with pytest.raises(F.FqError, match="buffer too small"):
         F.head_loss(d, x, T_.zeros((10, 64), dtype=T_.bfloat16, device="cuda"), T_.zeros(1, device="cuda"),
                     labels=T_.zeros(4, dtype=T_.int32, device="cuda"), workspace=T_.zeros(64, dtype=T_.uint8, device="cuda"))
+
+
+def test_gradient_over_the_hidden_states():
+    F, T_ = _F(), torch()
+    h = T_.randn((70, 128), device="cuda").to(T_.bfloat16)
+    w = T_.randn((600, 128), device="cuda").to(T_.bfloat16)
+    lab = T_.randint(0, 600, (70,), device="cuda", dtype=T_.int32)
+    d = F.head_desc(70, 128, 600)
+    ws = T_.empty(F.head_loss_workspace_size(d), dtype=T_.uint8, device="cuda")
+    loss, grad = T_.empty(1, device="cuda"), T_.empty_like(h)
+    F.head_loss(d, h, w, loss, labels=lab, grad=grad, workspace=ws)
+    first = loss.clone()
+    F.head_loss(d, h, w, loss, labels=lab, grad=h, workspace=ws)
+    T_.cuda.synchronize()
+    assert T_.equal(h, grad) and T_.equal(loss, first)
+
+
+def test_packed_weights_under_another_format_are_refused():
+    # the same codes, scales for groups of 64, then asked for with groups of 32 (twice as many scales)
+    F, T_ = _F(), torch()
+    E, H, I = 4, 256, 128
+    none = F.qdesc()
+    gr = [F.qdesc(F.FQ_INT, F.FQ_PER_GROUP, g, F.FQ_LEARNABLE, -8, 7) for g in (64, 32)]
+    new = lambda dt, *s: T_.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+    P = F.packed_experts(dict(codes=new(T_.uint8, E, 2 * I, H // 2), scale=new(T_.float32, E, 2 * I, H // 64)),
+                         dict(codes=new(T_.uint8, E, H, I // 2), scale=new(T_.float32, E, H, I // 64)))
+    x, ids, tw = new(T_.bfloat16, 2, H), new(T_.int32, 2, 1), new(T_.float32, 2, 1)
+    y = T_.ones((2, H), dtype=T_.bfloat16, device="cuda")
+    L = [F.layer_desc(E, H, I, 2, 1, q, q, none, none) for q in gr]
+    ws = new(T_.uint8, F.packed_expert_workspace_size(L[0]))
+    F.packed_expert_fwd(L[0], P, x, ids, tw, y, ws)
+    T_.cuda.synchronize()
+    assert not from_dev(y).any()
+    with pytest.raises(ValueError, match="scale"):
+        F.packed_expert_fwd(L[1], P, x, ids, tw, y, ws)

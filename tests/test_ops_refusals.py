@@ -154,6 +154,7 @@ def test_packed_matvec_refusals():
                dict(q=NV, s=None, b=FAKE + 1, t=FAKE), dict(q=NV, s=None, b=FAKE, t=MIS)):
         assert _mv(**kw) == F.FQ_E_ALIGN, kw
     assert _mv(M=0, x=None, y=None) == F.FQ_OK
+    assert _mv(K=256, N=256) == F.FQ_E_INVALID                          # y is x
 
 
 def _pe(fmt="w4a16", E=8, H=256, I=128, T=4, k=2, P=None, x=FAKE, ids=FAKE, w=FAKE, y=FAKE, ws=FAKE, wsb=1 << 30,
@@ -192,3 +193,4 @@ def test_packed_expert_refusals():
     assert _pe(wsb=need - 1) == F.FQ_E_WORKSPACE
     assert _pe(ws=None) == F.FQ_E_WORKSPACE
     assert _pe(T=0, x=None, ids=None, w=None, y=None, ws=None) == F.FQ_OK
+    assert _pe() == F.FQ_E_INVALID                                      # y is x
