@@ -486,7 +486,9 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
  *     W = q d t (NVFP4: d the block code's E4M3 value, t the tensor scale)
  * with exact products and fp32 sums; W is not rounded to bf16 first, as the
  * fake-quantised weights of training are.  Deterministic, and a row's result
- * does not depend on the other rows.
+ * does not depend on the other rows, nor on other rows of W.  (INT4 sums x (136
+ * + q) and takes 136 x off again: a row of x with an infinity, or with values
+ * past 2^119, gives NaN.)
  *
  *   q            host; INT with a 4-bit range and scales per row or per group
  *                (32 .. 512), or NVFP4; the source does not matter.

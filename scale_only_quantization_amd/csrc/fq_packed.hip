@@ -206,7 +206,8 @@ __device__ __forceinline__ void add_slab(Slab<FMT> (&k)[NT], int c, int nseg, X&
                         part[m] = mfma(xu[m][i], wv, i == 0 ? b[m] : part[m]);
                     } else {
                         part[m] = mfma(xu[m][i], wv, mfma(xu[m][i], minus136, z));
-                        const float s = __uint_as_float(sc[n][i % Slab<FMT>::NS][u]);
+                        // past the row's end: zero, as the next row's scale may be a NaN
+                        const float s = (c + u) * 4 + i < nseg ? __uint_as_float(sc[n][i % Slab<FMT>::NS][u]) : 0.0f;
 #pragma unroll
                         for (int v = 0; v < 4; ++v) acc[n][m][v] = __builtin_fmaf(part[m][v], s, acc[n][m][v]);
                     }

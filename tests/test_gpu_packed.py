@@ -243,3 +243,41 @@ def test_experts_match_the_training_layer():
             err = np.linalg.norm(got - ref) / np.linalg.norm(ref)
             print(f"[packed] nvfp4 against the training layer: {err:.3e}", flush=True)
             assert err <= 0.08
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "g32", "row"])
+def test_rows_that_are_not_finite_stay_their_own(fmt):
+    # every second row of W has NaN scales (NVFP4: NaN block codes), one row of
+    # x a NaN and one an infinity; rows end inside a chunk of 128 columns
+    F, T_ = _F(), torch()
+    N, K, M = 48, 96, 5
+    rng = np.random.default_rng(4)
+    codes = rng.integers(0, 256, (1, N, K // 2)).astype(np.uint8)
+    x = bf16_rne(rng.standard_normal((M, K)).astype(np.float32))
+    if fmt == "nvfp4":
+        q = F.qdesc(F.FQ_NVFP4, F.FQ_PER_GROUP, 16, F.FQ_LEARNABLE)
+        bc = rng.integers(0x20, 0x60, (1, N, K // 16)).astype(np.uint8)
+        kw = dict(block_codes=bc, tensor_scale=np.array([0.01], np.float32))
+        W = OPK.dequant(codes, **kw)[0]
+        bad = bc.copy()
+        bad[:, 1::2] = 0x7F
+        kw["block_codes"] = bad
+    else:
+        q = F.qdesc(F.FQ_INT, F.FQ_PER_GROUP if fmt == "g32" else F.FQ_PER_ROW, 32 if fmt == "g32" else 0,
+                    F.FQ_LEARNABLE, -8, 7)
+        s = (rng.random((1, N, K // 32) if fmt == "g32" else (1, N)) * 0.01 + 0.001).astype(np.float32)
+        W = OPK.dequant(codes, scale=s)[0]
+        bad = s.copy()
+        bad[:, 1::2] = np.nan
+        kw = dict(scale=bad)
+    ref = x.astype(np.float64) @ W.T
+    x[1, 5], x[3, 95] = np.nan, np.inf
+    y = T_.empty((M, N), dtype=T_.bfloat16, device="cuda")
+    F.packed_matvec(q, to_dev(codes), to_dev_bf16(x), y, **{n: to_dev(v) for n, v in kw.items()})
+    T_.cuda.synchronize()
+    got = from_dev(y)
+    assert np.isnan(got[:, 1::2]).all() and not np.isfinite(got[[1, 3]]).any()
+    ok = got[[0, 2, 4], ::2]
+    # one rounding to bf16, and fp32 sums of 96 products of up to 143 |x| s
+    tol = 2.0 ** -8 * np.abs(ref) + 100 * 2.0 ** -24 * 143 / 7 * (np.abs(x[[0, 2, 4]]) @ np.abs(W).T).max() * 7
+    assert np.all(np.abs(ok - ref[[0, 2, 4], ::2]) <= tol[[0, 2, 4], ::2])
