@@ -25,6 +25,9 @@ optim     the scale optimiser step: AdamW with global-norm clipping and the
           range projection of the updated scales.
 distill   the self-distillation losses on logits (kl, rkl, cakld, top-k kl) with
           the LM cross entropy, and their gradients.
+norm      RMS norm with the residual's addition, and its gradient.
+head      the output layer's loss from hidden states, and its gradient.
+packed    dequantisation of packed 4-bit codes and the routed layer on them.
 
 Precision: every codec step is IEEE float32 (numpy float32 arithmetic is
 correctly rounded); GEMMs, gradients and sums are float64.  Pure-Python loops

@@ -28,6 +28,11 @@
 // (a load per chunk touches 16 cache lines for 128 bytes: 6 us of those 15).
 // All loads go through buffer resources: a lane's constant plus a scalar, and
 // rows past the end read as zero without a branch.
+// Measured: 13 rows by 12289 x 8192 in NVFP4 21 us (2.7 TB/s; a large read 6.1);
+// one row by 2048 x 2048 in INT4 4.2 us in the kernel, latency; the layer of 128
+// experts, 2048 by 768, top-8: one token in INT4 17.2 us (fc1 8, fc2 6, combine
+// 4), 16 tokens in NVFP4 79-83 us (fc1 45, 3.4 TB/s, fc2 27), bound by the
+// chains of dependent loads of blocks that pass few slabs each.
 #include <type_traits>
 
 #include "fq_act.h"
