@@ -26,7 +26,7 @@
 // computed once, never stored, and rounded to bf16 only as a probability
 // beside fp32 sums (P's rounding, 2^-9 of each term, averages out over the
 // product's sum).  The two products carry the time (16384 tokens of hidden 2048,
-// 151936 entries, 64 teacher ids: 17.5-18.0 ms, of which probs 8.0 and grad 8.0,
+// 151936 entries, 64 teacher ids: 17.4-18.2 ms, of which probs 8.0 and grad 8.0,
 // 1270 TFLOP/s each where a library product of that size reaches 1357; their
 // matrix units are busy 65 and 77% of the time at 1.7 GHz, the clock that the
 // power allows); sparse and out, 65 rows of the weight per token each, read at
@@ -198,22 +198,40 @@ __global__ __launch_bounds__(256) void k_head_sparse(HeadArgs a) {
     }
     const int slots = a.k + 1, nvec = a.H >> 3;
     const uint4* hr = reinterpret_cast<const uint4*>(a.h + t * a.H);
-    for (int j = w; j < slots; j += 4) {
-        const int id = j < a.k ? a.top_i[t * a.k + j] : (a.labels ? a.labels[t] : -1);
-        float z = -INFINITY;
-        if (id >= 0 && id < a.V) {
-            const uint4* wr = reinterpret_cast<const uint4*>(a.w + (int64_t)id * a.H);
-            float acc = 0.0f;
+    // four slots of a wave at a time, so that their rows are in flight together
+    // (65 rows of 2048 for 16384 tokens: 622 us, 7 TB/s; one at a time 673)
+    for (int j0 = w; j0 < slots; j0 += 16) {
+        int id[4], some = -1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int j = j0 + 4 * q;
+            id[q] = __builtin_amdgcn_readfirstlane(
+                j < a.k ? a.top_i[t * a.k + j] : (j == a.k && a.labels ? a.labels[t] : -1));
+            if (id[q] >= a.V) id[q] = -1;
+            some = max(some, id[q]);
+        }
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (some >= 0) {
+            const uint4* wr[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)               // an absent slot reads a row that is read anyway
+                wr[q] = reinterpret_cast<const uint4*>(a.w + (int64_t)(id[q] >= 0 ? id[q] : some) * a.H);
             for (int c = lane; c < nvec; c += 64) {
                 float x[8], y[8];
                 unpack8(hr[c], x);
-                unpack8(wr[c], y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc = __builtin_fmaf(x[i], y[i], acc);
+                for (int q = 0; q < 4; ++q) {
+                    unpack8(wr[q][c], y);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[q] = __builtin_fmaf(x[i], y[i], acc[q]);
+                }
             }
-            z = wave_sum(acc);
         }
-        if (lane == 0) sz[j] = z;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float z = wave_sum(acc[q]);
+            if (lane == 0 && j0 + 4 * q < slots) sz[j0 + 4 * q] = id[q] >= 0 ? z : -INFINITY;
+        }
     }
     __syncthreads();
     for (int j = threadIdx.x; j < slots; j += 256) a.zs[t * slots + j] = sz[j];
@@ -532,7 +550,7 @@ __global__ __launch_bounds__(256) void k_head_out(HeadArgs a) {
         // an id's q counts once, at its first slot; the label's slot is the first of all
         bool own = id >= 0 && id != lab;
         for (int j = 0; j < a.k; ++j) {
-            const int o = __shfl(id, j);
+            const int o = __builtin_amdgcn_readlane(id, j);
             if (j < lane && o == id) own = false;
         }
         if (lane < a.k) {
