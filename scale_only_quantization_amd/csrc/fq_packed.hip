@@ -31,8 +31,9 @@
 // Measured: 13 rows by 12289 x 8192 in NVFP4 21 us (2.7 TB/s; a large read 6.1);
 // one row by 2048 x 2048 in INT4 4.2 us in the kernel, latency; the layer of 128
 // experts, 2048 by 768, top-8: one token in INT4 17.2 us (fc1 8, fc2 6, combine
-// 4), 16 tokens in NVFP4 79-83 us (fc1 45, 3.4 TB/s, fc2 27), bound by the
-// chains of dependent loads of blocks that pass few slabs each.
+// 4), 16 tokens in NVFP4 76 us (fc1 39-41, 3.8 TB/s, fc2 23), bound by the
+// chains of dependent loads of blocks that pass few slabs each, and by the
+// conversions (in INT4 33 and 21).
 #include <type_traits>
 
 #include "fq_act.h"
@@ -315,51 +316,178 @@ struct XLds {
     }
 };
 
-// Rows of x in LDS times two tiles of 16 weight rows that start at rows row0
-// and row1 of r, over this wave's slabs kp, kp + KW, ...  begin() sends the
-// first slab's loads, before the rows of x are there; run() takes this lane's
-// row at byte xo (its quarter of a 32-column segment included).  One slab is
-// in registers at a time: a second one (the next slab's loads during this
-// one's products) took the registers that hold a fourth wave per SIMD, and
-// the layer's blocks, short chains of dependent loads, need the waves more
-// (fc1 of 16 tokens in NVFP4: 45 us against 58).
-template <int FMT, int KW>
+// For rows of x in LDS: two tiles of 16 weight rows that start at rows row0 and
+// row1 of a resource, up to 8 rows of x.  A load reads 128 bytes of each of 8
+// weight rows, two chunks, whole cache lines (in 64-byte pieces of 16 rows fc1
+// of 16 tokens took 41 us in NVFP4 and 38 in INT4, with these 39 and 35): lane
+// n = lane%16 holds a quarter of chunk n%2 of row n/2 of those 8.  So that the
+// chunks need no exchange between lanes, rows 0-7 of the product's x are the
+// rows' even chunk and rows 8-15 their odd one: of the product, even n have
+// their sum in rows 0-7 and odd n theirs in rows 8-15, the other half is of no
+// meaning, and lanes 33 apart (in exclusive or) hold a weight row's two sums.
+template <int FMT>
+struct PairRows {
+    __amdgpu_buffer_rsrc_t codes, scale;
+    uint32_t vc, vs, cb, sb;
+    __device__ __forceinline__ PairRows(const PackedW& w, int64_t row0, int64_t rows) {
+        const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+        cb = (uint32_t)w.K >> 1;
+        sb = FMT == NVFP4 ? (uint32_t)w.K >> 4 : (uint32_t)w.spr * 4;
+        codes = make_rsrc(w.codes + row0 * cb, rows * cb);
+        scale = FMT == NVFP4 ? make_rsrc(w.bcodes + row0 * sb, rows * sb) : make_rsrc(w.scale + row0 * w.spr, rows * sb);
+        vc = (n >> 1) * cb + (n & 1) * 64 + g * 16;
+        vs = (8 * (g & 1) + (n >> 1)) * sb;
+    }
+};
+
+// Four chunks of a tile: q[2 p + h] is of chunks c + 2 p + n%2 of rows 8 h ..
+// 8 h + 7; lane group g loads the scales that go with q[g].
+template <int FMT>
+struct PairSlab {
+    static constexpr int NS = Slab<FMT>::NS;
+    u32x4 q[XC];
+    uint32_t s[NS];
+    __device__ __forceinline__ void load(const PackedW& w, const PairRows<FMT>& r, int row, int c) {
+        const uint32_t oc = row * r.cb + c * 64, os = row * r.sb;
+        const int cg = c + 2 * ((threadIdx.x & 63) >> 5) + (threadIdx.x & 1);
+#pragma unroll
+        for (int u = 0; u < XC; ++u)
+            q[u] = __builtin_amdgcn_raw_buffer_load_b128(r.codes, r.vc, oc + (u >> 1) * 128 + (u & 1) * 8 * r.cb, 0);
+        if (FMT == NVFP4) {                               // the layer's columns are multiples of 128
+            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r.scale, r.vs + cg * 8, os, 0);
+            s[0] = v.x;
+            s[NS - 1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                s[i] = __builtin_amdgcn_raw_buffer_load_b32(r.scale, r.vs + ((cg * NS + i) >> w.gshift) * 4, os, 0);
+        }
+    }
+};
+
+// acc[n][h] += rows of x times tile n's rows 8 h .. 8 h + 7, chunks c .. c + 3
+// of nch.  xp + xo: this lane's row of x, its quarter of a 32-column segment.
+template <int FMT>
+__device__ __forceinline__ void add_pairs(PairSlab<FMT> (&k)[2], int c, int nch, const lds_t* xp, uint32_t xo,
+                                          f32x4 (&acc)[2][2]) {
+    constexpr int NS = Slab<FMT>::NS;
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    const f32x4 z = {0, 0, 0, 0};
+    const u32x4 zero = {0, 0, 0, 0}, minus136 = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};
+    uint32_t sc[2][NS][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) spread4(k[n].s[i], sc[n][i]);
+#pragma unroll
+    for (int p = 0; p < XC / 2; ++p) {
+        const int cp = c + 2 * p;
+        if (cp >= nch) continue;                      // past the row's end
+        const bool half = cp + 1 >= nch;              // the row ends between the chunks: x and factors of the odd one zero
+        const uint32_t at = xo + cp * 256 + (!half && (lane & 8) ? 256 : 0);
+        u32x4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(xp + at + i * 64);
+        }
+        if (half) {
+            asm volatile("");                         // a branch, not selects on every step
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = lane & 8 ? zero : x[i];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < NS; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) sc[n][i][2 * p + h] = lane & 1 ? 0 : sc[n][i][2 * p + h];
+        }
+        f32x4 b = z;
+        if (FMT == INT_WIDE)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b = mfma(x[i], minus136, b);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int u = 2 * p + h;
+                transpose4(k[n].q[u]);
+                float dd[4];
+                if (FMT == NVFP4) {                   // word i is the g-th quarter of segment i: block 2 i + g/2
+                    const int sh = 4 * (g & 2);
+                    const int d0 = (int)(sc[n][0][u] >> sh), d1 = (int)(sc[n][NS - 1][u] >> sh);
+                    dd[0] = __builtin_amdgcn_cvt_f32_fp8(d0, 0);
+                    dd[1] = __builtin_amdgcn_cvt_f32_fp8(d0, 2);
+                    dd[2] = __builtin_amdgcn_cvt_f32_fp8(d1, 0);
+                    dd[3] = __builtin_amdgcn_cvt_f32_fp8(d1, 2);
+                }
+                f32x4 part = b;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const u32x4 wv = FMT == NVFP4 ? fp4_words(k[n].q[u][i], dd[i]) : int_words(k[n].q[u][i]);
+                    if (FMT == NVFP4) {
+                        acc[n][h] = mfma(x[i], wv, acc[n][h]);
+                    } else if (FMT == INT_WIDE) {
+                        part = mfma(x[i], wv, part);
+                    } else {
+                        part = mfma(x[i], wv, mfma(x[i], minus136, z));
+                        const float s = __uint_as_float(sc[n][i % NS][u]);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[n][h][v] = __builtin_fmaf(part[v], s, acc[n][h][v]);
+                    }
+                }
+                if (FMT == INT_WIDE) {
+                    const float s = __uint_as_float(sc[n][0][u]);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[n][h][v] = __builtin_fmaf(part[v], s, acc[n][h][v]);
+                }
+            }
+    }
+}
+
+// Of the sums in `run`'s result, a lane has tile n's row pair_col() and rows
+// 4 (lane/16 % 2) + v of x, if pair_has().
+__device__ __forceinline__ int pair_col() { return 8 * (threadIdx.x & 1) + ((threadIdx.x & 15) >> 1); }
+__device__ __forceinline__ bool pair_has() { return ((threadIdx.x >> 5) & 1) == (threadIdx.x & 1); }
+__device__ __forceinline__ int pair_row() { return 4 * ((threadIdx.x >> 4) & 1); }
+
+// The columns are split into VW shares (slabs s, s + VW, ... each), whose sums
+// are added in order.  SHARE: this wave has the one share `s`; else it takes
+// all of them in turn, with the same bits.  begin() sends the first slab's
+// loads, before the rows of x are there.  One slab is in registers at a time: a
+// second one (the next slab's loads during this one's products) took the
+// registers that hold a fourth wave per SIMD, which was slower (fc1 of 16 tokens
+// in NVFP4: 58 us against 45 then).
+template <int FMT, int VW, bool SHARE>
 struct DotLds {
     const PackedW& w;
-    const Rows<FMT>& r;
-    int row0, row1, c;
-    Slab<FMT> sl[2];
-    __device__ __forceinline__ void load() {
+    const PairRows<FMT>& r;
+    int row0, row1, s;
+    PairSlab<FMT> sl[2];
+    __device__ __forceinline__ void load(int c) {
         sl[0].load(w, r, row0, c);
         sl[1].load(w, r, row1, c);
     }
-    __device__ __forceinline__ void begin(int kp) {
-        c = kp * XC;
-        if (c * 128 < w.K) load();
+    __device__ __forceinline__ void begin(int share) {
+        s = share;
+        if (s * XC * 128 < w.K) load(s * XC);
     }
-    __device__ __forceinline__ void run(const lds_t* xp, uint32_t xo, f32x4 (&acc)[2][1]) {
+    __device__ __forceinline__ void run(const lds_t* xp, uint32_t xo, f32x4 (&sum)[2]) {
         const f32x4 z = {0, 0, 0, 0};
-        const u32x4 minus136 = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};
-        const int nseg = w.K >> 5, nch = (nseg + 3) >> 2;
-        acc[0][0] = acc[1][0] = z;
-        while (c < nch) {
-            add_slab<FMT, 1, 2>(
-                sl, c, nseg,
-                [&](int u, u32x4 (&o)[1][4]) {
+        const int nch = w.K >> 7;
+        const bool odd = threadIdx.x & 1;
+        sum[0] = sum[1] = z;
+        for (int v = s; v < (SHARE ? s + 1 : VW); ++v) {
+            f32x4 acc[2][2] = {{z, z}, {z, z}};
+            for (int c = v * XC; c < nch; c += VW * XC) {
+                add_pairs<FMT>(sl, c, nch, xp, xo, acc);
+                const int next = c + VW * XC < nch ? c + VW * XC : SHARE ? nch : (v + 1) * XC;
+                if (next < nch) load(next);
+            }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o[0][i] = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(
-                            xp + xo + (c + u) * 256 + i * 64);
-                },
-                [&](const u32x4 (&v)[4], int, int) {
-                    f32x4 b = z;
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) b = mfma(v[i], minus136, b);
-                    return b;
-                },
-                acc);
-            c += KW * XC;
-            if (c < nch) load();
+                for (int i = 0; i < 4; ++i)
+                    sum[n][i] += (odd ? acc[n][1][i] : acc[n][0][i]) + __shfl_xor(odd ? acc[n][0][i] : acc[n][1][i], 33);
         }
     }
 };
@@ -531,12 +659,12 @@ struct Group {
 // The sums of a team of KW waves for two tiles: value i = 4 tile + v of lane l
 // at red[wave][i][l], added in wave order.
 template <int KW>
-__device__ __forceinline__ void team_put(float (*red)[8][64], const f32x4 (&acc)[2][1]) {
+__device__ __forceinline__ void team_put(float (*red)[8][64], const f32x4 (&sum)[2]) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-        red[w][v][lane] = acc[0][0][v];
-        red[w][4 + v][lane] = acc[1][0][v];
+        red[w][v][lane] = sum[0][v];
+        red[w][4 + v][lane] = sum[1][v];
     }
     lds_barrier();
 }
@@ -550,94 +678,111 @@ __device__ __forceinline__ float team_get(float (*red)[8][64], int i) {
 }
 
 // fc1 and SwiGLU of one group of rows: 16 gate rows and their 16 up rows per
-// block, the waves splitting the columns.  `cap` rows of x at a time are in
-// LDS.  The tile of h goes through the second activation quantiser on the way
-// (a 16-block of NVFP4 is the tile's row).
-template <int FMT>
+// block, the waves splitting the columns (SHARE), or per wave.  `cap` rows of
+// x at a time are in LDS.  The tile of h goes through the second activation
+// quantiser on the way (a 16-block of NVFP4 is the tile's row).
+template <int FMT, bool SHARE>
 __global__ __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(FMT == INT_NARROW ? 3 : 4))) void k_packed_fc1(
     PackedExpertArgs a, int cap) {
     extern __shared__ __attribute__((aligned(16))) char dyn[];
-    __shared__ float red[WV][8][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int r0 = blockIdx.y, i0 = blockIdx.x * 16;
+    __shared__ float red[SHARE ? WV : 1][8][64];
+    const int lane = threadIdx.x & 63, w = wave_id();
+    const int r0 = blockIdx.y, i0 = SHARE ? blockIdx.x * 16 : (blockIdx.x * WV + w) * 16;    // I is a multiple of 128
     const Group gr(a, r0);
     if (gr.count == 0) return;
     const int e = clamp_id(sload(a.ids, r0), a.E);
-    const Rows<FMT> rows(a.w1, (int64_t)e * 2 * a.I, 2 * a.I);
+    const PairRows<FMT> rows(a.w1, (int64_t)e * 2 * a.I, 2 * a.I);
     const float t1 = FMT == NVFP4 ? sload(a.w1.tscale, e) : 1.0f;
     const int kind2 = a.a2.q.kind;
     const float s2 = kind2 != K_NONE ? sload(a.a2.s, e) : 0.0f;
     XLds<FMT> x{(lds_t*)dyn, XLds<FMT>::bytes_per_row(a.H)};
-    DotLds<FMT, WV> dot{a.w1, rows, i0, i0 + a.I};
+    DotLds<FMT, WV, SHARE> dot{a.w1, rows, i0, i0 + a.I};
     for (int b = 0; b < gr.count; b += cap) {
         const int n = min(cap, gr.count - b);
-        dot.begin(w);
+        dot.begin(SHARE ? w : 0);
         if (b > 0) lds_barrier();                      // the last rows and sums have been read
         x.fill(a.H, n, [&](int m) {
             const int r = gr.at_uniform(b + m);
             return a.xhat ? a.xhat + (int64_t)r * a.H : a.x + (int64_t)(r / a.k) * a.H;
         });
         lds_barrier();
-        f32x4 acc[2][1];
-        dot.run(x.p, (uint32_t)min(lane & 15, n - 1) * x.stride + (lane >> 4) * 16, acc);
-        team_put<WV>(red, acc);
-        const int m = 4 * (lane >> 4) + w;             // wave w takes the w-th row of each lane group
-        float gate = team_get<WV>(red, w), up = team_get<WV>(red, 4 + w), sig;
-        if (FMT == NVFP4) {
-            gate *= t1;
-            up *= t1;
-        }
-        uint16_t hb = bf16_of(silu_sig(gate, &sig) * up);
-        if (kind2 != K_NONE) {
-            const float h = __uint_as_float((uint32_t)hb << 16);
-            Div dv;
-            float dfac;
-            if (kind2 == K_NVFP4) {
-                dv.set(act_scale_t<K_NVFP4>(a.a2, s2, group_max(fabsf(h), 16), 0.0f, 0.0f, &dfac));
-                hb = bf16_of(quant_elem<K_NVFP4>(h, dv, -6.0f, 6.0f).q * dv.s);
-            } else {
-                dv.set(s2);
-                const Elem q = kind2 == K_FP8 ? quant_elem<K_FP8>(h, dv, -448.0f, 448.0f)
-                                              : quant_elem<K_INT>(h, dv, a.a2.q.qmin, a.a2.q.qmax);
-                hb = bf16_of(q.q * s2);
+        f32x4 sum[2];
+        dot.run(x.p, (uint32_t)min(lane & 7, n - 1) * x.stride + (lane >> 4) * 16, sum);
+        auto store = [&](int v, float gate, float up) {
+            const int m = pair_row() + v;
+            const bool mine = pair_has() && m < n;
+            float sig;
+            if (FMT == NVFP4) {
+                gate *= t1;
+                up *= t1;
             }
+            uint16_t hb = bf16_of(silu_sig(gate, &sig) * up);
+            if (kind2 != K_NONE) {
+                const float h = __uint_as_float((uint32_t)hb << 16);
+                Div dv;
+                float dfac;
+                if (kind2 == K_NVFP4) {
+                    float top = group_max(mine ? fabsf(h) : 0.0f, 16);       // the tile's row is in two half waves
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                    dv.set(act_scale_t<K_NVFP4>(a.a2, s2, top, 0.0f, 0.0f, &dfac));
+                    hb = bf16_of(quant_elem<K_NVFP4>(h, dv, -6.0f, 6.0f).q * dv.s);
+                } else {
+                    dv.set(s2);
+                    const Elem q = kind2 == K_FP8 ? quant_elem<K_FP8>(h, dv, -448.0f, 448.0f)
+                                                  : quant_elem<K_INT>(h, dv, a.a2.q.qmin, a.a2.q.qmax);
+                    hb = bf16_of(q.q * s2);
+                }
+            }
+            if (mine) a.h[(int64_t)gr.at(b + m) * a.I + i0 + pair_col()] = hb;
+        };
+        if constexpr (SHARE) {
+            team_put<WV>(red, sum);
+            store(w, team_get<WV>(red, w), team_get<WV>(red, 4 + w));
+        } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (v < n) store(v, sum[0][v], sum[1][v]);
         }
-        if (m < n) a.h[(int64_t)gr.at(b + m) * a.I + i0 + (lane & 15)] = hb;
     }
 }
 
 // fc2 of one group of rows: y_r in fp32, one row per routed row; 32 columns of
-// y per pair of waves
-template <int FMT>
+// y per pair of waves, or (not SHARE) per wave
+template <int FMT, bool SHARE>
 __global__ __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(FMT == INT_NARROW ? 3 : 4))) void k_packed_fc2(
     PackedExpertArgs a, int cap) {
-    constexpr int KW = FC2_KW;
+    constexpr int KW = SHARE ? FC2_KW : 1;
     extern __shared__ __attribute__((aligned(16))) char dyn[];
-    __shared__ float red[WV][8][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    __shared__ float red[SHARE ? WV : 1][8][64];
+    const int lane = threadIdx.x & 63, w = wave_id();
     const int r0 = blockIdx.y, n0 = (blockIdx.x * (WV / KW) + w / KW) * 32;      // H is a multiple of 128
     const Group gr(a, r0);
     if (gr.count == 0) return;
     const int e = clamp_id(sload(a.ids, r0), a.E);
-    const Rows<FMT> rows(a.w2, (int64_t)e * a.H, a.H);
+    const PairRows<FMT> rows(a.w2, (int64_t)e * a.H, a.H);
     const float t2 = FMT == NVFP4 ? sload(a.w2.tscale, e) : 1.0f;
     XLds<FMT> x{(lds_t*)dyn, XLds<FMT>::bytes_per_row(a.I)};
-    DotLds<FMT, KW> dot{a.w2, rows, n0, n0 + 16};
+    DotLds<FMT, FC2_KW, SHARE> dot{a.w2, rows, n0, n0 + 16};
     for (int b = 0; b < gr.count; b += cap) {
         const int n = min(cap, gr.count - b);
-        dot.begin(w % KW);
+        dot.begin(SHARE ? w % KW : 0);
         if (b > 0) lds_barrier();
         x.fill(a.I, n, [&](int m) { return a.h + (int64_t)gr.at_uniform(b + m) * a.I; });
         lds_barrier();
-        f32x4 acc[2][1];
-        dot.run(x.p, (uint32_t)min(lane & 15, n - 1) * x.stride + (lane >> 4) * 16, acc);
-        team_put<KW>(red, acc);
+        f32x4 sum[2];
+        dot.run(x.p, (uint32_t)min(lane & 7, n - 1) * x.stride + (lane >> 4) * 16, sum);
+        auto store = [&](int i, float s) {             // value 4 tile + v of this lane
+            const int m = pair_row() + (i & 3);
+            if (pair_has() && m < n)
+                a.yr[(int64_t)gr.at(b + m) * a.H + n0 + 16 * (i >> 2) + pair_col()] = FMT == NVFP4 ? s * t2 : s;
+        };
+        if constexpr (SHARE) {
+            team_put<KW>(red, sum);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = j * KW + w % KW, m = 4 * (lane >> 4) + (i & 3);
-            const float s = team_get<KW>(red, i);
-            if (m < n)
-                a.yr[(int64_t)gr.at(b + m) * a.H + n0 + 16 * (i >> 2) + (lane & 15)] = FMT == NVFP4 ? s * t2 : s;
+            for (int j = 0; j < 4; ++j) store(j * KW + w % KW, team_get<KW>(red, j * KW + w % KW));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) store(i, sum[i >> 2][i & 3]);
         }
     }
 }
@@ -678,23 +823,39 @@ hipError_t run_matvec(const MatvecArgs& a, hipStream_t st) {
 }
 
 // Rows of x a block keeps in LDS at a time: as many as a group can have, up to
-// 16 and to 32 KB (four blocks to a CU).
+// 8 and to 32 KB (four blocks to a CU).
 int lds_rows(int K, int T) {
-    const int fit = 32768 / (K * 2 + 16), most = T < 16 ? T : 16;
+    const int fit = 32768 / (K * 2 + 16), most = T < 8 ? T : 8;
     return fit < 1 ? 1 : fit < most ? fit : most;
 }
+// A tile per wave where that leaves blocks enough (counted over all routed rows,
+// of which some open no group), else the waves share its columns.  128 experts,
+// 2048 by 768, top-8, shared against not: NVFP4 fc1 of 16 tokens (1536 blocks of
+// four tiles) 38.8 and 40.6 us, of 32 55.9 and 52.8; INT4 fc1 of 4 tokens (384)
+// 17.4 and 17.9, of 8 25.2 and 24.0, of 16 35.4 and 32.6; fc2 of 8 tokens (1024)
+// 16.4 and 17.2 in NVFP4, of 16 21.5 and 20.7 in INT4.
 template <int FMT>
 hipError_t run_fc1(const PackedExpertArgs& a, hipStream_t st) {
     const int cap = lds_rows(a.H, a.R / a.k);
-    hipLaunchKernelGGL(k_packed_fc1<FMT>, dim3((unsigned)(a.I / 16), (unsigned)a.R), dim3(64 * WV),
-                       (size_t)cap * (a.H * 2 + 16), st, a, cap);
+    const size_t lds = (size_t)cap * (a.H * 2 + 16);
+    if (a.R * (a.I / 64) >= (FMT == NVFP4 ? 2048 : 512))
+        hipLaunchKernelGGL((k_packed_fc1<FMT, false>), dim3((unsigned)(a.I / 64), (unsigned)a.R), dim3(64 * WV), lds, st,
+                           a, cap);
+    else
+        hipLaunchKernelGGL((k_packed_fc1<FMT, true>), dim3((unsigned)(a.I / 16), (unsigned)a.R), dim3(64 * WV), lds, st,
+                           a, cap);
     return hipGetLastError();
 }
 template <int FMT>
 hipError_t run_fc2(const PackedExpertArgs& a, hipStream_t st) {
     const int cap = lds_rows(a.I, a.R / a.k);
-    hipLaunchKernelGGL(k_packed_fc2<FMT>, dim3((unsigned)(a.H / 64), (unsigned)a.R), dim3(64 * WV),
-                       (size_t)cap * (a.I * 2 + 16), st, a, cap);
+    const size_t lds = (size_t)cap * (a.I * 2 + 16);
+    if (a.R * (a.H / 128) >= 2048)
+        hipLaunchKernelGGL((k_packed_fc2<FMT, false>), dim3((unsigned)(a.H / 128), (unsigned)a.R), dim3(64 * WV), lds, st,
+                           a, cap);
+    else
+        hipLaunchKernelGGL((k_packed_fc2<FMT, true>), dim3((unsigned)(a.H / 64), (unsigned)a.R), dim3(64 * WV), lds, st,
+                           a, cap);
     return hipGetLastError();
 }
 

@@ -178,7 +178,7 @@ def _check_layer(d, got, what):
 
 @pytest.mark.parametrize("fmt", ["w4a16", "nvfp4", "nvfp4a16", "w4afp8"])
 @pytest.mark.parametrize("E,H,I,T,k", [(8, 256, 128, 1, 2), (8, 256, 128, 7, 4), (1, 128, 128, 3, 1),
-                                       (16, 2048, 768, 1, 8), (4, 384, 256, 40, 3)])
+                                       (16, 2048, 768, 1, 8), (4, 384, 256, 40, 3), (8, 384, 256, 200, 4)])
 def test_experts(fmt, E, H, I, T, k):
     d = _layer(E + H + T, fmt, E, H, I, T, k)
     got = _run(d)
@@ -281,3 +281,37 @@ def test_rows_that_are_not_finite_stay_their_own(fmt):
     # one rounding to bf16, and fp32 sums of 96 products of up to 143 |x| s
     tol = 2.0 ** -8 * np.abs(ref) + 100 * 2.0 ** -24 * 143 / 7 * (np.abs(x[[0, 2, 4]]) @ np.abs(W).T).max() * 7
     assert np.all(np.abs(ok - ref[[0, 2, 4], ::2]) <= tol[[0, 2, 4], ::2])
+
+
+@pytest.mark.parametrize("wf", ["g32", "g64", "g128", "row"])
+@pytest.mark.parametrize("E,H,I,T,k", [(4, 384, 128, 1, 3), (4, 384, 256, 9, 2), (8, 384, 256, 200, 4)])
+def test_experts_of_every_scale_layout(wf, E, H, I, T, k):
+    # groups of less than a chunk, one scale per row; both splits of the
+    # columns, rows that end between two chunks; a token alone has the same bits
+    F, T_ = _F(), torch()
+    q1, w1, W1 = _weights(E + T, wf, E, 2 * I, H)
+    q2, w2, W2 = _weights(E + T + 1, wf, E, H, I)
+    for w, W, n in ((w1, W1, H), (w2, W2, I)):
+        w["scale"] *= np.float32(1.0 / (np.sqrt(np.mean(W ** 2)) * np.sqrt(n)))
+    W1, W2 = OPK.dequant(**w1), OPK.dequant(**w2)
+    rng = np.random.default_rng(T)
+    x = bf16_rne(rng.standard_normal((T, H)).astype(np.float32))
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)        # an expert may be named twice
+    tw = rng.random((T, k)).astype(np.float32)
+    none = F.qdesc()
+    P = F.packed_experts(*({n: to_dev(v) for n, v in w.items()} for w in (w1, w2)))
+
+    def run(rows):
+        L = F.layer_desc(E, H, I, len(x[rows]), k, q1, q2, none, none)
+        y = T_.empty((len(x[rows]), H), dtype=T_.bfloat16, device="cuda")
+        ws = T_.full((F.packed_expert_workspace_size(L),), 255, dtype=T_.uint8, device="cuda")
+        F.packed_expert_fwd(L, P, to_dev_bf16(x[rows]), to_dev(ids[rows]), to_dev(tw[rows]), y, ws)
+        T_.cuda.synchronize()
+        return from_dev(y)
+
+    got = run(slice(None))
+    _, _, a1, a2 = OP.PRESETS["w4a16"]
+    ref = OPK.experts(W1, W2, x, ids, tw, a1, None, a2, None)
+    err = np.linalg.norm(got - ref) / np.linalg.norm(ref)
+    assert err <= 2.0 ** -7, f"{err:.2e}"                    # as for the presets above
+    np.testing.assert_array_equal(run(slice(T // 2, T // 2 + 1))[0], got[T // 2])
