@@ -800,9 +800,12 @@ __global__ __launch_bounds__(256) void k_packed_combine(PackedExpertArgs a) {
 
 // Up to 2048 columns four waves split a tile's columns, above eight do (12289 x
 // 8192, 13 rows, NVFP4: 22 us against 27; 49152 x 2048: 22 against 19); by the
-// columns only, so that a row's bits do not depend on the other rows.  Four
-// tiles per block reuse x where that leaves blocks for most CUs, else one
-// (2048 x 2048, one row: 4.2 us against 6.3).
+// columns only, so that a row's bits do not depend on the other rows.  A CU
+// holds one block at a time, whose time grows with its tiles from a fixed part
+// on (12289 x 8192, 13 rows: 9.3 us a round of blocks of one tile, 14.4 of two,
+// 16 of three, 22 of four), so the tiles per block are those with the least sum
+// over the rounds (8192 x 8192, one row, one tile 16.1 us, two 12.2, four 18.6;
+// 12000 x 2048, 16 rows: 10.0, 9.6, three 8.0, four 9.1).
 template <int FMT, int KW>
 hipError_t run_matvec(const MatvecArgs& a, hipStream_t st) {
     const unsigned tiles = (unsigned)((a.N + 15) / 16);
@@ -811,10 +814,18 @@ hipError_t run_matvec(const MatvecArgs& a, hipStream_t st) {
     else if (a.M > 16)
         hipLaunchKernelGGL((k_matvec<FMT, 2, 2, KW>), dim3((tiles + 1) / 2, (unsigned)((a.M + 31) / 32)), dim3(64 * KW),
                            0, st, a);
-    else if (tiles >= 768)
-        hipLaunchKernelGGL((k_matvec<FMT, 1, 4, KW>), dim3((tiles + 3) / 4), dim3(64 * KW), 0, st, a);
-    else
-        hipLaunchKernelGGL((k_matvec<FMT, 1, 1, KW>), dim3(tiles), dim3(64 * KW), 0, st, a);
+    else {
+        unsigned best = 0, least = 0;
+        for (unsigned n = 1; n <= 4; ++n) {
+            const unsigned cost = ((tiles + n - 1) / n + 255) / 256 * (4 + 3 * n);
+            if (best == 0 || cost < least) best = n, least = cost;
+        }
+        const dim3 grid((tiles + best - 1) / best), block(64 * KW);
+        if (best == 1) hipLaunchKernelGGL((k_matvec<FMT, 1, 1, KW>), grid, block, 0, st, a);
+        else if (best == 2) hipLaunchKernelGGL((k_matvec<FMT, 1, 2, KW>), grid, block, 0, st, a);
+        else if (best == 3) hipLaunchKernelGGL((k_matvec<FMT, 1, 3, KW>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((k_matvec<FMT, 1, 4, KW>), grid, block, 0, st, a);
+    }
     return hipGetLastError();
 }
 template <int FMT>

@@ -79,6 +79,14 @@ def test_matvec(fmt, N, K, M):
     np.testing.assert_array_equal(_matvec(q, w, x[M // 2:M // 2 + 1], N=N)[0], got[M // 2])
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "row", "g32", "g128"])
+@pytest.mark.parametrize("N,K,M", [(4200, 288, 5), (9001, 160, 16), (12300, 288, 3), (4100, 2176, 2), (9000, 2304, 1),
+                                   (12289, 2176, 2)])
+def test_matvec_of_many_rows(fmt, N, K, M):
+    # two, three and four tiles a block, four and eight waves
+    test_matvec(fmt, N, K, M)
+
+
 @pytest.mark.parametrize("fmt", ["nvfp4", "g128", "g32"])
 @pytest.mark.parametrize("M", [1, 5, 70])
 def test_matvec_by_matrix(fmt, M):
