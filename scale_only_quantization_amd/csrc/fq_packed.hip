@@ -31,7 +31,7 @@
 // Measured: 13 rows by 12289 x 8192 in NVFP4 21 us (2.7 TB/s; a large read 6.1);
 // one row by 2048 x 2048 in INT4 4.2 us in the kernel, latency; the layer of 128
 // experts, 2048 by 768, top-8: one token in INT4 17.2 us (fc1 8, fc2 6, combine
-// 4), 16 tokens in NVFP4 76 us (fc1 39-41, 3.8 TB/s, fc2 23), bound by the
+// 4), 16 tokens in NVFP4 75-77 us (fc1 39-41, 3.8 TB/s, fc2 23), bound by the
 // chains of dependent loads of blocks that pass few slabs each, and by the
 // conversions (in INT4 33 and 21).
 #include <type_traits>
