@@ -79,7 +79,8 @@ def _check(got, h, w, tv, ti, lab, lm=0.8, dist=1.2, what=""):
 # of steps, more columns than a tile)
 @pytest.mark.parametrize("T,H,V,k", [(1, 64, 300, 4), (37, 128, 1000, 16), (300, 192, 777, 64), (513, 320, 2049, 1),
                                      (5, 64, 1, 0), (9, 64, 1, 1), (70, 640, 63, 33), (256, 64, 256, 64),
-                                     (129, 1024, 5003, 0)])
+                                     (129, 1024, 5003, 0),
+                                     (300, 128, 40000, 16), (700, 256, 30001, 4)])   # more tiles than CUs
 @pytest.mark.parametrize("what", ["both", "lm", "distill"])
 def test_matches_the_oracle(T, H, V, k, what):
     if what == "distill" and k == 0 or what == "lm" and k > 0 and T > 100:
