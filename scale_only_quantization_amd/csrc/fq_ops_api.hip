@@ -140,6 +140,10 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
         !aligned(labels, 4) || !aligned(loss, 4) || !aligned(row_loss, 4) || !aligned(grad, 16) ||
         !aligned(workspace, 256))
         return FQ_E_ALIGN;
+    if (d->tokens == 0) {                                                     // the mean of nothing: no workspace
+        FQ_TRY(launch_head(HeadArgs{}, HeadPlan{}, loss, static_cast<hipStream_t>(stream)));
+        return FQ_OK;
+    }
     const HeadPlan pl = head_plan(d->tokens, d->hidden, d->vocab);
     const HeadLayout y = head_layout(d, pl, grad != nullptr);
     if (!workspace || workspace_bytes < y.total) return FQ_E_WORKSPACE;

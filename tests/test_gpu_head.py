@@ -207,3 +207,13 @@ def test_gradient_matches_differences():
     # roundings of 2^-8 of each entry and of its terms, taken as independent, five times over
     tol = 5 * 2.0 ** -8 * np.linalg.norm((np.abs(g) + rest) * u) + 1e-6 * abs(d)
     assert abs(d - np.sum(g * u)) <= tol
+
+
+def test_no_tokens_without_workspace():
+    F, T_ = _F(), torch()
+    w = T_.zeros((100, 64), dtype=T_.bfloat16, device="cuda")
+    z = T_.empty((0, 64), dtype=T_.bfloat16, device="cuda")
+    for k in (0, 4):
+        out = T_.full((1,), 9.0, device="cuda")
+        F.head_loss(F.head_desc(0, 64, 100, k), z, w, out, grad=z)
+        assert from_dev(out)[0] == 0

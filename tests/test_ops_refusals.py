@@ -194,3 +194,13 @@ def test_packed_expert_refusals():
     assert _pe(ws=None) == F.FQ_E_WORKSPACE
     assert _pe(T=0, x=None, ids=None, w=None, y=None, ws=None) == F.FQ_OK
     assert _pe() == F.FQ_E_INVALID                                      # y is x
+
+
+def test_head_loss_of_no_tokens_needs_no_workspace():
+    # with no tokens only `loss` has to be there; the call gets as far as its
+    # launch, which has no GPU to go to here (with one, a GPU test makes the call)
+    if torch.cuda.is_available():
+        pytest.skip("no device memory behind the pointer")
+    for kw in (dict(), dict(k=4), dict(lab=None), dict(grad=FAKE)):
+        assert _hl(**{**dict(T=0, h=None, w=None, lab=None, ws=None, wsb=0), **kw}) == F.FQ_E_HIP, kw
+    assert _hl(T=0, h=None, w=None, lab=None, ws=None, wsb=0, loss=None) == F.FQ_E_INVALID
