@@ -177,18 +177,22 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
 // ------------------------------------------------------ packed 4-bit weights --
 namespace {
 
-// The packed form of `batch` matrices [rows, cols] under quantiser d.
-int check_packed(const fq_qdesc* d, int64_t cols, const uint8_t* codes, const uint8_t* block_codes, const float* scale,
-                 const float* tensor_scale, PackedW* w) {
-    QParams q;
-    const int s = check_qdesc(d, &q);
-    if (s != FQ_OK) return s;
+// The formats and row lengths of packed weights.
+int check_packed_format(const QParams& q, int64_t cols) {
     if (!four_bit(q)) return FQ_E_UNSUPPORTED;
     if (q.kind == FQ_INT && (q.qmin < -8.0f || q.qmax > 7.0f || q.gran == FQ_PER_TENSOR ||
                              (q.gran == FQ_PER_GROUP && q.group < 32)))
         return FQ_E_UNSUPPORTED;
     if (cols < 32 || cols % 32 || (q.gran == FQ_PER_GROUP && cols % q.group)) return FQ_E_SHAPE;
-    if (cols > 65536) return FQ_E_UNSUPPORTED;
+    return cols > 65536 ? FQ_E_UNSUPPORTED : FQ_OK;
+}
+
+// The packed form of `batch` matrices [rows, cols] under quantiser d.
+int check_packed(const fq_qdesc* d, int64_t cols, const uint8_t* codes, const uint8_t* block_codes, const float* scale,
+                 const float* tensor_scale, PackedW* w) {
+    QParams q;
+    int s = check_qdesc(d, &q);
+    if (s != FQ_OK || (s = check_packed_format(q, cols)) != FQ_OK) return s;
     if (!codes) return FQ_E_INVALID;
     if (q.kind == FQ_NVFP4 ? (!block_codes || !tensor_scale || scale) : (!scale || block_codes || tensor_scale))
         return FQ_E_INVALID;
@@ -217,8 +221,10 @@ bool packed_act(const QParams& a) {
 }
 
 int check_packed_layer(const fq_layer_desc* L, LayerQ* q) {
-    const int s = check_layer(L, q);
-    if (s != FQ_OK) return s;
+    int s = check_layer(L, q);
+    if (s != FQ_OK || (s = check_packed_format(q->w1, L->H)) != FQ_OK ||
+        (s = check_packed_format(q->w2, L->I)) != FQ_OK)
+        return s;
     if (!packed_act(q->a1) || !packed_act(q->a2) || L->T * L->topk > PACKED_MAX_ROWS) return FQ_E_UNSUPPORTED;
     return FQ_OK;
 }

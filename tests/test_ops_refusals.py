@@ -204,3 +204,17 @@ def test_head_loss_of_no_tokens_needs_no_workspace():
     for kw in (dict(), dict(k=4), dict(lab=None), dict(grad=FAKE)):
         assert _hl(**{**dict(T=0, h=None, w=None, lab=None, ws=None, wsb=0), **kw}) == F.FQ_E_HIP, kw
     assert _hl(T=0, h=None, w=None, lab=None, ws=None, wsb=0, loss=None) == F.FQ_E_INVALID
+
+
+def test_packed_expert_workspace_of_formats_that_the_layer_refuses():
+    # 0 for every descriptor that the call itself refuses
+    w1, w2, a1, a2 = F.preset("w4a16")
+    row8 = F.qdesc(F.FQ_INT, F.FQ_PER_ROW, 0, F.FQ_LEARNABLE, -128, 127)
+    g16 = F.qdesc(F.FQ_INT, F.FQ_PER_GROUP, 16, F.FQ_LEARNABLE, -8, 7)
+    wide = F.qdesc(F.FQ_INT, F.FQ_PER_ROW, 0, F.FQ_LEARNABLE, -9, 5)
+    for quants in ((row8, w2, a1, a2), (w1, row8, a1, a2), (g16, w2, a1, a2), (w1, wide, a1, a2), (F.qdesc(), w2, a1, a2),
+                   (w1, F.qdesc(F.FQ_FP8E4M3, F.FQ_PER_ROW), a1, a2)):
+        assert _pe(quants=quants) == F.FQ_E_UNSUPPORTED
+        assert F.packed_expert_workspace_size(F.layer_desc(8, 256, 128, 4, 2, *quants)) == 0
+    for fmt in ("nvfp4", "nvfp4a16", "w4a16", "w4afp8"):
+        assert F.packed_expert_workspace_size(F.layer_desc(8, 256, 128, 4, 2, *F.preset(fmt))) > 0
