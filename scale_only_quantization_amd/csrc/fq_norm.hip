@@ -75,7 +75,7 @@ __global__ __launch_bounds__(tpb(TPR)) void k_norm_fwd(NormArgs a) {
     __shared__ double red64[TPR / WAVE];
     __shared__ float red[TPR / WAVE];
     const int tid = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * (tpb(TPR) / TPR) + threadIdx.x / TPR;
+    const int64_t row = block_id() * (tpb(TPR) / TPR) + threadIdx.x / TPR;
     if (row >= a.rows) return;                     // whole waves; whole blocks where a row spans waves
     const int nvec = a.cols >> 3;
     const uint4* xr = reinterpret_cast<const uint4*>(a.x + row * a.cols);
@@ -304,7 +304,7 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st) {
     return by_shape(a.rows, a.cols, [&](auto tpr_c, auto nv_c) {
         constexpr int TPR = decltype(tpr_c)::value, NV = decltype(nv_c)::value;
         constexpr int RPB = tpb(TPR) / TPR;
-        const dim3 grid((unsigned)((a.rows + RPB - 1) / RPB)), block(tpb(TPR));
+        const dim3 grid = grid_of((a.rows + RPB - 1) / RPB), block(tpb(TPR));
         if (a.q.kind == K_NONE) hipLaunchKernelGGL((k_norm_fwd<TPR, NV, K_NONE>), grid, block, 0, st, a);
         else if (a.q.kind == K_INT) hipLaunchKernelGGL((k_norm_fwd<TPR, NV, K_INT>), grid, block, 0, st, a);
         else hipLaunchKernelGGL((k_norm_fwd<TPR, NV, K_FP8>), grid, block, 0, st, a);

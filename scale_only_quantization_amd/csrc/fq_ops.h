@@ -9,6 +9,15 @@
 
 namespace fq {
 
+// Blocks of a launch whose number the call decides: HIP takes fewer than 2^32
+// threads along x, so past GRID_X blocks they go on along z, and the last row of
+// the grid may hold blocks past the end, which have nothing to do.
+constexpr int64_t GRID_X = 1 << 20;
+inline dim3 grid_of(int64_t blocks, unsigned y = 1) {
+    return dim3((unsigned)(blocks < GRID_X ? blocks : GRID_X), y, (unsigned)((blocks + GRID_X - 1) / GRID_X));
+}
+__device__ __forceinline__ int64_t block_id() { return (int64_t)blockIdx.z * GRID_X + blockIdx.x; }
+
 // --------------------------------------------------------------- RMS norm ---
 struct NormArgs {
     QParams q;             // kind K_NONE: no codes

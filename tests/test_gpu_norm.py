@@ -183,3 +183,22 @@ def test_zero_rows():
                    workspace=T.empty(64, dtype=T.float32, device="cuda"))
     T.cuda.synchronize()
     assert not from_dev(dg).any()
+
+
+def test_more_blocks_than_one_grid_row():
+    # 2^26 + 7 short rows: four rows a block of 256 threads are more than 2^32 threads
+    F, T = _F(), torch()
+    R, C = (1 << 26) + 7, 8
+    x = T.randn((R, C), device="cuda", dtype=T.bfloat16)
+    g = T.linspace(0.5, 1.5, C, device="cuda").to(T.bfloat16)
+    y, r = T.full_like(x, 7), T.full((R + 1,), -1.0, device="cuda")
+    F.rms_norm_fwd(x, g, EPS, y=y, rstd=r[:R])
+    T.cuda.synchronize()
+    rng = np.random.default_rng(1)
+    edge = [(i << 22) + j for i in range(17) for j in range(-5, 6)]        # where the grid's rows of blocks meet
+    pick = np.unique(np.clip(np.concatenate([edge, rng.integers(0, R, 5000), [0, R - 1, R - 5, R - 6]]), 0, R - 1))
+    at = to_dev(pick.astype(np.int64))
+    _, ref, rr = ON.forward(from_dev(x[at]), from_dev(g), EPS)
+    assert_bits_equal(from_dev(y[at]), ref, "y")
+    np.testing.assert_allclose(from_dev(r[at]), rr, rtol=2.0 ** -23)
+    assert float(r[R]) == -1.0 and bool((r[:R] > 0).all())                 # no row left out, none past the end
