@@ -184,8 +184,9 @@ __device__ __forceinline__ bool counts(const HeadArgs& a, int64_t t) {
 __global__ __launch_bounds__(256) void k_head_sparse(HeadArgs a) {
     __shared__ float sz[65];
     __shared__ int red[4];
-    const int64_t t = blockIdx.x;
+    const int64_t t = block_id();
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    if (t > a.T) return;
     if (t == a.T) {
         int n = 0;
         for (int64_t r = threadIdx.x; r < a.T; r += 256) n += counts(a, r) ? 1 : 0;
@@ -660,7 +661,7 @@ hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t 
         a.vc = pl.vc;
         a.splits = pl.splits;
         a.ksplit = pl.ksplit;
-        hipLaunchKernelGGL(k_head_sparse, dim3((unsigned)a.T + 1), dim3(256), 0, st, a);
+        hipLaunchKernelGGL(k_head_sparse, grid_of(a.T + 1), dim3(256), 0, st, a);
         hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
         for (int i = 0; i < pl.pieces; ++i) {

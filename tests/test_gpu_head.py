@@ -217,3 +217,42 @@ def test_no_tokens_without_workspace():
         out = T_.full((1,), 9.0, device="cuda")
         F.head_loss(F.head_desc(0, 64, 100, k), z, w, out, grad=z)
         assert from_dev(out)[0] == 0
+
+
+def test_the_most_tokens():
+    # 2^24 - 1 tokens, the most of the contract: their sparse logits and the
+    # count of rows take 2^24 blocks, 2^32 threads; two pieces of the vocabulary
+    F, T_ = _F(), torch()
+    T, H, V, k = (1 << 24) - 1, 64, 300, 2
+    g = T_.Generator(device="cuda")
+    g.manual_seed(12)
+    h = T_.randn((T, H), generator=g, device="cuda", dtype=T_.bfloat16)
+    w = (T_.randn((V, H), generator=g, device="cuda") * 0.25).to(T_.bfloat16)
+    lab = T_.randint(0, V, (T,), generator=g, device="cuda", dtype=T_.int32)
+    lab[::7] = -1
+    ti = T_.randint(0, V, (T, k), generator=g, device="cuda", dtype=T_.int32)
+    tv = T_.randn((T, k), generator=g, device="cuda")
+    d = F.head_desc(T, H, V, k, 0.8, 1.2)
+    loss, rows = T_.empty(1, device="cuda"), T_.full((T,), -9.0, device="cuda")
+    grad = T_.full((T, H), 9.0, dtype=T_.bfloat16, device="cuda")
+    ws = T_.full((F.head_loss_workspace_size(d),), 255, dtype=T_.uint8, device="cuda")
+    F.head_loss(d, h, w, loss, top_v=tv, top_i=ti, labels=lab, row_loss=rows, grad=grad, workspace=ws)
+    T_.cuda.synchronize()
+    counted = int((lab >= 0).sum())
+    rng = np.random.default_rng(3)
+    pick = np.unique(np.concatenate([rng.integers(0, T, 200), [0, 1, T - 1, T - 2, T - 3], (1 << 20) * np.arange(1, 16),
+                                     (1 << 20) * np.arange(1, 16) - 1]))
+    at = to_dev(pick.astype(np.int64))
+    hh, ww, ll, vv, ii = from_dev(h[at]), from_dev(w), from_dev(lab[at]), from_dev(tv[at]), from_dev(ti[at])
+    _, ref, ref_grad, (rest, full) = head(hh, ww, vv, ii, ll, 0.8, 1.2)
+    live = ll >= 0
+    n = counted / live.sum()                                   # the oracle's mean is over the picked rows that count
+    ez = (H / 16 + 18) * 2.0 ** -24 * (np.abs(hh.astype(np.float64)) @ np.abs(ww.astype(np.float64)).T).max(-1)
+    err = np.abs(from_dev(rows[at]) - ref)                     # the bounds of _check
+    assert np.all(err <= 2.0 * (2 * ez + 2.0 ** -20 + 4 * 2.0 ** -24 * np.abs(ref)) + 2.0 ** -22)
+    # and of 1/n: its own rounding and the count's, 2^-23 of each value, in the room of 2^-18 of the terms
+    tol = (2.0 ** -8 * np.abs(ref_grad) + 2.0 ** -8 * rest + (4 * ez[:, None] + 2.0 ** -18) * full) / n + 1e-38
+    assert np.all(np.abs(from_dev(grad[at]) - ref_grad / n) <= tol)
+    assert bool((rows[::7] == 0).all()) and bool((rows >= -1e-3).all())
+    mean = float(rows.double().sum() / counted)
+    assert abs(from_dev(loss)[0] - mean) <= 2.0 ** -22 * mean  # 1/n and the loss, one rounding each
