@@ -492,6 +492,7 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
  *
  *   q            host; INT with a 4-bit range and scales per row or per group
  *                (32 .. 512), or NVFP4; the source does not matter.
+ *   batch, rows  1 .. 2^31 - 1.
  *   codes        device u8 [batch, rows, cols/2], 16-B aligned; cols % 32 == 0,
  *                cols <= 65536.
  *   block_codes  device u8 [batch, rows, cols/16], 2-B aligned, NVFP4 only, else NULL.

@@ -530,7 +530,8 @@ template <int FMT, int MT, int NT, int KW>
 __global__ __launch_bounds__(64 * KW) void k_matvec(MatvecArgs a) {
     __shared__ Reduce<MT, NT, KW> red;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t n0 = (int64_t)blockIdx.x * 16 * NT;
+    const int64_t n0 = block_id() * 16 * NT;
+    if (n0 >= a.N) return;
     const int m0 = blockIdx.y * 16 * MT;
     uint32_t vx[MT];
 #pragma unroll
@@ -558,7 +559,8 @@ __global__ __launch_bounds__(64 * KW) void k_matvec_which(MatvecArgs a) {
     __shared__ int ids[PACKED_MAX_ROWS], list[PACKED_MAX_ROWS];
     __shared__ int count;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r0 = blockIdx.y;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t n0 = block_id() * 16;
+    if (n0 >= a.N) return;
     for (int i = threadIdx.x; i < a.M; i += 64 * KW) ids[i] = a.which[i];
     __syncthreads();
     const int e = ids[r0];
@@ -810,17 +812,17 @@ template <int FMT, int KW>
 hipError_t run_matvec(const MatvecArgs& a, hipStream_t st) {
     const unsigned tiles = (unsigned)((a.N + 15) / 16);
     if (a.which)
-        hipLaunchKernelGGL((k_matvec_which<FMT, KW>), dim3(tiles, (unsigned)a.M), dim3(64 * KW), 0, st, a);
+        hipLaunchKernelGGL((k_matvec_which<FMT, KW>), grid_of(tiles, (unsigned)a.M), dim3(64 * KW), 0, st, a);
     else if (a.M > 16)
-        hipLaunchKernelGGL((k_matvec<FMT, 2, 2, KW>), dim3((tiles + 1) / 2, (unsigned)((a.M + 31) / 32)), dim3(64 * KW),
-                           0, st, a);
+        hipLaunchKernelGGL((k_matvec<FMT, 2, 2, KW>), grid_of((tiles + 1) / 2, (unsigned)((a.M + 31) / 32)),
+                           dim3(64 * KW), 0, st, a);
     else {
         unsigned best = 0, least = 0;
         for (unsigned n = 1; n <= 4; ++n) {
             const unsigned cost = ((tiles + n - 1) / n + 255) / 256 * (4 + 3 * n);
             if (best == 0 || cost < least) best = n, least = cost;
         }
-        const dim3 grid((tiles + best - 1) / best), block(64 * KW);
+        const dim3 grid = grid_of((tiles + best - 1) / best), block(64 * KW);
         if (best == 1) hipLaunchKernelGGL((k_matvec<FMT, 1, 1, KW>), grid, block, 0, st, a);
         else if (best == 2) hipLaunchKernelGGL((k_matvec<FMT, 1, 2, KW>), grid, block, 0, st, a);
         else if (best == 3) hipLaunchKernelGGL((k_matvec<FMT, 1, 3, KW>), grid, block, 0, st, a);

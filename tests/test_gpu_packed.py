@@ -323,3 +323,31 @@ def test_experts_of_every_scale_layout(wf, E, H, I, T, k):
     err = np.linalg.norm(got - ref) / np.linalg.norm(ref)
     assert err <= 2.0 ** -7, f"{err:.2e}"                    # as for the presets above
     np.testing.assert_array_equal(run(slice(T // 2, T // 2 + 1))[0], got[T // 2])
+
+
+@pytest.mark.parametrize("N,by_matrix,M", [((1 << 28) + 37, True, 2), ((1 << 29) + 37, False, 17),
+                                           ((1 << 30) + 37, False, 1)])
+def test_more_blocks_than_one_grid_row(N, by_matrix, M):
+    # matrices so long that their blocks are 2^32 threads and more, in each of
+    # the launches; the longest has 17 GB of codes
+    F, T = _F(), torch()
+    K = 32
+    codes = T.empty((1, N, K // 2), dtype=T.uint8, device="cuda").random_(0, 256)
+    scale = T.rand((1, N), device="cuda")
+    x = T.randn((M, K), device="cuda").to(T.bfloat16)
+    y = T.full((M, N), float("nan"), dtype=T.bfloat16, device="cuda")
+    which = T.zeros(M, dtype=T.int32, device="cuda") if by_matrix else None
+    F.packed_matvec(F.qdesc(F.FQ_INT, F.FQ_PER_ROW, 0, F.FQ_LEARNABLE, -8, 7), codes, x, y, scale=scale, which=which)
+    T.cuda.synchronize()
+    rng = np.random.default_rng(2)
+    step = 16 << 20                                        # rows of a full row of blocks, one tile each
+    meet = np.arange(step, N, step)[:, None] + np.arange(-3, 4)
+    pick = np.unique(np.concatenate([rng.integers(0, N, 3000), meet.ravel(), [0, 1, N - 1, N - 2, N - 40]]))
+    at = to_dev(pick.astype(np.int64))
+    W = OPK.dequant(from_dev(codes[:, at]), scale=from_dev(scale[:, at]))[0]
+    xs = from_dev(x).astype(np.float64)
+    ref = xs @ W.T
+    # one rounding to bf16; 32 products of up to 143 |x| s and the 136's as many, one matrix sum each and the scale
+    tol = 2.0 ** -8 * np.abs(ref) + 16 * 2.0 ** -24 * 280 * np.abs(xs).sum(1, keepdims=True) * from_dev(scale[0, at])
+    assert np.all(np.abs(from_dev(y[:, at]) - ref) <= tol)
+    assert not bool(T.isnan(y.sum()))                      # no row left out
