@@ -516,7 +516,8 @@ int fq_packed_matvec(const fq_qdesc* q, int64_t batch, int64_t rows, int64_t col
  *     x^ = fq_a1,e(x[t]),  z1 = x^ W1[e]^T (fp32),  h^ = fq_a2,e(bf16(silu(g) u))
  *     y[t] = bf16(sum_j topk_w[t, j] h^ W2[e]^T)
  * as in training, except that W, z1 and the experts' outputs are not rounded
- * to bf16 on the way. */
+ * to bf16 on the way.  Alignments as in fq_packed_matvec: codes 16 bytes, block
+ * codes 2. */
 typedef struct {
     const uint8_t* w1_codes;        /* device u8 [E, 2I, H/2]                            */
     const uint8_t* w1_block_codes;  /* device u8 [E, 2I, H/16], NVFP4, else NULL         */
@@ -532,7 +533,8 @@ typedef struct {
 /* Bytes of device workspace (256-B aligned), 0 on a descriptor that is not supported. */
 size_t fq_packed_expert_workspace_size(const fq_layer_desc* L);
 /* x device bf16 [T, H]; topk_ids device int32 [T, topk]; topk_w device fp32
- * [T, topk]; y device bf16 [T, H], not x.  Errors as fq_grouped_expert_fwd. */
+ * [T, topk]; y device bf16 [T, H], not x; x and y 16-B aligned.  Errors as
+ * fq_grouped_expert_fwd. */
 int fq_packed_expert_fwd(const fq_layer_desc* L, const fq_packed_experts* P, const void* x, const int32_t* topk_ids,
                          const float* topk_w, void* y, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -96,6 +96,7 @@ struct PackedW {           // a stack of matrices as fq_tensor's codes
     int K;                 // a multiple of 32
     int group;             // INT: columns per scale (at least 128 where one per row)
     int spr;               // INT: scales per row
+    int b8;                // NVFP4: a chunk's block codes (8 bytes) are 8-byte aligned in every row
     int gshift;            // INT: chunk >> gshift (groups from 128), 32-column segment >> gshift (below) is its scale
 };
 struct MatvecArgs {

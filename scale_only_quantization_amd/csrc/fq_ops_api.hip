@@ -205,6 +205,7 @@ int check_packed(const fq_qdesc* d, int64_t cols, const uint8_t* codes, const ui
     w->K = (int)cols;
     w->group = q.gran == FQ_PER_GROUP ? q.group : (int)(cols > 128 ? cols : 128);
     w->spr = q.gran == FQ_PER_GROUP ? (int)(cols / q.group) : 1;
+    w->b8 = cols % 128 == 0 && aligned(block_codes, 8);
     w->gshift = 30;
     if (q.gran == FQ_PER_GROUP)
         for (w->gshift = 0; (q.group < 128 ? 32 : 128) << w->gshift < q.group;) ++w->gshift;

@@ -130,6 +130,16 @@ __device__ __forceinline__ void spread4(uint32_t v, uint32_t (&o)[4]) {
     o[3] = b[1];
 }
 
+// The eight block codes of a chunk: one load where they are 8-byte aligned, else
+// (rows of any even number of them, or a stack that begins between) one per two.
+__device__ __forceinline__ u32x2 load_factors(const PackedW& w, __amdgpu_buffer_rsrc_t rs, uint32_t at, uint32_t os) {
+    if (w.b8) return __builtin_amdgcn_raw_buffer_load_b64(rs, at, os, 0);
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __builtin_amdgcn_raw_buffer_load_b16(rs, at + 2 * i, os, 0);
+    return u32x2{h[0] | h[1] << 16, h[2] | h[3] << 16};
+}
+
 // A slab of a tile's codes and scales, as loaded.
 template <int FMT>
 struct Slab {
@@ -142,17 +152,9 @@ struct Slab {
 #pragma unroll
         for (int u = 0; u < XC; ++u) q[u] = __builtin_amdgcn_raw_buffer_load_b128(r.codes, r.vc, oc + u * 64, 0);
         if (FMT == NVFP4) {
-            if ((w.K & 127) == 0) {
-                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r.scale, r.vs + cg * 8, os, 0);
-                s[0] = v.x;
-                s[1] = v.y;
-            } else {                                  // rows of any even number of block codes
-                uint32_t h[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = __builtin_amdgcn_raw_buffer_load_b16(r.scale, r.vs + cg * 8 + 2 * i, os, 0);
-                s[0] = h[0] | h[1] << 16;
-                s[1] = h[2] | h[3] << 16;
-            }
+            const u32x2 v = load_factors(w, r.scale, r.vs + cg * 8, os);
+            s[0] = v.x;
+            s[1] = v.y;
         } else {
 #pragma unroll
             for (int i = 0; i < NS; ++i)
@@ -353,8 +355,8 @@ struct PairSlab {
 #pragma unroll
         for (int u = 0; u < XC; ++u)
             q[u] = __builtin_amdgcn_raw_buffer_load_b128(r.codes, r.vc, oc + (u >> 1) * 128 + (u & 1) * 8 * r.cb, 0);
-        if (FMT == NVFP4) {                               // the layer's columns are multiples of 128
-            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r.scale, r.vs + cg * 8, os, 0);
+        if (FMT == NVFP4) {
+            const u32x2 v = load_factors(w, r.scale, r.vs + cg * 8, os);
             s[0] = v.x;
             s[NS - 1] = v.y;
         } else {

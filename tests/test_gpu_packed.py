@@ -351,3 +351,39 @@ def test_more_blocks_than_one_grid_row(N, by_matrix, M):
     tol = 2.0 ** -8 * np.abs(ref) + 16 * 2.0 ** -24 * 280 * np.abs(xs).sum(1, keepdims=True) * from_dev(scale[0, at])
     assert np.all(np.abs(from_dev(y[:, at]) - ref) <= tol)
     assert not bool(T.isnan(y.sum()))                      # no row left out
+
+
+def _at_offset(a, off):
+    """numpy uint8 array on the GPU, `off` bytes past an aligned address."""
+    T = torch()
+    buf = T.full((a.size + 16,), 0x7F, dtype=T.uint8, device="cuda")       # NaN factors around it
+    v = buf[off:off + a.size].view(a.shape)
+    v.copy_(to_dev(a))
+    assert v.data_ptr() % 8 == off % 8
+    return v
+
+
+@pytest.mark.parametrize("off", [2, 4, 6, 8])
+def test_block_codes_two_byte_aligned(off):
+    # the contract asks for 2 bytes; whole chunks (K % 128 == 0) are loaded 8
+    # bytes at a time where the address allows it.  The same bits either way
+    F, T = _F(), torch()
+    for K, M, which in ((256, 3, None), (2304, 20, None), (256, 5, np.array([1, 0, 2, 1, 1], np.int32)), (160, 2, None)):
+        E, N = (1 if which is None else 3), 50
+        q, w, _ = _weights(K + M, "nvfp4", E, N, K)
+        x = bf16_rne(np.random.default_rng(M).standard_normal((M, K)).astype(np.float32))
+        want = _matvec(q, w, x, which, N)
+        y = T.empty((M, N), dtype=T.bfloat16, device="cuda")
+        F.packed_matvec(q, to_dev(w["codes"]), to_dev_bf16(x), y, block_codes=_at_offset(w["block_codes"], off),
+                        tensor_scale=to_dev(w["tensor_scale"]), which=None if which is None else to_dev(which))
+        np.testing.assert_array_equal(from_dev(y), want)
+    for T_tok in (1, 9, 200):                              # both splits of the columns
+        d = _layer(T_tok, "nvfp4", 8, 384, 256, T_tok, 4)
+        want = _run(d)
+        dev = [dict(codes=to_dev(w["codes"]), tensor_scale=to_dev(w["tensor_scale"]),
+                    block_codes=_at_offset(w["block_codes"], off)) for w in (d["w1"], d["w2"])]
+        y = T.empty((T_tok, 384), dtype=T.bfloat16, device="cuda")
+        F.packed_expert_fwd(d["L"], F.packed_experts(*dev, to_dev(d["s1"]), to_dev(d["s2"])), to_dev_bf16(d["x"]),
+                            to_dev(d["ids"]), to_dev(d["tw"]), y,
+                            T.empty(F.packed_expert_workspace_size(d["L"]), dtype=T.uint8, device="cuda"))
+        np.testing.assert_array_equal(from_dev(y), want)
