@@ -130,3 +130,20 @@ def check_scale_grad(got, ref, abs_sum, what="", rel=2e-3):
     assert bad.size == 0, (f"{what}: {bad.size} of {ref.size} beyond tolerance; first {bad[:5]}: "
                            f"got {got[bad[:5]]} ref {ref[bad[:5]]}")
     assert np.linalg.norm(got - ref) <= rel * max(np.linalg.norm(ref), 1e-30), f"{what}: norm-wise"
+
+
+def int4_bound(x, W, scale, ref):
+    """Error of a product y[m, n] of bf16 x [M, K] with INT4 weights W [N, K] = q s, s of shape [N, K/g] or [N], in
+    the kernel's arithmetic, group by group.
+
+    Codes enter as 136 + q and 136 x comes off again, so of a chunk of up to 128 columns under one scale the
+    matrix instructions add up to (136 + 144) |x| a column, at most eight of them in a chain (four that take the
+    136 off, four with the codes), whose sums are off by at most two half ulps each: 16 * 2^-24 of the chunk's
+    sum.  The scale's product and the sum over the chunks (at most K/32 of them, and the waves' eight) then work
+    on values of up to 8 |x| s: one half ulp each.  Last the output's rounding to bf16."""
+    x, W, ref = (np.asarray(a, np.float64) for a in (x, W, ref))
+    N, K = W.shape
+    s = np.asarray(scale, np.float64).reshape(N, -1)
+    ax = np.abs(x).reshape(x.shape[0], s.shape[1], K // s.shape[1]).sum(-1)   # [M, groups]
+    sx = ax @ s.T                                                           # sum of s |x|
+    return 2.0 ** -8 * np.abs(ref) + 2.0 ** -24 * (16 * 280 + (K / 32 + 10) * 8) * sx + 1e-30

@@ -6,7 +6,7 @@ import pytest
 from oracle import packed as OPK
 from oracle import presets as OP
 from oracle.numerics import bf16_rne
-from tests.fq_testutil import check_gemm, from_dev, to_dev, to_dev_bf16, torch
+from tests.fq_testutil import check_gemm, from_dev, int4_bound, to_dev, to_dev_bf16, torch
 
 pytestmark = pytest.mark.gpu
 
@@ -387,3 +387,98 @@ def test_block_codes_two_byte_aligned(off):
                             to_dev(d["ids"]), to_dev(d["tw"]), y,
                             T.empty(F.packed_expert_workspace_size(d["L"]), dtype=T.uint8, device="cuda"))
         np.testing.assert_array_equal(from_dev(y), want)
+
+
+@pytest.mark.parametrize("fmt", ["row", "g32", "g64", "g128", "g512"])
+@pytest.mark.parametrize("N,K,M,E", [(65, 8192, 13, 1), (257, 2176, 3, 1), (33, 4096, 17, 1), (48, 512, 64, 1),
+                                     (12301, 2560, 1, 1), (9001, 1536, 16, 1), (50, 4608, 9, 3), (17, 1024, 1, 2)])
+def test_int4_within_each_groups_bound(fmt, N, K, M, E):
+    # a bound tight enough that 32 lost columns or a wrong scale exceed it (shown on the CPU, test_oracle_packed.py)
+    g = int(fmt[1:]) if fmt[0] == "g" else 32
+    K = -(-K // g) * g
+    q, w, W = _weights(N + K, fmt, E, N, K)
+    rng = np.random.default_rng(M)
+    x = bf16_rne((rng.standard_normal((M, K)) + 0.3).astype(np.float32))
+    which = rng.integers(0, E, M).astype(np.int32) if E > 1 else None
+    got = _matvec(q, w, x, which, N)
+    for e in range(E):
+        rows = slice(None) if which is None else which == e
+        ref = x[rows].astype(np.float64) @ W[e].T
+        tol = int4_bound(x[rows], W[e], w["scale"][e], ref)
+        err = np.abs(got[rows] - ref)
+        assert np.all(err <= tol), f"matrix {e}: {(err > tol).sum()} of {err.size}, worst {(err / tol).max():.2f}"
+
+
+def _layer_of(seed, E, H, I, T, k, f1, f2, s1=None, s2=None):
+    """Weights of formats f1 and f2 with z of order one, tokens, and the activation scales."""
+    q1, w1, W1 = _weights(seed, f1, E, 2 * I, H)
+    q2, w2, W2 = _weights(seed + 1, f2, E, H, I)
+    for f, w, W, n in ((f1, w1, W1, H), (f2, w2, W2, I)):
+        w["tensor_scale" if f == "nvfp4" else "scale"] *= np.float32(1.0 / (np.sqrt(np.mean(W ** 2)) * np.sqrt(n)))
+    rng = np.random.default_rng(seed + 2)
+    return dict(q=(q1, q2), w1=w1, w2=w2, x=bf16_rne(rng.standard_normal((T, H)).astype(np.float32)),
+                ids=np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32),
+                tw=rng.random((T, k)).astype(np.float32), s1=s1, s2=s2)
+
+
+def _check_layer_of(d, a1, a2, qa1, qa2):
+    """The layer on d under activation quantisers a1, a2 (oracle) and qa1, qa2 (descriptors); a token alone too."""
+    F, T_ = _F(), torch()
+    E, I, H = d["w2"]["codes"].shape[0], d["w2"]["codes"].shape[2] * 2, d["x"].shape[1]
+    P = F.packed_experts(*({n: to_dev(v) for n, v in w.items()} for w in (d["w1"], d["w2"])),
+                         *(None if s is None else to_dev(s) for s in (d["s1"], d["s2"])))
+
+    def run(rows):
+        x, ids, tw = d["x"][rows], d["ids"][rows], d["tw"][rows]
+        L = F.layer_desc(E, H, I, len(x), ids.shape[1], *d["q"], qa1, qa2)
+        y = T_.empty((len(x), H), dtype=T_.bfloat16, device="cuda")
+        ws = T_.full((F.packed_expert_workspace_size(L),), 255, dtype=T_.uint8, device="cuda")
+        F.packed_expert_fwd(L, P, to_dev_bf16(x), to_dev(ids), to_dev(tw), y, ws)
+        T_.cuda.synchronize()
+        return from_dev(y)
+
+    got = run(slice(None))
+    ref = OPK.experts(OPK.dequant(**d["w1"]), OPK.dequant(**d["w2"]), d["x"], d["ids"], d["tw"], a1, d["s1"], a2, d["s2"])
+    check_gemm(got, ref)
+    err = np.linalg.norm(got - ref) / np.linalg.norm(ref)
+    assert err <= 2.0 ** -7, f"{err:.2e}"                    # as in _check_layer
+    t = len(d["x"]) // 2
+    np.testing.assert_array_equal(run(slice(t, t + 1))[0], got[t])
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "w4a16", "w4afp8"])
+@pytest.mark.parametrize("E,H,I,T,k", [(3, 4096, 128, 8, 3), (2, 8192, 128, 5, 2), (2, 128, 8192, 5, 2),
+                                       (2, 256, 4096, 12, 2), (2, 4224, 2176, 4, 1), (4, 8192, 1024, 1, 2)])
+def test_experts_of_wide_layers(fmt, E, H, I, T, k):
+    # hidden and intermediate sizes past 2048: as few as one row of x in LDS at
+    # a time, so that a group's rows take several passes over its weights
+    d = _layer(E + H + T, fmt, E, H, I, T, k)
+    got = _run(d)
+    _check_layer(d, got, f"{fmt} E={E} H={H} I={I} T={T} k={k}")
+    np.testing.assert_array_equal(_run(d, slice(T // 2, T // 2 + 1))[0], got[T // 2])
+
+
+@pytest.mark.parametrize("wf", ["nvfp4", "g64"])
+@pytest.mark.parametrize("E,H,I,T,k", [(8, 256, 128, 1, 2), (4, 384, 256, 40, 3), (8, 384, 256, 200, 4)])
+@pytest.mark.parametrize("which", ["both", "first", "second"])
+def test_experts_with_int8_activations(wf, E, H, I, T, k, which):
+    # one INT8 scale per expert in front of either product; both splits of the columns
+    from oracle.codec import QSpec
+    F = _F()
+    rng = np.random.default_rng(E + T)
+    s1 = ((3.5 + rng.random(E)) / 127).astype(np.float32) if which != "second" else None
+    s2 = ((2.5 + rng.random(E)) / 127).astype(np.float32) if which != "first" else None
+    d = _layer_of(5 * E + T, E, H, I, T, k, wf, wf, s1, s2)
+    a, qa = QSpec("int", "tensor", 0, "learnable", -128, 127), F.qdesc(F.FQ_INT, F.FQ_PER_TENSOR, 0, F.FQ_LEARNABLE, -128, 127)
+    none = QSpec()
+    _check_layer_of(d, a if s1 is not None else none, a if s2 is not None else none,
+                    qa if s1 is not None else F.qdesc(), qa if s2 is not None else F.qdesc())
+
+
+@pytest.mark.parametrize("f1,f2", [("nvfp4", "g128"), ("g32", "nvfp4"), ("row", "g64"), ("g512", "row")])
+@pytest.mark.parametrize("T", [1, 6, 170])
+def test_experts_of_two_weight_formats(f1, f2, T):
+    from oracle.codec import QSpec
+    F = _F()
+    d = _layer_of(T, 6, 512, 256, T, 3, f1, f2)
+    _check_layer_of(d, QSpec(), QSpec(), F.qdesc(), F.qdesc())

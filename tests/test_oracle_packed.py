@@ -55,3 +55,29 @@ def test_experts_by_brute_force():
                 h.append(float(bf16_rne(np.array([g / (1 + np.exp(-g)) * u], np.float32))[0]))
             ref += tw[t, j] * np.array([sum(W2[ids[t, j], n, i] * h[i] for i in range(I)) for n in range(H)])
         np.testing.assert_allclose(y[t], ref, rtol=1e-12)
+
+
+@pytest.mark.parametrize("g", [32, 64, 128, 512, 0], ids=lambda g: f"g{g}" if g else "row")
+@pytest.mark.parametrize("N,K,M", [(65, 8192, 13), (257, 2048, 3), (48, 512, 64)])
+def test_the_int4_bound_sees_a_lost_segment_and_a_wrong_scale(N, K, M, g):
+    # the bound that the GPU's INT4 products are held to, against results with
+    # a mistake: 32 columns left out, and one group under its neighbour's scale
+    from tests.fq_testutil import int4_bound
+    rng = np.random.default_rng(N)
+    codes = rng.integers(0, 256, (1, N, K // 2)).astype(np.uint8)
+    s = (rng.random((1, N, K // g) if g else (1, N)) * 0.01 + 1e-3).astype(np.float32)
+    x = bf16_rne((rng.standard_normal((M, K)) + 0.3).astype(np.float32)).astype(np.float64)
+    W = OPK.dequant(codes, scale=s)[0]
+    ref = x @ W.T
+    tol = int4_bound(x, W, s[0], ref)
+    assert np.all(np.abs(bf16_rne(ref.astype(np.float32)) - ref) <= tol)     # the right result, rounded
+    lost = W.copy()
+    lost[:, K - 32:] = 0
+    # half of all results and more must be seen to be wrong: 32 columns are of the order of 5 s sqrt(32) = 28 s
+    assert np.mean(np.abs(x @ lost.T - ref) > tol) > 0.5
+    if g:
+        swap = s.copy()
+        swap[:, :, -1] = s[:, :, -2] if s.shape[2] > 1 else 0
+        # neighbours differ by 0.004 of 0.006 (rms), at times by nearly nothing: with groups of 32 of 8192 columns
+        # the change is 0.004 * 4.6 * sqrt(32) = 0.1 (rms) against bounds of 0.02 to 0.06, so a quarter must be seen
+        assert np.mean(np.abs(x @ OPK.dequant(codes, scale=swap)[0].T - ref) > tol) > 0.25
