@@ -256,3 +256,82 @@ def test_the_most_tokens():
     assert bool((rows[::7] == 0).all()) and bool((rows >= -1e-3).all())
     mean = float(rows.double().sum() / counted)
     assert abs(from_dev(loss)[0] - mean) <= 2.0 ** -22 * mean  # 1/n and the loss, one rounding each
+
+
+def _piece(F, T, H, V, k):
+    """Vocabulary entries of a piece: without the gradient the workspace grows by 8 bytes per token and 64 entries
+    of a piece, a piece has whole multiples of 256, and 256 where the vocabulary is no longer."""
+    size = lambda v: F.head_loss_workspace_size(F.head_desc(T, H, v, k), grad=False)  # noqa: E731
+    assert T * 32 % 256 == 0                                    # the parts' rounding up takes no share in the difference
+    return 256 + (size(V) - size(max(k, 1))) * 64 // (8 * T)
+
+
+def _many_pieces(seed, T, H, V, k, far):
+    """Numpy inputs of several pieces: labels and teacher ids from 72 entries that lie at both ends of every piece
+    and between, and whose logits stand out, so that each has about a hundredth of a token's probability; with `far`
+    later entries reach ever higher instead, hundreds of binary orders above those."""
+    F = _F()
+    vc = _piece(F, T, H, V, k)
+    ends = [e for p in range(0, V, vc) for e in (p, p + 1, min(p + vc, V) - 1, min(p + vc, V) - 2)]
+    assert vc < V
+    rng = np.random.default_rng(seed)
+    special = np.array(sorted(set(ends) | set(rng.integers(0, V, 72 - len(set(ends))).tolist())), np.int32)
+    w = rng.standard_normal((V, H)).astype(np.float32)
+    h = rng.standard_normal((T, H)).astype(np.float32)
+    if far:
+        w *= np.linspace(1.0, 25.0, V, dtype=np.float32)[:, None]
+    else:
+        # logits of standard deviation 0.5; the special ones 8 and, in all, as much again as half of the others
+        w *= np.float32(0.5 / np.sqrt(H))
+        h[:, 0] = 4.0
+        w[special, 0] = (8.0 + np.log(V / 7e4)) / 4.0
+    w, h = bf16_rne(w), bf16_rne(h)
+    pick = np.argsort(rng.random((T, special.size)), axis=1)[:, :k + 1]
+    lab, ti = special[pick[:, -1]], special[pick[:, :k]]
+    own = rng.random(T) < 0.5
+    ti[own, 5 % max(k, 1)] = lab[own]                           # the label among the teacher's ids, in half the rows
+    lab[::17] = -1
+    return h, w, (rng.standard_normal((T, k)) * 2).astype(np.float32), np.ascontiguousarray(ti), lab, vc, special
+
+
+# merges of 16 tokens and of 4 a block; 65 slots a token (16 * 65 are more than the block's threads); four to six
+# pieces, moved frames with the teacher's entries among them.  Near, one slot's share counted twice would be beyond
+# the bound in every row that counts, in three quarters of its elements
+@pytest.mark.parametrize("T,V", [(4200, 250000), (1024, 700000), (1000, 700000)])
+@pytest.mark.parametrize("far", [False, True], ids=["near", "far"])
+def test_a_teacher_over_several_pieces(T, V, far):
+    F, T_ = _F(), torch()
+    H, k = 64, 64
+    h, w, tv, ti, lab, vc, special = _many_pieces(T, T, H, V, k, far)
+    loss, rows, grad = _run(h, w, tv, ti, lab)
+    pick = np.random.default_rng(7).permutation(T)[:40]
+    pick[0] = 0                                                # a row that does not count
+    _, ref_rows, ref_grad, (rest, full) = head(h[pick], w, tv[pick], ti[pick], lab[pick], 0.8, 1.2)
+    n = (lab >= 0).sum() / (lab[pick] >= 0).sum()              # the oracle's mean is over the picked rows that count
+    ez = (H / 16 + 18) * 2.0 ** -24 * (np.abs(h[pick].astype(np.float64)) @ np.abs(w.astype(np.float64)).T).max(-1)
+    # the bounds of _check
+    assert np.all(np.abs(rows[pick] - ref_rows) <= 2.0 * (2 * ez + 2.0 ** -20 + 4 * 2.0 ** -24 * np.abs(ref_rows)) + 2.0 ** -22)
+    tol = (2.0 ** -8 * np.abs(ref_grad) + 2.0 ** -8 * rest + (4 * ez[:, None] + 2.0 ** -18) * full) / n + 1e-38
+    bad = np.abs(grad[pick] - ref_grad / n) > tol
+    assert not bad.any(), f"{bad.sum()} of {bad.size}, worst {(np.abs(grad[pick] - ref_grad / n) / tol).max():.2f}"
+    assert rows[0] == 0 and not grad[0].any()
+    mean = rows.astype(np.float64).sum() / (lab >= 0).sum()
+    assert abs(loss - mean) <= 2.0 ** -22 * abs(mean)
+    alone = _run(h, w, tv, ti, lab, want_grad=False)           # the loss alone: bit for bit
+    assert alone[0] == loss
+    np.testing.assert_array_equal(alone[1], rows)
+
+
+@pytest.mark.parametrize("T", [7, 300])
+@pytest.mark.parametrize("spread", [30.0, 300.0])
+def test_far_logits_with_few_tokens(T, spread):
+    # as above in one piece with merges of 4 tokens a block: every row and element against the oracle
+    rng = np.random.default_rng(T)
+    H, V, k = 64, 20000, 9
+    w = rng.standard_normal((V, H)) * (spread / 8) * np.linspace(0.2, 1.0, V)[:, None]
+    w, h = bf16_rne(w.astype(np.float32)), bf16_rne(rng.standard_normal((T, H)).astype(np.float32))
+    lab = rng.integers(0, V // 10, T).astype(np.int32)
+    ti = np.stack([np.append(rng.permutation(V // 10)[:k - 1], rng.integers(0, V)) for _ in range(T)]).astype(np.int32)
+    tv = (rng.standard_normal((T, k)) * 2).astype(np.float32)
+    for args in ((tv, ti, lab), (None, None, lab), (tv, ti, None)):
+        _check(_run(h, w, *args), h, w, *args, what=f"{T} spread {spread}")
