@@ -34,6 +34,7 @@
 // 4), 16 tokens in NVFP4 75-77 us (fc1 39-41, 3.8 TB/s, fc2 23), bound by the
 // chains of dependent loads of blocks that pass few slabs each, and by the
 // conversions (in INT4 33 and 21).
+#include <cmath>
 #include <type_traits>
 
 #include "fq_act.h"
@@ -843,17 +844,25 @@ int lds_rows(int K, int T) {
     const int fit = 32768 / (K * 2 + 16), most = T < 8 ? T : 8;
     return fit < 1 ? 1 : fit < most ? fit : most;
 }
-// A tile per wave where that leaves blocks enough (counted over all routed rows,
-// of which some open no group), else the waves share its columns.  128 experts,
-// 2048 by 768, top-8, shared against not: NVFP4 fc1 of 16 tokens (1536 blocks of
-// four tiles) 38.8 and 40.6 us, of 32 55.9 and 52.8; INT4 fc1 of 4 tokens (384)
-// 17.4 and 17.9, of 8 25.2 and 24.0, of 16 35.4 and 32.6; fc2 of 8 tokens (1024)
-// 16.4 and 17.2 in NVFP4, of 16 21.5 and 20.7 in INT4.
+// Experts that evenly routed tokens hit: as many groups of rows, and so blocks
+// along the grid's other axis that have work.
+double groups_hit(const PackedExpertArgs& a) {
+    return a.E * (1.0 - std::pow(1.0 - (double)a.k / a.E, a.R / a.k));   // k <= E
+}
+// A tile per wave where that leaves blocks enough with work, else the waves share
+// a tile's columns.  Shared against not, in us of the whole layer, blocks of four
+// tiles with work beside them.  128 experts, 2048 by 768, top-8: NVFP4 fc1 of 24
+// tokens (1210) 91.7 and 92.4, of 32 (1341) 103.0 and 102.0; INT4 fc1 of 4
+// tokens (349) 31.7 and 33.0, of 8 (619) 48.2 and 46.5; fc2 in NVFP4 of 4 tokens
+// (466) 35.0 and 35.4, of 8 (826) 52.4 and 52.0.  32 experts, 2048 by 1024,
+// top-8, 32 tokens (512): NVFP4 fc1 77.4 and 94.3, fc2 77.4 and 83.8; INT4 fc1
+// 69.5 and 76.8.  8 experts, 4096 by 4096, top-2, 64 tokens (fc1 512, fc2 256):
+// NVFP4 fc1 298 and 342, fc2 298 and 350.
 template <int FMT>
 hipError_t run_fc1(const PackedExpertArgs& a, hipStream_t st) {
     const int cap = lds_rows(a.H, a.R / a.k);
     const size_t lds = (size_t)cap * (a.H * 2 + 16);
-    if (a.R * (a.I / 64) >= (FMT == NVFP4 ? 2048 : 512))
+    if (groups_hit(a) * (a.I / 64) >= (FMT == NVFP4 ? 1280 : 576))
         hipLaunchKernelGGL((k_packed_fc1<FMT, false>), dim3((unsigned)(a.I / 64), (unsigned)a.R), dim3(64 * WV), lds, st,
                            a, cap);
     else
@@ -865,7 +874,7 @@ template <int FMT>
 hipError_t run_fc2(const PackedExpertArgs& a, hipStream_t st) {
     const int cap = lds_rows(a.I, a.R / a.k);
     const size_t lds = (size_t)cap * (a.I * 2 + 16);
-    if (a.R * (a.H / 128) >= 2048)
+    if (groups_hit(a) * (a.H / 128) >= 704)
         hipLaunchKernelGGL((k_packed_fc2<FMT, false>), dim3((unsigned)(a.H / 128), (unsigned)a.R), dim3(64 * WV), lds, st,
                            a, cap);
     else
