@@ -534,7 +534,6 @@ __global__ __launch_bounds__(64 * KW) void k_matvec(MatvecArgs a) {
     __shared__ Reduce<MT, NT, KW> red;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t n0 = block_id() * 16 * NT;
-    if (n0 >= a.N) return;
     const int m0 = blockIdx.y * 16 * MT;
     uint32_t vx[MT];
 #pragma unroll
@@ -563,7 +562,6 @@ __global__ __launch_bounds__(64 * KW) void k_matvec_which(MatvecArgs a) {
     __shared__ int count;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r0 = blockIdx.y;
     const int64_t n0 = block_id() * 16;
-    if (n0 >= a.N) return;
     for (int i = threadIdx.x; i < a.M; i += 64 * KW) ids[i] = a.which[i];
     __syncthreads();
     const int e = ids[r0];
