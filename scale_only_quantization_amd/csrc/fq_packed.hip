@@ -804,11 +804,19 @@ __global__ __launch_bounds__(256) void k_packed_combine(PackedExpertArgs a) {
 // Up to 2048 columns four waves split a tile's columns, above eight do (12289 x
 // 8192, 13 rows, NVFP4: 22 us against 27; 49152 x 2048: 22 against 19); by the
 // columns only, so that a row's bits do not depend on the other rows.  A CU
-// holds one block at a time, whose time grows with its tiles from a fixed part
-// on (12289 x 8192, 13 rows: 9.3 us a round of blocks of one tile, 14.4 of two,
-// 16 of three, 22 of four), so the tiles per block are those with the least sum
-// over the rounds (8192 x 8192, one row, one tile 16.1 us, two 12.2, four 18.6;
-// 12000 x 2048, 16 rows: 10.0, 9.6, three 8.0, four 9.1).
+// holds one block of eight waves at a time, whose time grows with its tiles from
+// a fixed part on (12289 x 8192, 13 rows: 9.3 us a round of blocks of one tile,
+// 14.4 of two, 16 of three, 22 of four), so the tiles per block are those with
+// the least sum over the rounds (8192 x 8192, one row, one tile 16.1 us, two
+// 12.2, four 18.6).  Of four waves a CU holds three blocks of one tile (INT with
+// wide groups two); with 2048 columns they share the CU's units and the same rule
+// holds (12000 x 2048, 16 rows: one tile 10.0 us, two 9.6, three 8.0, four 9.1),
+// but short rows are latency, and while all blocks of one tile fit at once that
+// is least (one row, 8192 x 512: one tile 3.7 us and two 4.6 in INT4 and 4.8 in
+// NVFP4; 10000 x 512 in NVFP4: 3.8, 4.9, three 6.1; 8192 x 1024: NVFP4 4.6 and
+// 4.9; INT4 with wide groups and 16 rows 5.3 and 5.0).  Blocks past the last row
+// of a grid's last line read zeros and store nothing (to return early took 0.1 us
+// of every call).
 template <int FMT, int KW>
 hipError_t run_matvec(const MatvecArgs& a, hipStream_t st) {
     const unsigned tiles = (unsigned)((a.N + 15) / 16);
@@ -818,10 +826,11 @@ hipError_t run_matvec(const MatvecArgs& a, hipStream_t st) {
         hipLaunchKernelGGL((k_matvec<FMT, 2, 2, KW>), grid_of((tiles + 1) / 2, (unsigned)((a.M + 31) / 32)),
                            dim3(64 * KW), 0, st, a);
     else {
-        unsigned best = 0, least = 0;
-        for (unsigned n = 1; n <= 4; ++n) {
+        const bool at_once = a.w.K <= (FMT == INT_WIDE ? 512 : 1024) && tiles <= 256 * (FMT == INT_WIDE ? 2 : 3);
+        unsigned best = 1, least = (tiles + 255) / 256 * 7;
+        for (unsigned n = 2; n <= 4 && !at_once; ++n) {
             const unsigned cost = ((tiles + n - 1) / n + 255) / 256 * (4 + 3 * n);
-            if (best == 0 || cost < least) best = n, least = cost;
+            if (cost < least) best = n, least = cost;
         }
         const dim3 grid = grid_of((tiles + best - 1) / best), block(64 * KW);
         if (best == 1) hipLaunchKernelGGL((k_matvec<FMT, 1, 1, KW>), grid, block, 0, st, a);
