@@ -557,3 +557,11 @@ def test_experts_with_a_tile_per_wave(fmt):
         # border of the float8 quantiser that fp32 sums decide their code, and one
         # code is an eighth of its h
         _check_layer_bound(got, d, *OP.PRESETS[fmt][2:])
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "row", "g32", "g128"])
+@pytest.mark.parametrize("N,K,M", [(4200, 1152, 5), (9001, 1184, 16), (12300, 1056, 3), (12300, 288, 1), (20001, 160, 2)])
+def test_matvec_of_many_rows_and_four_waves(fmt, N, K, M):
+    # two, three and four tiles a block of four waves, in every format: rows past the short ones, which stay at one
+    # tile while their blocks fit at once, and more short rows than that
+    test_matvec(fmt, N, K, M)
