@@ -4,8 +4,11 @@
 //   y[m, n] = sum_k x[m, k] W[n, k],  W = q s (INT4, a scale per row or group)
 //                                     W = q d t (NVFP4: E2M1, E4M3 per 16, fp32 per matrix)
 // A few rows against megabytes of weights: what counts is the stream of codes
-// from HBM, so every byte is read once and all vector work per code is kept
-// under the 2.5 operations a CU has per code at the full HBM rate.  The
+// from HBM, so one pass over them serves as many rows of x as the kernel holds
+// (32; of one matrix among several 16; in the layer up to 8, fewer of long rows:
+// lds_rows), and all vector work per code is kept under the 2.5 operations a CU
+// has per code at the full HBM rate.  More rows take further passes, which load
+// and convert the codes again.  The
 // products themselves go to the matrix cores (v_mfma_f32_16x16x32_bf16, 16
 // rows of x by 16 rows of W; unused rows of x cost nothing that counts): codes
 // become bf16 exactly, x is bf16, sums are fp32.
@@ -26,14 +29,19 @@
 // 22 were x through the L2, against 15 for codes and scales alone); and the
 // scales of a slab are one load, a lane group per chunk, spread by lane swaps
 // (a load per chunk touches 16 cache lines for 128 bytes: 6 us of those 15).
-// All loads go through buffer resources: a lane's constant plus a scalar, and
-// rows past the end read as zero without a branch.
+// All loads go through buffer resources, and rows past the end read as zero
+// without a branch.  In the layer a load's offset is a lane's constant plus a
+// scalar; in the products the wave's index reaches the chunk as a vector value,
+// and the compiler puts most loads (41 of the 61 of k_matvec<NVFP4, 1, 4, 8>, all
+// in INT4) in a loop over the lanes' offsets that passes once.
 // Measured: 13 rows by 12289 x 8192 in NVFP4 21 us (2.7 TB/s; a large read 6.1);
-// one row by 2048 x 2048 in INT4 4.2 us in the kernel, latency; the layer of 128
-// experts, 2048 by 768, top-8: one token in INT4 17.2 us (fc1 8, fc2 6, combine
-// 4), 16 tokens in NVFP4 75-77 us (fc1 39-41, 3.8 TB/s, fc2 23), bound by the
+// one row by 2048 x 2048 in INT4 4.4 us in the kernel, latency; 4096 x 4096 in
+// INT4 17 rows 10.8 us, 64 13.4, 256 47, 1024 183; the layer of 128 experts, 2048
+// by 768, top-8: one token in INT4 16.6 us (fc1 8, fc2 6, combine 4), in NVFP4
+// 21-23, 16 tokens in NVFP4 74-77 us (fc1 41, 3.8 TB/s, fc2 24), bound by the
 // chains of dependent loads of blocks that pass few slabs each, and by the
-// conversions (in INT4 33 and 21).
+// conversions (in INT4 68 us); 8 experts of 2048 by 1024, top-8, 32 tokens, five
+// passes over the codes: 74 and 70 us.
 #include <cmath>
 #include <type_traits>
 
