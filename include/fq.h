@@ -478,6 +478,111 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
                  const int32_t* teacher_topk_ids, const int32_t* labels, float* loss, float* row_loss,
                  void* grad, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- log probabilities of given tokens, entropy, the most likely tokens ---------
+ * What a teacher's pass hands to the top-k distillation (the KL over the
+ * teacher's top-k tokens, so that the [tokens, vocab] teacher tensor never
+ * exists: the nxmr.cn article, section 二.5), and what scores an answer: per row
+ * z of logits, from the logits (fq_logprob_*) or from the hidden states and the
+ * output weight, z = h w^T without storing it (fq_head_logprob_*),
+ *     lse = log sum_v e^z_v,   p = e^(z - lse)
+ *     logp_j = min(z[id_j] - lse, 0) of each given token; 0 for an id outside
+ *              [0, vocab) (padding, e.g. -1).  Ids may repeat.
+ *     entropy = -sum_v p_v log p_v
+ *     top: the ids of the largest z in descending order, the lowest id first
+ *          among equal ones, with their log probabilities.  Where fewer than
+ *          `top` logits are above -inf the rest is id -1 and -inf.
+ * top_logp and top_ids are valid teacher_topk_logits / teacher_topk_ids of
+ * fq_head_loss and fq_distill_loss (a shift by lse does not change their
+ * softmax).  Logits may be -inf (ruled-out tokens: p = 0); a row of nothing
+ * else has lse and logp -inf, entropy 0 and gradient 0.
+ * The gradient, with a_j = dL/dlogp_j (ids inside the vocabulary), A = sum_j a_j
+ * and b = dL/dentropy; top_ids and top_logp pass none:
+ *     dL/dz_v = sum_j a_j [v = id_j] - p_v (A + b (log p_v + entropy))
+ *     dL/dh = sum_v dL/dz_v w_v
+ * Sums are fp32; bitwise deterministic.  From hidden states z is an fp32 sum, so
+ * two ids whose logits differ by less than its error may change places; in the
+ * gradient's product dL/dz is rounded to bf16, except the given tokens', which
+ * are added in fp32. */
+typedef struct {
+    int64_t tokens;            /* rows, >= 0, < 2^24                                  */
+    int64_t hidden;            /* fq_head_logprob_*: a multiple of 64, 64 .. 16384; fq_logprob_*: 0 */
+    int64_t vocab;             /* >= 1, < 2^31                                        */
+    int32_t given;             /* given tokens per row, 0 .. 64                       */
+    int32_t top;               /* most likely tokens per row, 0 .. min(64, vocab)     */
+} fq_logprob_desc;
+/* Bytes of fq_logprob_fwd's device workspace (256-B aligned); 0 on a bad descriptor. */
+size_t fq_logprob_workspace_size(const fq_logprob_desc* d);
+/* logits: device bf16 [tokens, row_stride], 16-B aligned, of each row the first
+ *   vocab elements; row_stride >= vocab, a multiple of 8.
+ * ids: device int32 [tokens, given] and logp: device fp32 [tokens, given]; NULL
+ *   with given == 0.
+ * lse, entropy: nullable device fp32 [tokens].
+ * top_ids: device int32 [tokens, top] and top_logp: device fp32 [tokens, top];
+ *   NULL with top == 0.
+ * Errors: FQ_E_INVALID (nulls, given outside 0 .. 64, top outside 0 .. min(64,
+ * vocab), nothing to write), FQ_E_SHAPE, FQ_E_ALIGN, FQ_E_WORKSPACE, FQ_E_HIP.
+ * Zero tokens are a no-op. */
+int fq_logprob_fwd(const fq_logprob_desc* d, const void* logits, int64_t row_stride, const int32_t* ids, float* logp,
+                   float* lse, float* entropy, int32_t* top_ids, float* top_logp, void* workspace,
+                   size_t workspace_bytes, void* stream);
+/* lse (and entropy, with dentropy): the forward's.  dlogp: device fp32 [tokens,
+ * given], NULL with given == 0.  dentropy: nullable device fp32 [tokens].
+ * grad: device bf16 [tokens, grad_stride], 16-B aligned, grad_stride as
+ * row_stride; may be logits with the same stride.  Columns from vocab on are
+ * left as they were.  Errors as above, and FQ_E_INVALID without both dlogp and
+ * dentropy. */
+int fq_logprob_bwd(const fq_logprob_desc* d, const void* logits, int64_t row_stride, const int32_t* ids,
+                   const float* lse, const float* entropy, const float* dlogp, const float* dentropy, void* grad,
+                   int64_t grad_stride, void* stream);
+/* The same from h: device bf16 [tokens, hidden] and w: device bf16 [vocab,
+ * hidden], both 16-B aligned.  with_grad: the size for the backward instead of
+ * the forward; at most about 640 MB for a piece of the vocabulary beside 8 bytes
+ * per token, alternative and 64 vocabulary entries (forward) or fp32 sums of the
+ * gradient (backward), or what one piece of 256 entries takes. */
+size_t fq_head_logprob_workspace_size(const fq_logprob_desc* d, int32_t with_grad);
+int fq_head_logprob_fwd(const fq_logprob_desc* d, const void* h, const void* w, const int32_t* ids, float* logp,
+                        float* lse, float* entropy, int32_t* top_ids, float* top_logp, void* workspace,
+                        size_t workspace_bytes, void* stream);
+/* grad: device bf16 [tokens, hidden], 16-B aligned (may be h).  The output
+ * weight gets no gradient (it stays frozen). */
+int fq_head_logprob_bwd(const fq_logprob_desc* d, const void* h, const void* w, const int32_t* ids, const float* lse,
+                        const float* entropy, const float* dlogp, const float* dentropy, void* grad, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* ---- the norm of many gradients, and clipping by it --------------------------------
+ * The joint clipping of a whole model, whose scales are more tensors than one
+ * fq_scale_adamw call takes (FQ_MAX_SCALE_PARAMS): fq_grad_norm over all layers'
+ * gradients, fq_grad_clip by it, then fq_scale_adamw layer by layer with
+ * max_grad_norm 0 (the optim block's grad clip of the AngelSlim page, "Train
+ * from YAML").
+ *     norm = sqrt(sum of all g^2)                 (fp64, a fixed order)
+ *     c = min(1, max_grad_norm / (norm + 1e-6)),  out = c g, rounded to the type
+ * Between the two calls a caller of several processes reduces the norms: `norm`
+ * is read from device memory.  An infinite norm gives c = 0 (and NaN where g is
+ * infinite); a NaN norm gives NaN everywhere. */
+typedef enum {
+    FQ_F32 = 0,
+    FQ_BF16 = 1
+} fq_dtype;
+typedef struct {
+    const void* grad;          /* device fp32 or bf16 [count], aligned to its type    */
+    void* out;                 /* fq_grad_clip: device, the same type, [count]: grad itself, or memory
+                                  that overlaps no tensor of the call; fq_grad_norm does not look at it */
+    int64_t count;             /* >= 0, < 2^40                                        */
+    int32_t dtype;             /* fq_dtype                                            */
+} fq_grad_tensor;
+/* Bytes of fq_grad_norm's device workspace (8-B aligned; 0 if none is needed or on bad input). */
+size_t fq_grad_norm_workspace_size(const fq_grad_tensor* tensors, int32_t ntensors);
+/* tensors: host array of ntensors (0 .. 65536) descriptors.  norm: device fp32 [1].
+ * Errors: FQ_E_INVALID (nulls, a bad type or count), FQ_E_SHAPE (ntensors < 0),
+ * FQ_E_UNSUPPORTED (ntensors > 65536), FQ_E_ALIGN, FQ_E_WORKSPACE, FQ_E_HIP. */
+int fq_grad_norm(const fq_grad_tensor* tensors, int32_t ntensors, float* norm, void* workspace,
+                 size_t workspace_bytes, void* stream);
+/* max_grad_norm: > 0, finite.  Where c is 1 tensors that are their own out are
+ * not touched. */
+int fq_grad_clip(const fq_grad_tensor* tensors, int32_t ntensors, float max_grad_norm, const float* norm,
+                 void* stream);
+
 /* ---- products of packed 4-bit weights --------------------------------------------
  * For a served model: the weights as fq_tensor's packed codes with their
  * scales, a few rows of activations.

@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfq.so")
 SOURCES = ["fq_api.hip", "fq_tensor.hip", "fq_layer.hip", "fq_gemm.hip", "fq_optim.hip", "fq_distill.hip",
-           "fq_norm.hip", "fq_head.hip", "fq_packed.hip", "fq_ops_api.hip"]
+           "fq_norm.hip", "fq_head.hip", "fq_packed.hip", "fq_logprob.hip", "fq_grad.hip", "fq_ops_api.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = [

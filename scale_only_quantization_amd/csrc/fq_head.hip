@@ -526,12 +526,18 @@ HeadPlan head_plan(int64_t T, int64_t H, int64_t V) {
     return p;
 }
 
+hipError_t launch_head_grad(const HeadArgs& a, hipStream_t st) {
+    const int64_t mt = (a.T + a.bm - 1) / a.bm, nt = (a.H + BN - 1) / BN;
+    hipLaunchKernelGGL(k_head_grad, dim3((unsigned)((mt * nt * a.splits + 7) / 8 * 8)), dim3(512), 0, st, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t st) {
     if (a.T > 0) {
         // Tiles of equally many rows, in whole sub-tiles: 333 tokens are 192 and
         // 141, not 256 and 77, and a tile's time goes with its sub-tiles.
         a.bm = (int)(((a.T + (a.T + BM - 1) / BM - 1) / ((a.T + BM - 1) / BM) + 31) / 32 * 32);
-        const int64_t mt = (a.T + a.bm - 1) / a.bm, nt = (a.H + BN - 1) / BN;
+        const int64_t mt = (a.T + a.bm - 1) / a.bm;
         a.vc = pl.vc;
         a.splits = pl.splits;
         a.ksplit = pl.ksplit;
@@ -546,10 +552,7 @@ hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t 
             else hipLaunchKernelGGL(k_head_probs<false>, dim3(g1), dim3(512), 0, st, a);
             if (a.T >= 1024) hipLaunchKernelGGL(k_head_merge<16>, dim3((unsigned)((a.T + 15) / 16)), dim3(1024), 0, st, a);
             else hipLaunchKernelGGL(k_head_merge<4>, dim3((unsigned)((a.T + 3) / 4)), dim3(1024), 0, st, a);
-            if (a.grad)
-                hipLaunchKernelGGL(k_head_grad, dim3((unsigned)((mt * nt * pl.splits + 7) / 8 * 8)), dim3(512), 0, st,
-                                   a);
-            err = hipGetLastError();
+            err = a.grad ? launch_head_grad(a, st) : hipGetLastError();
             if (err != hipSuccess) return err;
         }
         // 4 columns a thread where the splits' sums are the most that is read,

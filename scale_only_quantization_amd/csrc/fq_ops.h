@@ -85,6 +85,104 @@ struct HeadArgs {
     int bm;                // tokens per tile of the two products, <= 256
 };
 hipError_t launch_head(HeadArgs a, const HeadPlan& pl, float* loss, hipStream_t st);
+// the second product alone, of a piece: g = (first ? 0 : step g) + p w
+hipError_t launch_head_grad(const HeadArgs& a, hipStream_t st);
+
+// ------------------------------------------------ log probabilities of rows ---
+constexpr int LOGP_MAX_TOP = 64;
+constexpr int ROWS_TPB = 256;
+struct RowsArgs {          // rows of logits in chunks of columns, then joined
+    int64_t T, V;
+    int m, k;              // given tokens and alternatives per row
+    const void* z;         // bf16 or fp32 logits [T, ld] of the columns c0 .. c0 + n - 1
+    int64_t ld;
+    int64_t c0, n;
+    int64_t nc;            // chunks of a whole row
+    int64_t chunk0, pc;    // first chunk and chunks of these columns
+    float4* part;          // workspace [T, nc]: maximum, sum of e^(z - max), sum of e^(z - max) (z - max)
+    uint64_t* keys;        // workspace [T, nc, k], with k
+    const float* zs;       // nullable [T, m]: the given tokens' logits; else they are read from z
+    const int32_t* ids;    // [T, m]
+    float* logp;
+    float* lse;            // nullable
+    float* entropy;        // nullable
+    int32_t* top_ids;      // [T, k]
+    float* top_logp;
+};
+struct LogpBwdArgs {       // dL/dz of rows of bf16 logits
+    int64_t T, V;
+    int m;
+    const uint16_t* z;
+    int64_t ld, gld;
+    const int32_t* ids;
+    const float* lse;
+    const float* entropy;  // with dent
+    const float* dlogp;    // [T, m]
+    const float* dent;     // nullable
+    uint16_t* grad;        // [T, gld]; may be z
+};
+int64_t rows_chunk(int64_t T, int64_t V);          // columns of a chunk of bf16 logits
+hipError_t launch_logprob_rows(const RowsArgs& a, hipStream_t st);
+hipError_t launch_logprob_bwd(const LogpBwdArgs& a, hipStream_t st);
+
+struct HeadLogpArgs {
+    int64_t T;
+    int H;                 // a multiple of 64
+    int64_t V;
+    int m, k;
+    const uint16_t* h;     // [T, H]
+    const uint16_t* w;     // [V, H]
+    const int32_t* ids;    // [T, m]
+    float* lse;            // forward: nullable; backward: read
+    float* entropy;        // forward: nullable; backward: read with dent
+    float* logp;
+    int32_t* top_ids;
+    float* top_logp;
+    const float* dlogp;    // backward
+    const float* dent;     // nullable
+    uint16_t* grad;        // [T, H]
+    // workspace
+    float* zs;             // [T, m] the given tokens' logits
+    float* z;              // forward: [T, vc] logits of a piece
+    float4* part;          // forward
+    uint64_t* keys;        // forward
+    float4* rowc;          // backward [T]: lse log2 e, A + b (entropy), b
+    uint16_t* p;           // backward [T, vc]
+    float* g;              // backward [splits, T, H]
+    float* ones;           // backward [T]
+    // filled per launch
+    int64_t c0;
+    int vc, bm;
+};
+struct HeadLogpPlan {
+    int64_t vc, pieces;    // entries of a piece (a multiple of 256), pieces
+    int64_t pc, nc;        // chunks of a piece and of all
+};
+HeadLogpPlan head_logp_plan(int64_t T, int64_t H, int64_t V);
+hipError_t launch_head_logprob_fwd(HeadLogpArgs a, const HeadLogpPlan& pl, hipStream_t st);
+hipError_t launch_head_logprob_bwd(HeadLogpArgs a, const HeadPlan& pl, hipStream_t st);
+
+// ------------------------------------------------- the norm of many gradients ---
+constexpr int GRAD_CHUNK = 16384;                  // elements per block
+constexpr int GRAD_LIST = 96;                      // tensors per launch: their entries are kernel arguments (under 4 KB)
+struct GradEntry {
+    const void* g;
+    void* out;
+    int64_t count;
+    int64_t blk0;          // the tensor's first block of the launch
+    int32_t bf;            // bf16, else fp32
+};
+struct GradArgs {
+    GradEntry t[GRAD_LIST];
+    int n;
+    int64_t blocks;
+    double* part;          // norm: [blocks]
+    const float* norm;     // clip
+    double max_norm;
+};
+hipError_t launch_grad_sq(const GradArgs& a, hipStream_t st);
+hipError_t launch_grad_norm(const double* part, int64_t n, float* norm, hipStream_t st);
+hipError_t launch_grad_clip(const GradArgs& a, hipStream_t st);
 
 // ------------------------------------------------- packed 4-bit weights ---
 constexpr int PACKED_MAX_ROWS = 1024;

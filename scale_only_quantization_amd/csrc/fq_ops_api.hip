@@ -174,6 +174,314 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
     return FQ_OK;
 }
 
+// ------------------------------------- log probabilities, entropy, alternatives --
+namespace {
+
+int check_logprob(const fq_logprob_desc* d, bool hidden) {
+    if (!d || d->given < 0 || d->given > 64 || d->top < 0 || d->top > LOGP_MAX_TOP || d->top > d->vocab)
+        return FQ_E_INVALID;
+    if (d->tokens < 0 || d->tokens >= (int64_t)1 << 24 || d->vocab < 1 || d->vocab >= (int64_t)1 << 31)
+        return FQ_E_SHAPE;
+    if (!hidden) return d->hidden != 0 ? FQ_E_SHAPE : FQ_OK;
+    if (d->hidden < 64 || d->hidden % 64) return FQ_E_SHAPE;
+    return d->hidden > 16384 ? FQ_E_UNSUPPORTED : FQ_OK;
+}
+
+// the outputs of both forwards
+int check_logprob_out(const fq_logprob_desc* d, const int32_t* ids, const float* logp, const float* lse,
+                      const float* entropy, const int32_t* top_ids, const float* top_logp) {
+    if (d->tokens > 0) {
+        if (d->given > 0 ? !ids || !logp : ids || logp) return FQ_E_INVALID;
+        if (d->top > 0 ? !top_ids || !top_logp : top_ids || top_logp) return FQ_E_INVALID;
+        if (!logp && !lse && !entropy && !top_ids) return FQ_E_INVALID;
+    }
+    return aligned(ids, 4) && aligned(logp, 4) && aligned(lse, 4) && aligned(entropy, 4) && aligned(top_ids, 4) &&
+                   aligned(top_logp, 4)
+               ? FQ_OK
+               : FQ_E_ALIGN;
+}
+
+// the upstream gradients of both backwards
+int check_logprob_up(const fq_logprob_desc* d, const int32_t* ids, const float* lse, const float* entropy,
+                     const float* dlogp, const float* dentropy, const void* grad) {
+    if (d->tokens > 0) {
+        if (d->given > 0 ? !ids || !dlogp : ids || dlogp) return FQ_E_INVALID;
+        if (!lse || !grad || (!dlogp && !dentropy) || (dentropy && !entropy)) return FQ_E_INVALID;
+    }
+    return aligned(ids, 4) && aligned(lse, 4) && aligned(entropy, 4) && aligned(dlogp, 4) && aligned(dentropy, 4) &&
+                   aligned(grad, 16)
+               ? FQ_OK
+               : FQ_E_ALIGN;
+}
+
+struct Placer {
+    size_t total = 0;
+    size_t operator()(size_t bytes) {
+        const size_t at = total;
+        total = round_up(total + bytes, 256);
+        return at;
+    }
+};
+
+struct RowsLayout {
+    size_t part, keys, total;
+};
+RowsLayout rows_layout(const fq_logprob_desc* d) {
+    Placer place;
+    const size_t n = (size_t)d->tokens * (size_t)((d->vocab + rows_chunk(d->tokens, d->vocab) - 1) /
+                                                  rows_chunk(d->tokens, d->vocab));
+    RowsLayout y{};
+    y.part = place(n * sizeof(float4));
+    y.keys = place(n * (size_t)d->top * 8);
+    y.total = place.total;
+    return y;
+}
+
+struct HeadLogpLayout {
+    size_t zs, z, part, keys, rowc, ones, p, g, total;
+};
+HeadLogpLayout head_logp_layout(const fq_logprob_desc* d, bool grad) {
+    Placer place;
+    HeadLogpLayout y{};
+    const size_t T = (size_t)d->tokens;
+    y.zs = place(T * (size_t)d->given * 4);
+    if (grad) {
+        const HeadPlan pl = head_plan(d->tokens, d->hidden, d->vocab);
+        y.rowc = place(T * 16);
+        y.ones = place(T * 4);
+        y.p = place(T * (size_t)pl.vc * 2);
+        y.g = place((size_t)pl.splits * T * (size_t)d->hidden * 4);
+    } else {
+        const HeadLogpPlan pl = head_logp_plan(d->tokens, d->hidden, d->vocab);
+        y.z = place(T * (size_t)pl.vc * 4);
+        y.part = place(T * (size_t)pl.nc * sizeof(float4));
+        y.keys = place(T * (size_t)pl.nc * (size_t)d->top * 8);
+    }
+    y.total = place.total;
+    return y;
+}
+
+bool bad_stride(int64_t stride, int64_t vocab) { return stride < vocab || stride % 8; }
+
+}  // namespace
+
+size_t fq_logprob_workspace_size(const fq_logprob_desc* d) {
+    return check_logprob(d, false) == FQ_OK ? rows_layout(d).total : 0;
+}
+
+int fq_logprob_fwd(const fq_logprob_desc* d, const void* logits, int64_t row_stride, const int32_t* ids, float* logp,
+                   float* lse, float* entropy, int32_t* top_ids, float* top_logp, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+    int s = check_logprob(d, false);
+    if (s != FQ_OK) return s;
+    if (bad_stride(row_stride, d->vocab)) return FQ_E_SHAPE;
+    if (d->tokens > 0 && !logits) return FQ_E_INVALID;
+    if ((s = check_logprob_out(d, ids, logp, lse, entropy, top_ids, top_logp)) != FQ_OK) return s;
+    if (!aligned(logits, 16) || !aligned(workspace, 256)) return FQ_E_ALIGN;
+    if (d->tokens == 0) return FQ_OK;
+    const RowsLayout y = rows_layout(d);
+    if (!workspace || workspace_bytes < y.total) return FQ_E_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    RowsArgs a{};
+    a.T = d->tokens;
+    a.V = a.n = d->vocab;
+    a.m = d->given;
+    a.k = d->top;
+    a.z = logits;
+    a.ld = row_stride;
+    a.nc = a.pc = (d->vocab + rows_chunk(a.T, a.V) - 1) / rows_chunk(a.T, a.V);
+    a.part = reinterpret_cast<float4*>(ws + y.part);
+    a.keys = reinterpret_cast<uint64_t*>(ws + y.keys);
+    a.ids = ids;
+    a.logp = logp;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logp = top_logp;
+    FQ_TRY(launch_logprob_rows(a, static_cast<hipStream_t>(stream)));
+    return FQ_OK;
+}
+
+int fq_logprob_bwd(const fq_logprob_desc* d, const void* logits, int64_t row_stride, const int32_t* ids,
+                   const float* lse, const float* entropy, const float* dlogp, const float* dentropy, void* grad,
+                   int64_t grad_stride, void* stream) {
+    int s = check_logprob(d, false);
+    if (s != FQ_OK) return s;
+    if (bad_stride(row_stride, d->vocab) || bad_stride(grad_stride, d->vocab)) return FQ_E_SHAPE;
+    if (d->tokens > 0 && (!logits || (grad == logits && grad_stride != row_stride))) return FQ_E_INVALID;
+    if ((s = check_logprob_up(d, ids, lse, entropy, dlogp, dentropy, grad)) != FQ_OK) return s;
+    if (!aligned(logits, 16)) return FQ_E_ALIGN;
+    if (d->tokens == 0) return FQ_OK;
+    LogpBwdArgs a{};
+    a.T = d->tokens;
+    a.V = d->vocab;
+    a.m = d->given;
+    a.z = static_cast<const uint16_t*>(logits);
+    a.ld = row_stride;
+    a.gld = grad_stride;
+    a.ids = ids;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.dlogp = dlogp;
+    a.dent = dentropy;
+    a.grad = static_cast<uint16_t*>(grad);
+    FQ_TRY(launch_logprob_bwd(a, static_cast<hipStream_t>(stream)));
+    return FQ_OK;
+}
+
+size_t fq_head_logprob_workspace_size(const fq_logprob_desc* d, int32_t with_grad) {
+    return check_logprob(d, true) == FQ_OK ? head_logp_layout(d, with_grad != 0).total : 0;
+}
+
+int fq_head_logprob_fwd(const fq_logprob_desc* d, const void* h, const void* w, const int32_t* ids, float* logp,
+                        float* lse, float* entropy, int32_t* top_ids, float* top_logp, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    int s = check_logprob(d, true);
+    if (s != FQ_OK) return s;
+    if (d->tokens > 0 && (!h || !w)) return FQ_E_INVALID;
+    if ((s = check_logprob_out(d, ids, logp, lse, entropy, top_ids, top_logp)) != FQ_OK) return s;
+    if (!aligned(h, 16) || !aligned(w, 16) || !aligned(workspace, 256)) return FQ_E_ALIGN;
+    if (d->tokens == 0) return FQ_OK;
+    const HeadLogpLayout y = head_logp_layout(d, false);
+    if (!workspace || workspace_bytes < y.total) return FQ_E_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    HeadLogpArgs a{};
+    a.T = d->tokens;
+    a.H = (int)d->hidden;
+    a.V = d->vocab;
+    a.m = d->given;
+    a.k = d->top;
+    a.h = static_cast<const uint16_t*>(h);
+    a.w = static_cast<const uint16_t*>(w);
+    a.ids = ids;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.logp = logp;
+    a.top_ids = top_ids;
+    a.top_logp = top_logp;
+    a.zs = reinterpret_cast<float*>(ws + y.zs);
+    a.z = reinterpret_cast<float*>(ws + y.z);
+    a.part = reinterpret_cast<float4*>(ws + y.part);
+    a.keys = reinterpret_cast<uint64_t*>(ws + y.keys);
+    FQ_TRY(launch_head_logprob_fwd(a, head_logp_plan(a.T, a.H, a.V), static_cast<hipStream_t>(stream)));
+    return FQ_OK;
+}
+
+int fq_head_logprob_bwd(const fq_logprob_desc* d, const void* h, const void* w, const int32_t* ids, const float* lse,
+                        const float* entropy, const float* dlogp, const float* dentropy, void* grad, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    int s = check_logprob(d, true);
+    if (s != FQ_OK) return s;
+    if (d->tokens > 0 && (!h || !w)) return FQ_E_INVALID;
+    if ((s = check_logprob_up(d, ids, lse, entropy, dlogp, dentropy, grad)) != FQ_OK) return s;
+    if (!aligned(h, 16) || !aligned(w, 16) || !aligned(workspace, 256)) return FQ_E_ALIGN;
+    if (d->tokens == 0) return FQ_OK;
+    const HeadLogpLayout y = head_logp_layout(d, true);
+    if (!workspace || workspace_bytes < y.total) return FQ_E_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    HeadLogpArgs a{};
+    a.T = d->tokens;
+    a.H = (int)d->hidden;
+    a.V = d->vocab;
+    a.m = d->given;
+    a.h = static_cast<const uint16_t*>(h);
+    a.w = static_cast<const uint16_t*>(w);
+    a.ids = ids;
+    a.lse = const_cast<float*>(lse);
+    a.entropy = const_cast<float*>(entropy);
+    a.dlogp = dlogp;
+    a.dent = dentropy;
+    a.grad = static_cast<uint16_t*>(grad);
+    a.zs = reinterpret_cast<float*>(ws + y.zs);
+    a.rowc = reinterpret_cast<float4*>(ws + y.rowc);
+    a.ones = reinterpret_cast<float*>(ws + y.ones);
+    a.p = reinterpret_cast<uint16_t*>(ws + y.p);
+    a.g = reinterpret_cast<float*>(ws + y.g);
+    FQ_TRY(launch_head_logprob_bwd(a, head_plan(a.T, a.H, a.V), static_cast<hipStream_t>(stream)));
+    return FQ_OK;
+}
+
+// ------------------------------------------- the norm of many gradients, clipping --
+namespace {
+
+constexpr int32_t GRAD_MAX_TENSORS = 65536;
+
+int check_grads(const fq_grad_tensor* t, int32_t n, bool out) {
+    if (n < 0) return FQ_E_SHAPE;
+    if (n > GRAD_MAX_TENSORS) return FQ_E_UNSUPPORTED;
+    if (n > 0 && !t) return FQ_E_INVALID;
+    for (int32_t i = 0; i < n; ++i) {
+        if ((t[i].dtype != FQ_F32 && t[i].dtype != FQ_BF16) || t[i].count < 0 || t[i].count >= (int64_t)1 << 40)
+            return FQ_E_INVALID;
+        if (t[i].count == 0) continue;
+        if (!t[i].grad || (out && !t[i].out)) return FQ_E_INVALID;
+        const size_t size = t[i].dtype == FQ_BF16 ? 2 : 4;
+        if (!aligned(t[i].grad, size) || (out && !aligned(t[i].out, size))) return FQ_E_ALIGN;
+    }
+    return FQ_OK;
+}
+
+int64_t grad_chunks(int64_t count) { return (count + GRAD_CHUNK - 1) / GRAD_CHUNK; }
+
+// The tensors in launches of up to GRAD_LIST: f(args) of each, with its blocks' place among all.
+extern "C++" template <typename F>
+int each_list(const fq_grad_tensor* t, int32_t n, F&& f) {
+    GradArgs a{};
+    int64_t before = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        if (t[i].count > 0) a.t[a.n++] = GradEntry{t[i].grad, t[i].out, t[i].count, a.blocks, t[i].dtype == FQ_BF16};
+        a.blocks += grad_chunks(t[i].count);
+        if (a.n == GRAD_LIST || (i == n - 1 && a.n > 0)) {
+            FQ_TRY(f(a, before));
+            before += a.blocks;
+            a.n = 0;
+            a.blocks = 0;
+        }
+    }
+    return FQ_OK;
+}
+
+}  // namespace
+
+size_t fq_grad_norm_workspace_size(const fq_grad_tensor* tensors, int32_t ntensors) {
+    if (check_grads(tensors, ntensors, false) != FQ_OK) return 0;
+    int64_t n = 0;
+    for (int32_t i = 0; i < ntensors; ++i) n += grad_chunks(tensors[i].count);
+    return (size_t)n * sizeof(double);
+}
+
+int fq_grad_norm(const fq_grad_tensor* tensors, int32_t ntensors, float* norm, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+    int s = check_grads(tensors, ntensors, false);
+    if (s != FQ_OK) return s;
+    if (!norm) return FQ_E_INVALID;
+    if (!aligned(norm, 4) || !aligned(workspace, 8)) return FQ_E_ALIGN;
+    const size_t need = fq_grad_norm_workspace_size(tensors, ntensors);
+    if (workspace_bytes < need || (need && !workspace)) return FQ_E_WORKSPACE;
+    double* part = static_cast<double*>(workspace);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    s = each_list(tensors, ntensors, [&](GradArgs& a, int64_t before) {
+        a.part = part + before;
+        return launch_grad_sq(a, st);
+    });
+    if (s != FQ_OK) return s;
+    FQ_TRY(launch_grad_norm(part, (int64_t)(need / sizeof(double)), norm, st));
+    return FQ_OK;
+}
+
+int fq_grad_clip(const fq_grad_tensor* tensors, int32_t ntensors, float max_grad_norm, const float* norm,
+                 void* stream) {
+    const int s = check_grads(tensors, ntensors, true);
+    if (s != FQ_OK) return s;
+    if (!norm || !std::isfinite(max_grad_norm) || max_grad_norm <= 0.0f) return FQ_E_INVALID;
+    if (!aligned(norm, 4)) return FQ_E_ALIGN;
+    return each_list(tensors, ntensors, [&](GradArgs& a, int64_t) {
+        a.norm = norm;
+        a.max_norm = (double)max_grad_norm;
+        return launch_grad_clip(a, static_cast<hipStream_t>(stream));
+    });
+}
+
 // ------------------------------------------------------ packed 4-bit weights --
 namespace {
 

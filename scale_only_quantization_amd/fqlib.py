@@ -78,6 +78,14 @@ class HeadDesc(Structure):
                 ("lm_weight", ctypes.c_float), ("distill_weight", ctypes.c_float)]
 
 
+class LogprobDesc(Structure):
+    _fields_ = [("tokens", c_int64), ("hidden", c_int64), ("vocab", c_int64), ("given", c_int32), ("top", c_int32)]
+
+
+class GradTensor(Structure):
+    _fields_ = [("grad", c_void_p), ("out", c_void_p), ("count", c_int64), ("dtype", c_int32)]
+
+
 class DistillDesc(Structure):
     _fields_ = [("type", c_int32), ("topk", c_int32), ("lm_weight", ctypes.c_float),
                 ("distill_weight", ctypes.c_float)]
@@ -86,6 +94,7 @@ class DistillDesc(Structure):
 DISTILL_TYPES = {"kl": 0, "rkl": 1, "cakld": 2, "topk_kl": 3}
 FQ_PROJ_POSITIVE, FQ_PROJ_E4M3_BLOCK = 0, 1
 FQ_MAX_SCALE_PARAMS = 16
+FQ_F32, FQ_BF16 = 0, 1
 FQ_SCALE_ADAMW_NOALLOC_MAX_BLOCKS = 32768
 
 
@@ -139,6 +148,19 @@ def _load():
         "fq_head_loss_workspace_size": (c_size_t, [POINTER(HeadDesc), c_int32]),
         "fq_head_loss": (c_int32, [POINTER(HeadDesc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                    c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "fq_logprob_workspace_size": (c_size_t, [POINTER(LogprobDesc)]),
+        "fq_logprob_fwd": (c_int32, [POINTER(LogprobDesc), c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "fq_logprob_bwd": (c_int32, [POINTER(LogprobDesc), c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
+                                     c_void_p, c_void_p, c_int64, c_void_p]),
+        "fq_head_logprob_workspace_size": (c_size_t, [POINTER(LogprobDesc), c_int32]),
+        "fq_head_logprob_fwd": (c_int32, [POINTER(LogprobDesc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                          c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "fq_head_logprob_bwd": (c_int32, [POINTER(LogprobDesc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                          c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "fq_grad_norm_workspace_size": (c_size_t, [POINTER(GradTensor), c_int32]),
+        "fq_grad_norm": (c_int32, [POINTER(GradTensor), c_int32, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "fq_grad_clip": (c_int32, [POINTER(GradTensor), c_int32, ctypes.c_float, c_void_p, c_void_p]),
         "fq_packed_matvec": (c_int32, [Q, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
                                        c_void_p, c_void_p, c_void_p, c_void_p]),
         "fq_packed_expert_workspace_size": (c_size_t, [L]),
@@ -160,7 +182,9 @@ EXPORTS = ("fq_abi_version", "fq_status_string", "fq_last_hip_error", "fq_preset
            "fq_scale_adamw_workspace_size", "fq_scale_adamw", "fq_scale_adamw_noalloc",
            "fq_distill_workspace_size", "fq_distill_loss", "fq_rms_norm_fwd",
            "fq_rms_norm_bwd_workspace_size", "fq_rms_norm_bwd", "fq_head_loss_workspace_size",
-           "fq_head_loss", "fq_packed_matvec", "fq_packed_expert_workspace_size", "fq_packed_expert_fwd")
+           "fq_head_loss", "fq_logprob_workspace_size", "fq_logprob_fwd", "fq_logprob_bwd",
+           "fq_head_logprob_workspace_size", "fq_head_logprob_fwd", "fq_head_logprob_bwd",
+           "fq_grad_norm_workspace_size", "fq_grad_norm", "fq_grad_clip", "fq_packed_matvec", "fq_packed_expert_workspace_size", "fq_packed_expert_fwd")
 
 
 def lib():
@@ -465,6 +489,141 @@ def head_loss(d: HeadDesc, h, w, loss, top_v=None, top_i=None, labels=None, row_
           _expect(n, "top_i", top_i, i32, (T, k), dev), _expect(n, "labels", labels, i32, (T,), dev),
           _expect(n, "loss", loss, f32, (1,), dev), _expect(n, "row_loss", row_loss, f32, (T,), dev),
           _expect(n, "grad", grad, bf, (T, d.hidden), dev), ws, nb)
+
+
+def logprob_desc(tokens: int, vocab: int, given: int = 0, top: int = 0, hidden: int = 0) -> LogprobDesc:
+    """Rows, vocabulary, given tokens and most likely tokens per row; hidden for the head_logprob calls."""
+    return LogprobDesc(tokens, hidden, vocab, given, top)
+
+
+def logprob_workspace_size(d: LogprobDesc) -> int:
+    return _lib.fq_logprob_workspace_size(ctypes.byref(d))
+
+
+def _rows(where, name, t, shape, device):
+    """(address, row stride) of a bf16 tensor of this shape whose rows may be padded to a stride of their own."""
+    T, V = shape
+    ld = t.stride(0) if T > 1 and t.dim() == 2 else (V + 7) // 8 * 8
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != device or (V > 1 and t.stride(1) != 1) or ld < V:
+        raise ValueError(f"{where}: {name} must be a {_BF16} tensor of shape {list(shape)} on GPU {device} with rows in "
+                         f"one piece, got {t.dtype} {list(t.shape)}, strides {t.stride()} on {t.device}")
+    if V % 8 and T and t.untyped_storage().nbytes() // 2 - t.storage_offset() < (T - 1) * ld + (V + 7) // 8 * 8:
+        raise ValueError(f"{where}: the last row of {name} must be padded to a multiple of 8 elements too")
+    return t.data_ptr(), ld
+
+
+def _logprob_out(n, d, dev, ids, logp, lse, entropy, top_ids, top_logp):
+    T, m, k = d.tokens, d.given, d.top
+    f32, i32 = _F32, _I32
+    return (_expect(n, "ids", ids, i32, (T, m), dev), _expect(n, "logp", logp, f32, (T, m), dev),
+            _expect(n, "lse", lse, f32, (T,), dev), _expect(n, "entropy", entropy, f32, (T,), dev),
+            _expect(n, "top_ids", top_ids, i32, (T, k), dev), _expect(n, "top_logp", top_logp, f32, (T, k), dev))
+
+
+def logprob_fwd(d: LogprobDesc, logits, ids=None, logp=None, lse=None, entropy=None, top_ids=None, top_logp=None,
+                workspace=None, stream=None):
+    """Log probabilities of given tokens, lse, entropy and the most likely tokens of bf16 logits [tokens, vocab]
+    (fq_logprob_fwd); rows may have a stride of their own, a multiple of 8.  Writes what is given."""
+    n = "logprob_fwd"
+    dev = _device_of(n, logits)
+    z, ld = _rows(n, "logits", logits, (d.tokens, d.vocab), dev)
+    ws, nb = _scratch(n, workspace, dev)
+    _call(n, _lib.fq_logprob_fwd, dev, stream, ctypes.byref(d), z, ld,
+          *_logprob_out(n, d, dev, ids, logp, lse, entropy, top_ids, top_logp), ws, nb)
+
+
+def _logprob_up(n, d, dev, ids, lse, entropy, dlogp, dentropy):
+    T, m = d.tokens, d.given
+    f32 = _F32
+    return (_expect(n, "ids", ids, _I32, (T, m), dev), _expect(n, "lse", lse, f32, (T,), dev),
+            _expect(n, "entropy", entropy, f32, (T,), dev), _expect(n, "dlogp", dlogp, f32, (T, m), dev),
+            _expect(n, "dentropy", dentropy, f32, (T,), dev))
+
+
+def logprob_bwd(d: LogprobDesc, logits, lse, grad, ids=None, dlogp=None, entropy=None, dentropy=None, stream=None):
+    """d L / d logits into grad (bf16 [tokens, vocab], rows as those of logits; may be logits) from the gradients of
+    logprob_fwd's logp and entropy (fq_logprob_bwd)."""
+    n = "logprob_bwd"
+    dev = _device_of(n, logits)
+    full = (d.tokens, d.vocab)
+    z, ld = _rows(n, "logits", logits, full, dev)
+    g, gld = _rows(n, "grad", grad, full, dev)
+    _call(n, _lib.fq_logprob_bwd, dev, stream, ctypes.byref(d), z, ld,
+          *_logprob_up(n, d, dev, ids, lse, entropy, dlogp, dentropy), g, gld)
+
+
+def head_logprob_workspace_size(d: LogprobDesc, grad: bool = False) -> int:
+    return _lib.fq_head_logprob_workspace_size(ctypes.byref(d), 1 if grad else 0)
+
+
+def head_logprob_fwd(d: LogprobDesc, h, w, ids=None, logp=None, lse=None, entropy=None, top_ids=None, top_logp=None,
+                     workspace=None, stream=None):
+    """logprob_fwd of the logits h w^T, which are not stored, from bf16 hidden states h [tokens, hidden] and the
+    output weight w [vocab, hidden] (fq_head_logprob_fwd)."""
+    n = "head_logprob_fwd"
+    dev = _device_of(n, h)
+    ws, nb = _scratch(n, workspace, dev)
+    _call(n, _lib.fq_head_logprob_fwd, dev, stream, ctypes.byref(d),
+          _expect(n, "h", h, _BF16, (d.tokens, d.hidden), dev), _expect(n, "w", w, _BF16, (d.vocab, d.hidden), dev),
+          *_logprob_out(n, d, dev, ids, logp, lse, entropy, top_ids, top_logp), ws, nb)
+
+
+def head_logprob_bwd(d: LogprobDesc, h, w, lse, grad, ids=None, dlogp=None, entropy=None, dentropy=None,
+                     workspace=None, stream=None):
+    """d L / d h into grad (bf16 [tokens, hidden]; may be h) from the gradients of head_logprob_fwd's logp and
+    entropy (fq_head_logprob_bwd)."""
+    n = "head_logprob_bwd"
+    dev = _device_of(n, h)
+    ws, nb = _scratch(n, workspace, dev)
+    full = (d.tokens, d.hidden)
+    _call(n, _lib.fq_head_logprob_bwd, dev, stream, ctypes.byref(d), _expect(n, "h", h, _BF16, full, dev),
+          _expect(n, "w", w, _BF16, (d.vocab, d.hidden), dev),
+          *_logprob_up(n, d, dev, ids, lse, entropy, dlogp, dentropy), _expect(n, "grad", grad, _BF16, full, dev),
+          ws, nb)
+
+
+class GradList:
+    """Gradients (fp32 or bf16, any shapes) and the places of their clipped values (the gradients themselves
+    without outs), as fq_grad_norm and fq_grad_clip take them.  Keeps the tensors."""
+
+    def __init__(self, grads, outs=None):
+        n = "grad_list"
+        self.grads, self.outs = list(grads), list(grads if outs is None else outs)
+        if len(self.grads) != len(self.outs):
+            raise ValueError(f"{n}: {len(self.grads)} gradients and {len(self.outs)} outputs")
+        self.device = _device_of(n, self.grads[0]) if self.grads else None
+        self.tensors = (GradTensor * len(self.grads))()
+        for e, g, o in zip(self.tensors, self.grads, self.outs):
+            if g.dtype is not _F32 and g.dtype is not _BF16:
+                raise ValueError(f"{n}: gradients must be {_F32} or {_BF16}, got {g.dtype}")
+            e.grad = _expect(n, "a gradient", g, g.dtype, g.shape, self.device)
+            e.out = _expect(n, "an output", o, g.dtype, g.shape, self.device)
+            e.count, e.dtype = g.numel(), FQ_F32 if g.dtype is _F32 else FQ_BF16
+
+
+def grad_list(grads, outs=None) -> GradList:
+    return GradList(grads, outs)
+
+
+def grad_norm_workspace_size(g: GradList) -> int:
+    return _lib.fq_grad_norm_workspace_size(g.tensors, len(g.tensors))
+
+
+def grad_norm(g: GradList, norm, workspace=None, stream=None):
+    """The L2 norm over all gradients of the list into norm (fp32 [1]; fq_grad_norm)."""
+    n = "grad_norm"
+    dev = _device_of(n, norm) if g.device is None else g.device
+    ws, nb = _scratch(n, workspace, dev)
+    _call(n, _lib.fq_grad_norm, dev, stream, g.tensors, len(g.tensors), _expect(n, "norm", norm, _F32, (1,), dev), ws,
+          nb)
+
+
+def grad_clip(g: GradList, max_grad_norm: float, norm, stream=None):
+    """Scale the list's gradients by min(1, max_grad_norm / (norm + 1e-6)) into its outputs (fq_grad_clip)."""
+    n = "grad_clip"
+    dev = _device_of(n, norm) if g.device is None else g.device
+    _call(n, _lib.fq_grad_clip, dev, stream, g.tensors, len(g.tensors), max_grad_norm,
+          _expect(n, "norm", norm, _F32, (1,), dev))
 
 
 def _scale_shape(q: QDesc, E, N, K):
