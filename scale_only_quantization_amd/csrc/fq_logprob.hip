@@ -11,6 +11,8 @@
 // combines the chunks of a row.  An entry is a key of 64 bits, the logit's order
 // above the id's complement: keys are distinct, and the largest key is the
 // largest logit, the lowest id among equal ones, in whatever order keys are met.
+#include <algorithm>
+
 #include "fq_head_product.h"
 #include "fq_ops.h"
 
@@ -18,35 +20,136 @@ namespace fq {
 namespace {
 
 constexpr int TPB = ROWS_TPB;
+// Blocks of rows: a row's chunks along x, rows along y and, from ROWS_Y on, z.
+constexpr int ROWS_Y = 32768;
+dim3 rows_grid(int64_t chunks, int64_t T) {
+    return dim3((unsigned)chunks, (unsigned)std::min<int64_t>(T, ROWS_Y), (unsigned)((T + ROWS_Y - 1) / ROWS_Y));
+}
 constexpr float FLOOR = -200.0f;          // e^FLOOR is 0 in fp32: keeps 0 times -inf out of sums
 constexpr float FLOOR2 = -300.0f;         // and 2^FLOOR2
+constexpr float PAST = -1e30f;            // a column past the vocabulary: below what a sum can hold, and finite
 
-__device__ __forceinline__ uint64_t key_of(float z, int64_t col) {
+// The order of a logit as a whole number: 0 is below all of them.
+__device__ __forceinline__ uint32_t order_of(float z) {
     const uint32_t b = __float_as_uint(z + 0.0f);                  // -0 counts as 0
-    const uint32_t o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-    return ((uint64_t)o << 32) | (uint32_t)~(uint32_t)col;
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+constexpr uint32_t ORDER_MIN = 0x007fffffu;                        // the order of -inf
+__device__ __forceinline__ uint64_t key_of(float z, int64_t col) {
+    return ((uint64_t)order_of(z) << 32) | (uint32_t)~(uint32_t)col;
 }
 __device__ __forceinline__ int32_t key_id(uint64_t key) { return (int32_t)~(uint32_t)key; }
-__device__ __forceinline__ float key_z(uint64_t key) {
-    const uint32_t o = (uint32_t)(key >> 32);
-    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+__device__ __forceinline__ float key_z(uint64_t key) { return value_of((uint32_t)(key >> 32)); }
+
+// lanes below this one in a mask
+__device__ __forceinline__ int lanes_before(uint64_t mask) {
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// Wave reductions by moves inside the vector unit (row_shr 1, 2, 4, 8, then
+// row_bcast 15 and 31; the last lane has the result), about a sixth of the time of
+// an exchange through LDS at each of the six steps.  In a fixed order.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t x) {            // 0 where no lane is moved in
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, ROWS == 0xf);
+}
+__device__ __forceinline__ uint32_t wave_top(uint32_t x) {
+    x = max(x, moved<0x111, 0xf>(x));
+    x = max(x, moved<0x112, 0xf>(x));
+    x = max(x, moved<0x114, 0xf>(x));
+    x = max(x, moved<0x118, 0xf>(x));
+    x = max(x, moved<0x142, 0xa>(x));
+    x = max(x, moved<0x143, 0xc>(x));
+    return __builtin_amdgcn_readlane(x, 63);
+}
+__device__ __forceinline__ float wave_total(float x) {
+    auto add = [&](uint32_t y) { x += __uint_as_float(y); };
+    add(moved<0x111, 0xf>(__float_as_uint(x)));
+    add(moved<0x112, 0xf>(__float_as_uint(x)));
+    add(moved<0x114, 0xf>(__float_as_uint(x)));
+    add(moved<0x118, 0xf>(__float_as_uint(x)));
+    add(moved<0x142, 0xa>(__float_as_uint(x)));
+    add(moved<0x143, 0xc>(__float_as_uint(x)));
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 63));
+}
+
+// A bound that at least `want` of the wave's 64 N numbers reach, near the largest
+// such: steps down from the largest, `top`, until enough reach it, then halves
+// until exactly `want` do, or 2^12 is left between the bounds.  Counting is one
+// comparison and a population count of its mask, without the lanes' exchange
+// that a sort needs (21 steps of two moves through LDS).
+template <int N>
+__device__ __forceinline__ uint32_t reached_by(const uint32_t (&o)[N], int want, uint32_t top) {
+    auto count = [&](uint32_t x) {
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) c += __popcll(__ballot(o[i] >= x));
+        return c;
+    };
+    uint32_t lo = top, hi = top, d = 1u << 20;
+    int c = count(lo);
+    while (c < want) {                                             // ends at 0, which all reach
+        hi = lo;
+        lo = lo > d ? lo - d : 0;
+        d <<= 1;
+        if (d == 0) lo = 0;
+        c = count(lo);
+    }
+    while (c > want && hi - lo > (1u << 12)) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const int n = count(mid);
+        if (n >= want) {
+            lo = mid;
+            c = n;
+        } else {
+            hi = mid;
+        }
+    }
+    return lo;
+}
+
+// 64 keys, one per lane: sorted in descending order (21 exchanges), and the 64
+// largest of two such lists (7).
+__device__ __forceinline__ uint64_t exchanged(uint64_t x, int d, bool larger) {
+    const uint64_t o = __shfl_xor((unsigned long long)x, d);
+    return (x > o) == larger ? x : o;
+}
+__device__ __forceinline__ uint64_t sorted_keys(uint64_t x) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int size = 2; size <= 64; size <<= 1)
+#pragma unroll
+        for (int d = size >> 1; d > 0; d >>= 1) x = exchanged(x, d, ((lane & size) == 0) == ((lane & d) == 0));
+    return x;
+}
+// `reversed` is the other list's key of lane 63 - lane
+__device__ __forceinline__ uint64_t merged_keys(uint64_t x, uint64_t reversed) {
+    const int lane = threadIdx.x & 63;
+    x = x > reversed ? x : reversed;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x = exchanged(x, d, (lane & d) == 0);
+    return x;
 }
 
 // The best keys of a block, in LDS: appended in any order, cut down to the k
 // best by counting for each key how many are larger.
 struct Best {
     static constexpr int CAP = 768;
-    uint64_t key[CAP];
+    __attribute__((aligned(16))) uint64_t key[CAP];
     uint64_t kth;          // keys below it cannot be among the k best
     int count;
+    // all threads call it; a barrier has to follow before the first push
     __device__ __forceinline__ void clear() {
         if (threadIdx.x == 0) {
             count = 0;
             kth = 1;                                               // 0 is no key
         }
-        __syncthreads();
     }
-    __device__ __forceinline__ void push(uint64_t x) {
+    __device__ __forceinline__ void push(bool in, uint64_t x) {
+        if (!in) return;
         const int at = atomicAdd(&count, 1);
         if (at < CAP) key[at] = x;
     }
@@ -57,47 +160,49 @@ struct Best {
         __syncthreads();
         return f;
     }
+    template <int Q>
+    __device__ __forceinline__ void rank(int n, int k) {
+        uint64_t mine[Q];
+        int r[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            mine[q] = (int)threadIdx.x + q * TPB < n ? key[threadIdx.x + q * TPB] : 0;
+            r[q] = 0;
+        }
+        const int to = wave_id() * WAVE < n ? n : 0;               // a wave without keys has nothing to count
+        int j = 0;
+        for (; j + 8 <= to; j += 8) {
+            uint64_t o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = key[j + e];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int q = 0; q < Q; ++q) r[q] += o[e] > mine[q] ? 1 : 0;
+        }
+        for (; j < to; ++j) {
+            const uint64_t o = key[j];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) r[q] += o > mine[q] ? 1 : 0;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (mine[q] != 0 && r[q] < k) {
+                key[r[q]] = mine[q];
+                if (r[q] == k - 1) kth = mine[q];
+            }
+    }
     // the k best in descending order at key[0 ..]; all threads call it
     __device__ void cut(int k) {
         __syncthreads();
         const int n = min(count, CAP);
-        uint64_t mine[CAP / TPB];
-        int rank[CAP / TPB];
-#pragma unroll
-        for (int q = 0; q < CAP / TPB; ++q) {
-            mine[q] = (int)threadIdx.x + q * TPB < n ? key[threadIdx.x + q * TPB] : 0;
-            rank[q] = 0;
-        }
-        for (int j = 0; j < n; ++j) {
-            const uint64_t o = key[j];
-#pragma unroll
-            for (int q = 0; q < CAP / TPB; ++q) rank[q] += o > mine[q] ? 1 : 0;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int q = 0; q < CAP / TPB; ++q)
-            if (mine[q] != 0 && rank[q] < k) {
-                key[rank[q]] = mine[q];
-                if (rank[q] == k - 1) kth = mine[q];
-            }
+        if (n <= TPB) rank<1>(n, k);
+        else rank<CAP / TPB>(n, k);
         if (threadIdx.x == 0) count = min(n, k);
         __syncthreads();
     }
 };
-
-// v of the wave's lanes in descending order
-__device__ __forceinline__ float sorted(float v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int size = 2; size <= 64; size <<= 1)
-#pragma unroll
-        for (int d = size >> 1; d > 0; d >>= 1) {
-            const float o = __shfl_xor(v, d);
-            const bool larger = ((lane & size) == 0) == ((lane & d) == 0);
-            v = larger ? fmaxf(v, o) : fminf(v, o);
-        }
-    return v;
-}
 
 // 16 bytes of a row as fp32
 template <typename IN>
@@ -105,14 +210,14 @@ struct Vec;
 template <>
 struct Vec<uint16_t> {
     static constexpr int N = 8;
+    __device__ static __forceinline__ float one(uint16_t x) { return bf_from_bits(x); }
     __device__ static __forceinline__ float get(const uint4& v, int e) {
         const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
         return (e & 1) ? bf_hi(w) : bf_lo(w);
     }
-    __device__ static __forceinline__ uint4 nothing() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
     // elements from n on are -inf
-    __device__ static __forceinline__ uint4 cut(uint4 v, int64_t n) {
-        auto two = [](uint32_t w, int64_t left) {
+    __device__ static __forceinline__ uint4 cut(uint4 v, int n) {
+        auto two = [](uint32_t w, int left) {
             return left >= 2 ? w : left == 1 ? (w & 0xffffu) | 0xff800000u : 0xff80ff80u;
         };
         return make_uint4(two(v.x, n), two(v.y, n - 2), two(v.z, n - 4), two(v.w, n - 6));
@@ -121,38 +226,51 @@ struct Vec<uint16_t> {
 template <>
 struct Vec<float> {
     static constexpr int N = 4;
+    __device__ static __forceinline__ float one(float x) { return x; }
     __device__ static __forceinline__ float get(const uint4& v, int e) {
         return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
     }
-    __device__ static __forceinline__ uint4 nothing() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
-    __device__ static __forceinline__ uint4 cut(uint4 v, int64_t n) {
+    __device__ static __forceinline__ uint4 cut(uint4 v, int n) {
         return make_uint4(n > 0 ? v.x : 0xff800000u, n > 1 ? v.y : 0xff800000u, n > 2 ? v.z : 0xff800000u,
                           n > 3 ? v.w : 0xff800000u);
     }
 };
 
-// A chunk: NL vectors per thread.
-template <typename IN, int NL>
+// The compiler is not to keep what it formed of these before (a second set of
+// registers for a chunk's unpacked elements halves the waves of a SIMD).
+template <int N>
+__device__ __forceinline__ void opaque(uint4 (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i].x), "+v"(v[i].y), "+v"(v[i].z), "+v"(v[i].w));
+}
+
+// A chunk: NL vectors per thread.  Its alternatives are the entries that reach a
+// bound which k threads' maxima reach: about 73 of 16384 for k = 64, kept
+// unsorted, at most rows_keys(k) of them.
+template <typename IN, int NL, bool ENT>
 __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
-    constexpr int VEC = Vec<IN>::N, CH = NL * VEC * TPB;
+    constexpr int VEC = Vec<IN>::N, CH = NL * VEC * TPB, WAVES = TPB / 64;
     __shared__ Best best;
-    __shared__ float red[3][TPB / 64];
-    const int64_t b = block_id(), t = b / a.pc, c = b - t * a.pc;
+    __shared__ float red[2][WAVES];
+    __shared__ uint32_t maxima[TPB];
+    __shared__ int found[WAVES];
+    const int64_t t = (int64_t)blockIdx.z * ROWS_Y + blockIdx.y, c = blockIdx.x;
     if (t >= a.T) return;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = wave_id();
     const IN* row = static_cast<const IN*>(a.z) + t * a.ld;
     const int64_t lo = c * CH;
+    // all loads first: past the row's end a thread reads its last vector again
+    const IN* src = row + lo;
+    const int left = (int)min(a.V - lo, (int64_t)CH), end = (left - 1) / VEC * VEC;
     uint4 v[NL];
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        const int64_t col = lo + (int64_t)(i * TPB + threadIdx.x) * VEC;
-        v[i] = col < a.n ? *reinterpret_cast<const uint4*>(row + col) : Vec<IN>::nothing();
-    }
-    if (lo + CH > a.n) {
+    for (int i = 0; i < NL; ++i)
+        v[i] = *reinterpret_cast<const uint4*>(src + min((i * TPB + (int)threadIdx.x) * VEC, end));
+    if (left < CH) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const int64_t left = a.n - (lo + (int64_t)(i * TPB + threadIdx.x) * VEC);
-            if (left < VEC) v[i] = Vec<IN>::cut(v[i], left);
+            const int n = left - (i * TPB + (int)threadIdx.x) * VEC;
+            if (n < VEC) v[i] = Vec<IN>::cut(v[i], n);
         }
     }
     float tm = -INFINITY;
@@ -160,63 +278,77 @@ __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
     for (int i = 0; i < NL; ++i)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) tm = fmaxf(tm, Vec<IN>::get(v[i], e));
-    const float wmax = wave_max(tm);
-    // The chunk's k-th best is at least what k threads reach: with a quarter of
-    // k threads in each wave, the least of the waves' values there.
-    const float at = a.k > 0 ? __shfl(sorted(tm), (a.k + TPB / 64 - 1) / (TPB / 64) - 1) : 0.0f;
-    if (lane == 0) {
-        red[0][w] = wmax;
-        red[1][w] = at;
-    }
-    if (a.k > 0) best.clear();
+    maxima[threadIdx.x] = order_of(tm);
+    best.clear();
     __syncthreads();
-    float M = red[0][0], thr = red[1][0];
+    // every wave for itself: the chunk's maximum and the bound
+    uint32_t o[WAVES], most = 0;
 #pragma unroll
-    for (int i = 1; i < TPB / 64; ++i) {
-        M = fmaxf(M, red[0][i]);
-        thr = fminf(thr, red[1][i]);
+    for (int i = 0; i < WAVES; ++i) {
+        o[i] = maxima[lane + 64 * i];
+        most = max(most, o[i]);
     }
+    most = wave_top(most);
+    const float M = value_of(most);
     if (a.k > 0) {
-        auto each = [&](auto&& f) {
+        const uint32_t r = reached_by(o, a.k, most);
+        const float thr = r > ORDER_MIN ? value_of(r) : -0x1.fffffep+127f;   // -inf is no alternative
+        // a wave's own part of the list, counted in a scalar
+        constexpr int PART = Best::CAP / WAVES;
+        int mine = 0;
+        opaque(v);
 #pragma unroll
-            for (int i = 0; i < NL; ++i)
+        for (int i = 0; i < NL; ++i)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float x = Vec<IN>::get(v[i], e);
-                    f(x, x >= thr && x > -INFINITY, a.c0 + lo + (int64_t)(i * TPB + threadIdx.x) * VEC + e);
+            for (int e = 0; e < VEC; ++e) {
+                const float x = Vec<IN>::get(v[i], e);
+                const uint64_t mask = __ballot(x >= thr);
+                if (mask != 0) {
+                    const int at = mine + lanes_before(mask);
+                    if (x >= thr && at < PART)
+                        best.key[w * PART + at] = key_of(x, lo + (i * TPB + (int)threadIdx.x) * VEC + e);
+                    mine += __popcll(mask);
                 }
-        };
-        each([&](float x, bool in, int64_t col) {
-            if (in) best.push(key_of(x, col));
-        });
+            }
+        if (lane == 0) found[w] = mine;
         __syncthreads();
-        if (best.count > Best::CAP) {                              // many equal ones: again, cut down on the way
-            __syncthreads();
-            best.clear();
-            each([&](float x, bool in, int64_t col) {
-                const uint64_t key = key_of(x, col);
-                if (in && key >= best.kth) best.push(key);
-                if (best.full()) best.cut(a.k);
-            });
+        const int cap = rows_keys(a.k);
+        int total = 0, base = 0;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+            base += i < w ? found[i] : 0;
+            total += found[i];
         }
-        best.cut(a.k);
-        uint64_t* out = a.keys + (t * a.nc + a.chunk0 + c) * a.k;
-        if ((int)threadIdx.x < a.k) out[threadIdx.x] = (int)threadIdx.x < best.count ? best.key[threadIdx.x] : 0;
+        uint64_t* out = a.keys + (t * a.nc + c) * cap;
+        if (total <= cap) {                                        // cap <= PART: no part is cut off
+            for (int i = lane; i < mine; i += 64) out[base + i] = best.key[w * PART + i];
+            for (int i = total + threadIdx.x; i < cap; i += TPB) out[i] = 0;
+        } else {                                                   // many equal ones: again, cut down on the way
+            for (int col = threadIdx.x; col < CH; col += TPB) {
+                const float x = col < left ? Vec<IN>::one(src[col]) : -INFINITY;
+                const uint64_t key = key_of(x, lo + col);
+                best.push(x >= thr && key >= best.kth, key);
+                if (total > Best::CAP && best.full()) best.cut(a.k);
+            }
+            best.cut(a.k);
+            for (int i = threadIdx.x; i < cap; i += TPB) out[i] = i < best.count ? best.key[i] : 0;
+        }
     }
-    const float f = M == -INFINITY ? 0.0f : M;
+    // the frame is M log2 e, rounded; its rounding d is taken off at the end
+    const float m = M == -INFINITY ? 0.0f : M, f = m * LOG2E, d = __builtin_fmaf(m, LOG2E, -f);
     float s = 0.0f, u = 0.0f;
+    opaque(v);
 #pragma unroll
     for (int i = 0; i < NL; ++i)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            const float d = Vec<IN>::get(v[i], e) - f;
-            const float x = exp2_hw(d * LOG2E);
+            const float l = __builtin_fmaf(Vec<IN>::get(v[i], e), LOG2E, -f);
+            const float x = exp2_hw(l);
             s += x;
-            u = __builtin_fmaf(x, fmaxf(d, FLOOR), u);
+            if (ENT) u = __builtin_fmaf(x, fmaxf(l, FLOOR2), u);
         }
-    s = wave_sum(s);
-    u = wave_sum(u);
-    __syncthreads();
+    s = wave_total(s);
+    if (ENT) u = wave_total(u);
     if (lane == 0) {
         red[0][w] = s;
         red[1][w] = u;
@@ -225,47 +357,109 @@ __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
     if (threadIdx.x == 0) {
         s = red[0][0];
         u = red[1][0];
-        for (int i = 1; i < TPB / 64; ++i) {
+        for (int i = 1; i < WAVES; ++i) {
             s += red[0][i];
             u += red[1][i];
         }
-        a.part[t * a.nc + a.chunk0 + c] = make_float4(M, s, u, 0.0f);
+        a.part[t * a.nc + c] = make_float4(M, __builtin_fmaf(-d * LN2, s, s), LN2 * __builtin_fmaf(-d, s, u), 0.0f);
     }
 }
 
-// The chunks of a row.
+// The chunks of a row.  Keys come in batches of 8 a thread, of which those are
+// kept that reach a bound formed as in a chunk.
+template <typename IN>
 __global__ __launch_bounds__(TPB) void k_rows_join(RowsArgs a) {
+    constexpr int WAVES = TPB / 64, PER = 8;
     __shared__ Best best;
-    __shared__ float red[4][TPB / 64];
-    __shared__ uint64_t floor_key[TPB / 64];
+    __shared__ float red[3][WAVES];
+    __shared__ uint32_t maxima[TPB];
     const int64_t t = block_id();
     if (t >= a.T) return;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = wave_id();
+    // the first loads of everything that does not depend on another
     const float4* part = a.part + t * a.nc;
-    float M = -INFINITY;
-    for (int64_t i = threadIdx.x; i < a.nc; i += TPB) M = fmaxf(M, part[i].x);
-    M = wave_max(M);
+    float4 p0 = part[min((int64_t)threadIdx.x, a.nc - 1)];
+    const int cap = a.k > 0 ? rows_keys(a.k) : 0;
+    const int64_t n = a.nc * cap;
+    const uint64_t* keys = a.keys + t * n;
+    uint64_t x[PER];
+    auto load = [&](int64_t i0) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) x[i] = keys[min(i0 + i * TPB + threadIdx.x, n - 1)];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) x[i] = i0 + i * TPB + threadIdx.x < n ? x[i] : 0;
+    };
+    if (a.k > 0) load(0);
+    const int id = (int)threadIdx.x < a.m ? a.ids[t * a.m + threadIdx.x] : -1;
+    const bool given = id >= 0 && id < a.V;
+    if ((int64_t)threadIdx.x >= a.nc) p0 = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    float zg = 0.0f;
+    if (given) {
+        zg = Vec<IN>::one(static_cast<const IN*>(a.z)[t * a.ld + id]);
+    }
+    float M = p0.x;
+    for (int64_t i = threadIdx.x + TPB; i < a.nc; i += TPB) M = fmaxf(M, part[i].x);
+    M = value_of(wave_top(order_of(M)));
     if (lane == 0) red[0][w] = M;
+    if (a.k > 0) best.clear();
     __syncthreads();
-    for (int i = 0; i < TPB / 64; ++i) M = fmaxf(M, red[0][i]);
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) M = fmaxf(M, red[0][i]);
     const float f = M == -INFINITY ? 0.0f : M;
     float s = 0.0f, u = 0.0f;
-    for (int64_t i = threadIdx.x; i < a.nc; i += TPB) {
-        const float4 q = part[i];
-        const float d = q.x - f, x = exp2_hw(d * LOG2E);
-        s = __builtin_fmaf(q.y, x, s);
-        u = __builtin_fmaf(__builtin_fmaf(fmaxf(d, FLOOR), q.y, q.z), x, u);
-    }
-    s = wave_sum(s);
-    u = wave_sum(u);
+    auto add = [&](const float4& q) {
+        const float d = q.x - f, e = exp2_hw(d * LOG2E);
+        s = __builtin_fmaf(q.y, e, s);
+        u = __builtin_fmaf(__builtin_fmaf(fmaxf(d, FLOOR), q.y, q.z), e, u);
+    };
+    add(p0);
+    for (int64_t i = threadIdx.x + TPB; i < a.nc; i += TPB) add(part[i]);
+    s = wave_total(s);
+    u = wave_total(u);
     if (lane == 0) {
         red[1][w] = s;
         red[2][w] = u;
     }
+    for (int64_t i0 = 0; i0 < n; i0 += PER * TPB) {
+        if (i0 > 0) load(i0);
+        uint32_t own = 0, o[WAVES], most = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) own = max(own, (uint32_t)(x[i] >> 32));
+        maxima[threadIdx.x] = own;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+            o[i] = maxima[lane + 64 * i];
+            most = max(most, o[i]);
+        }
+        const uint32_t least = reached_by(o, a.k, wave_top(most));
+        const uint64_t kth = best.kth;
+        const int before = best.count;
+        const uint64_t from = max((uint64_t)least << 32, kth);     // kth is at least 1: 0 is no key
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PER; ++i) best.push(x[i] >= from, x[i]);
+        __syncthreads();
+        if (best.count > Best::CAP) {                              // many equal ones: again, cut down on the way
+            __syncthreads();
+            if (threadIdx.x == 0) best.count = before;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                best.push(x[i] >= from && x[i] >= best.kth, x[i]);
+                if (best.full()) best.cut(a.k);
+            }
+        }
+        if (i0 + PER * TPB < n) {
+            if (best.full()) best.cut(a.k);
+        } else {
+            best.cut(a.k);
+        }
+    }
     __syncthreads();
     s = red[1][0];
     u = red[2][0];
-    for (int i = 1; i < TPB / 64; ++i) {
+    for (int i = 1; i < WAVES; ++i) {
         s += red[1][i];
         u += red[2][i];
     }
@@ -276,42 +470,12 @@ __global__ __launch_bounds__(TPB) void k_rows_join(RowsArgs a) {
         if (a.entropy) a.entropy[t] = none ? 0.0f : ls - u / s;
     }
     auto logp = [&](float z) {
-        const float x = none ? -INFINITY : z - lse;
-        return x > 0.0f ? 0.0f : x;
+        const float q = none ? -INFINITY : z - lse;
+        return q > 0.0f ? 0.0f : q;
     };
-    for (int j = threadIdx.x; j < a.m; j += TPB) {
-        const int id = a.ids[t * a.m + j];
-        float x = 0.0f;
-        if (id >= 0 && id < a.V) {
-            x = a.zs ? a.zs[t * a.m + j] : bf_from_bits(static_cast<const uint16_t*>(a.z)[t * a.ld + id]);
-            x = logp(x);
-        }
-        a.logp[t * a.m + j] = x;
-    }
-    if (a.k == 0) return;
-    // The row's k-th best is at least what k / nc entries of every chunk reach.
-    const uint64_t* keys = a.keys + t * a.nc * a.k;
-    const int64_t n = a.nc * a.k, share = (a.k + a.nc - 1) / a.nc;
-    uint64_t least = ~0ull;
-    for (int64_t i = threadIdx.x; i < a.nc; i += TPB) {
-        const uint64_t x = keys[i * a.k + share - 1];
-        least = x < least ? x : least;
-    }
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const uint64_t o = __shfl_xor(least, m);
-        least = o < least ? o : least;
-    }
-    if (lane == 0) floor_key[w] = least;
-    best.clear();                                                  // its barrier orders floor_key
-    for (int i = 0; i < TPB / 64; ++i) least = floor_key[i] < least ? floor_key[i] : least;
-    for (int64_t i0 = 0; i0 < n; i0 += TPB) {
-        const uint64_t x = i0 + threadIdx.x < n ? keys[i0 + threadIdx.x] : 0;
-        if (x >= least && x >= best.kth) best.push(x);
-        if (best.full()) best.cut(a.k);
-    }
-    best.cut(a.k);
-    for (int j = threadIdx.x; j < a.k; j += TPB) {
+    if ((int)threadIdx.x < a.m) a.logp[t * a.m + threadIdx.x] = given ? logp(zg) : 0.0f;
+    if ((int)threadIdx.x < a.k) {
+        const int j = threadIdx.x;
         const bool there = j < best.count;
         a.top_ids[t * a.k + j] = there ? key_id(best.key[j]) : -1;
         a.top_logp[t * a.k + j] = there ? logp(key_z(best.key[j])) : -INFINITY;
@@ -325,8 +489,7 @@ __global__ __launch_bounds__(TPB) void k_logp_bwd(LogpBwdArgs a) {
     constexpr int CH = NB * 8 * TPB;
     __shared__ int sid[64];
     __shared__ float sa[64], sz[64];
-    const int64_t chunks = (a.V + CH - 1) / CH;
-    const int64_t b = block_id(), t = b / chunks, lo = (b - t * chunks) * CH;
+    const int64_t t = (int64_t)blockIdx.z * ROWS_Y + blockIdx.y, lo = (int64_t)blockIdx.x * CH;
     if (t >= a.T) return;
     const uint16_t* row = a.z + t * a.ld;
     if ((int)threadIdx.x < a.m) {
@@ -352,7 +515,7 @@ __global__ __launch_bounds__(TPB) void k_logp_bwd(LogpBwdArgs a) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
         const int64_t col = lo + (int64_t)(i * TPB + threadIdx.x) * 8;
-        if (col < a.V) v[i] = *reinterpret_cast<const uint4*>(row + col);
+        v[i] = *reinterpret_cast<const uint4*>(row + min(col, (a.V - 1) / 8 * 8));
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
@@ -393,23 +556,23 @@ int64_t rows_chunk(int64_t T, int64_t V) {
     return T * ((V + 16383) / 16384) >= 512 ? 16384 : 4096;
 }
 
-static hipError_t launch_join(const RowsArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL(k_rows_join, grid_of(a.T), dim3(TPB), 0, st, a);
+template <typename IN, int NL>
+static hipError_t launch_rows(const RowsArgs& a, hipStream_t st) {
+    if (a.entropy) hipLaunchKernelGGL((k_rows_chunk<IN, NL, true>), rows_grid(a.nc, a.T), dim3(TPB), 0, st, a);
+    else hipLaunchKernelGGL((k_rows_chunk<IN, NL, false>), rows_grid(a.nc, a.T), dim3(TPB), 0, st, a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL(k_rows_join<IN>, grid_of(a.T), dim3(TPB), 0, st, a);
     return hipGetLastError();
 }
 
 hipError_t launch_logprob_rows(const RowsArgs& a, hipStream_t st) {
-    if (rows_chunk(a.T, a.V) == 16384)
-        hipLaunchKernelGGL((k_rows_chunk<uint16_t, 8>), grid_of(a.T * a.pc), dim3(TPB), 0, st, a);
-    else
-        hipLaunchKernelGGL((k_rows_chunk<uint16_t, 2>), grid_of(a.T * a.pc), dim3(TPB), 0, st, a);
-    const hipError_t err = hipGetLastError();
-    return err != hipSuccess ? err : launch_join(a, st);
+    return rows_chunk(a.T, a.V) == 16384 ? launch_rows<uint16_t, 8>(a, st) : launch_rows<uint16_t, 2>(a, st);
 }
 
 hipError_t launch_logprob_bwd(const LogpBwdArgs& a, hipStream_t st) {
     const int64_t chunks = (a.V + NB * 8 * TPB - 1) / (NB * 8 * TPB);
-    hipLaunchKernelGGL(k_logp_bwd, grid_of(a.T * chunks), dim3(TPB), 0, st, a);
+    hipLaunchKernelGGL(k_logp_bwd, rows_grid(chunks, a.T), dim3(TPB), 0, st, a);
     return hipGetLastError();
 }
 
@@ -438,11 +601,94 @@ __global__ __launch_bounds__(256) void k_logp_given(HeadLogpArgs a) {
     if (lane == 0) a.zs[i] = acc;
 }
 
-// The tile product of the output layer's loss with another epilogue: the
-// forward stores the logits, the backward P = -p (A + b (log p + entropy)) in bf16.
-template <bool BWD>
+// Logits of a few tokens, in fp32: the weight is read once, 16 rows by 32 columns
+// a load (64 bytes of a row in neighbouring lanes, two loads a cache line), straight
+// into the matrix instruction's operand; the hidden states stand in LDS, rows 16
+// bytes apart from a multiple of the banks.  A wave takes every so many-th 16 rows
+// and has the loads of the next STEP columns in flight while it multiplies, over
+// the ends of rows too.
+constexpr int FEW_LOADS = 8, FEW_STEP = 32 * FEW_LOADS;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+template <int NT, int BYTES, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_head_few(HeadLogpArgs a) {
+    __shared__ __attribute__((aligned(16))) char sh[BYTES];
+    const int lane = threadIdx.x & 63, tok = lane & 15, kc = lane >> 4;
+    const int T = (int)a.T, H = a.H, ldh = 2 * H + 16, chunks = H >> 3;
+    for (int i = threadIdx.x; i < T * chunks; i += THREADS) {
+        const int t = i / chunks, c = i - t * chunks;
+        *reinterpret_cast<uint4*>(sh + t * ldh + c * 16) = reinterpret_cast<const uint4*>(a.h)[i];
+    }
+    __syncthreads();
+    const char* hb[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) hb[n] = sh + min(16 * n + tok, T - 1) * ldh + kc * 16;
+    const int64_t tiles = (a.V + 15) / 16, waves = (int64_t)gridDim.x * (THREADS / 64);
+    const int steps = (H + FEW_STEP - 1) / FEW_STEP;
+    int64_t tile = (int64_t)blockIdx.x * (THREADS / 64) + wave_id();
+    if (tile >= tiles) return;
+    int64_t ltile = tile;                                  // the loads' place, a step ahead
+    int lstep = 0;
+    const uint16_t* lrow = a.w + min(ltile * 16 + tok, a.V - 1) * H + kc * 8;
+    auto load = [&](bf16x8 (&v)[FEW_LOADS]) {
+        if (ltile >= tiles) return;
+#pragma unroll
+        for (int i = 0; i < FEW_LOADS; ++i) {
+            const int k = lstep * FEW_STEP + 32 * i;
+            v[i] = *reinterpret_cast<const bf16x8*>(lrow + (k < H ? k : 0));
+        }
+        if (++lstep == steps) {
+            lstep = 0;
+            ltile += waves;
+            lrow = a.w + min(ltile * 16 + tok, a.V - 1) * H + kc * 8;
+        }
+    };
+    f32x4 acc[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    int step = 0;
+    auto multiply = [&](const bf16x8 (&v)[FEW_LOADS]) {
+#pragma unroll
+        for (int i = 0; i < FEW_LOADS; ++i) {
+            const int k = step * FEW_STEP + 32 * i;
+            if (k < H)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        v[i], *reinterpret_cast<const bf16x8*>(hb[n] + 2 * k), acc[n], 0, 0, 0);
+        }
+        if (++step < steps) return;
+        step = 0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (16 * n + tok < T)
+                *reinterpret_cast<f32x4*>(a.z + (int64_t)(16 * n + tok) * a.vc + tile * 16 + 4 * kc) = acc[n];
+            acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        tile += waves;
+    };
+    bf16x8 v0[FEW_LOADS], v1[FEW_LOADS];
+    load(v0);
+    while (true) {
+        load(v1);
+        multiply(v0);
+        if (tile >= tiles) break;
+        load(v0);
+        multiply(v1);
+        if (tile >= tiles) break;
+    }
+}
+
+// The tile product of the output layer's loss with other epilogues.
+//   SUMS  of each token's 64 columns of a wave: the maximum m, s = sum 2^x with
+//         x = z log2 e - m log2 e, and with ENT u = sum 2^x x
+//   TOP   these, and the 64 logits themselves where m is above the token's bound,
+//         the k-th best logit of the pieces before: of a long row that is seldom
+//   GRAD  P = -p (A + b (log p + entropy)) in bf16
+enum : int { SUMS = 0, TOP = 1, GRAD = 2 };
+template <int MODE, bool ENT>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k_head_z(HeadLogpArgs a) {
-    constexpr int ROWC = BWD ? BM * 16 : 0;
+    // a token's constants of the epilogue: its bound, or its row of rowc
+    constexpr int CB = MODE == GRAD ? 16 : MODE == TOP ? 4 : 0, ROWC = BM * CB;
     __shared__ __attribute__((aligned(1024))) char smem_raw[SMEM + 2 * ROWC];
     lds_t* smem = (lds_t*)smem_raw;
     const int lane = threadIdx.x & 63, wave = wave_id();
@@ -467,12 +713,13 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
         int tn;
         const int rows = at(i, &m0, &tn);
         const int64_t v0 = a.c0 + (int64_t)tn * BN;
-        const int cols = (int)min((int64_t)BN, a.V - v0);
+        const int cols = (int)min((int64_t)BN, a.V - v0);             // may be <= 0 in the last piece's padding
         la.rs = make_rsrc_words(a.h + m0 * a.H, (int64_t)rows * a.H * 2);
         lb.rs = make_rsrc_words(a.w + (cols > 0 ? v0 : 0) * a.H, (int64_t)cols * a.H * 2);
-        if (BWD && wave < 4) {                                     // 64 rows' constants per wave
+        if (MODE != SUMS && wave < CB / 4) {                          // 1 KB per wave
+            const char* c = MODE == GRAD ? reinterpret_cast<const char*>(a.rowc + m0) : reinterpret_cast<const char*>(a.thr + m0);
             const uint32_t voff[1] = {(uint32_t)(wave * 64 + lane) * 16};
-            stage_loads<1, 0>(make_rsrc_words(a.rowc + m0, (int64_t)rows * 16),
+            stage_loads<1, 0>(make_rsrc_words(c, (int64_t)(rows + 3) / 4 * 4 * CB),
                               smem + SMEM + (i & 1) * ROWC + wave * 1024, voff, 0);
         }
     };
@@ -487,30 +734,71 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
         int tn;
         const int rows = at(i, &m0, &tn), sub = nti(i);
         int lane = threadIdx.x & 63;
-        asm volatile("" : "+v"(lane));
+        asm volatile("" : "+v"(lane));                                // what follows from it is not held through the steps
         const int cols = (int)min((int64_t)BN, a.V - a.c0 - (int64_t)tn * BN);
+        const lds_t* consts = smem + SMEM + (i & 1) * ROWC;
 #pragma unroll
         for (int ti = 0; ti < WTM; ++ti) {
             if (ti >= sub) break;
             const int row = wm * wr + ti * 32 + (lane & 31);
-            if (!BWD) {
-                const __amdgpu_buffer_rsrc_t zrs = make_rsrc(a.z + m0 * a.vc + (int64_t)tn * BN,
-                                                             (int64_t)(rows - 1) * a.vc * 4 + BN * 4);
+            auto past = [&](float x) {                                // the columns past the vocabulary become x
+                if (cols < BN) {
+#pragma unroll
+                    for (int tj = 0; tj < WTN; ++tj)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v)
+                            if (wn * 64 + tj * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3) >= cols)
+                                acc[ti][tj][v] = x;
+                }
+            };
+            if constexpr (MODE != GRAD) {
+                past(PAST);
+                float m = acc[ti][0][0];
 #pragma unroll
                 for (int tj = 0; tj < WTN; ++tj)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        u32x4 c;
+                    for (int v = 0; v < 16; ++v) m = fmaxf(m, acc[ti][tj][v]);
+                m = fmaxf(m, xor32(m));
+                if constexpr (MODE == TOP) {
+                    const __amdgpu_buffer_rsrc_t zrs = make_rsrc(a.z + m0 * a.vc + (int64_t)tn * BN,
+                                                                 (int64_t)(rows - 1) * a.vc * 4 + BN * 4);
+                    const float thr = reinterpret_cast<const __attribute__((address_space(3))) float*>(consts)[row];
+                    if (a.first || m > thr) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) c[j] = __float_as_uint(acc[ti][tj][4 * q + j]);
-                        const int col = wn * 64 + tj * 32 + 8 * q + 4 * (lane >> 5);
-                        __builtin_amdgcn_raw_buffer_store_b128(c, zrs, (uint32_t)row * (uint32_t)a.vc * 4u + col * 4, 0, 0);
+                        for (int tj = 0; tj < WTN; ++tj)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                u32x4 c;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) c[j] = __float_as_uint(acc[ti][tj][4 * q + j]);
+                                const int col = wn * 64 + tj * 32 + 8 * q + 4 * (lane >> 5);
+                                __builtin_amdgcn_raw_buffer_store_b128(
+                                    c, zrs, (uint32_t)row * (uint32_t)a.vc * 4u + col * 4, 0, 0);
+                            }
                     }
+                }
+                const float f = m * LOG2E;
+                float s = 0.0f, u = 0.0f;
+#pragma unroll
+                for (int tj = 0; tj < WTN; ++tj)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) {
+                        const float x = __builtin_fmaf(acc[ti][tj][v], LOG2E, -f), e = exp2_hw(x);
+                        s += e;
+                        if (ENT) u = __builtin_fmaf(e, x, u);
+                    }
+                s += xor32(s);
+                if (ENT) u += xor32(u);
+                const int64_t o = ((int64_t)tn * 4 + wn) * a.T + m0 + row;
+                if (lane < 32 && row < rows) {
+                    a.stats[o] = make_float2(m, s);
+                    if (ENT) a.ustats[o] = u;
+                }
             } else {
                 const __amdgpu_buffer_rsrc_t prs = make_rsrc(a.p + m0 * a.vc + (int64_t)tn * BN,
                                                              (int64_t)(rows - 1) * a.vc * 2 + BN * 2);
                 const __attribute__((address_space(3))) float4* rc =
-                    reinterpret_cast<const __attribute__((address_space(3))) float4*>(smem + SMEM + (i & 1) * ROWC);
+                    reinterpret_cast<const __attribute__((address_space(3))) float4*>(consts);
                 const float f = rc[row].x, c = rc[row].y, b = rc[row].z * LN2;
 #pragma unroll
                 for (int tj = 0; tj < WTN; ++tj)
@@ -519,14 +807,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
                         const float l = fmaxf(__builtin_fmaf(acc[ti][tj][v], LOG2E, -f), FLOOR2);   // log2 p
                         acc[ti][tj][v] = -exp2_hw(l) * __builtin_fmaf(b, l, c);
                     }
-                if (cols < BN) {                                   // columns past the vocabulary
-#pragma unroll
-                    for (int tj = 0; tj < WTN; ++tj)
-#pragma unroll
-                        for (int v = 0; v < 16; ++v)
-                            if (wn * 64 + tj * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3) >= cols)
-                                acc[ti][tj][v] = 0.0f;
-                }
+                past(0.0f);
 #pragma unroll
                 for (int tj = 0; tj < WTN; ++tj)
 #pragma unroll
@@ -547,6 +828,247 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
         }
     };
     product(la, lb, acc, smem, (t1 - t0 + per - 1) / per, a.H / BK, wr, next, nti, epilogue);
+}
+
+// A piece joins its tokens' running sums and alternatives: 16 / WPT tokens per
+// block, first 64 WPT threads per token over the strips of 64 columns, then WPT
+// waves per token over the strips that can hold an alternative.  A wave's best are
+// its lanes' keys in descending order; logits above the k-th are gathered in LDS
+// and put in 64 at a time by a sort and a merge, the last few one at a time.
+// Sums are joined in frames of z itself: a strip's base-2 frame, m log2 e rounded,
+// is known exactly with its rounding d, and s and u are brought from it to m.
+constexpr int MWORDS = LOGP_MAX_PIECE / 64 / 32, MLIST = 16, MPARTS = 256;
+template <int WPT>
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void k_logp_merge(HeadLogpArgs a) {
+    constexpr int TOK = 16 / WPT, PER = 1024 / TOK, SUB = MPARTS / PER, UN = 8;
+    __shared__ float red[3][16][TOK];
+    __shared__ float tmax[TOK][MPARTS];
+    __shared__ uint32_t flag[TOK][MWORDS];
+    __shared__ uint16_t list[16][MLIST * 32];
+    __shared__ float bound[TOK];
+    __shared__ uint64_t keys[16][128];
+    const int tok = threadIdx.x & (TOK - 1), sl = threadIdx.x / TOK, lane = threadIdx.x & 63, w = wave_id();
+    // An XCD has a run of neighbouring tokens: their strips lie in the same cache lines.
+    const int group = xcd_tile(blockIdx.x, gridDim.x, (int)((a.T + TOK - 1) / TOK));
+    if (group < 0) return;
+    const int64_t t0 = (int64_t)group * TOK, tc = min(t0 + tok, a.T - 1);
+    const int strips = (int)((min((int64_t)a.vc, a.V - a.c0) + 63) / 64), words = (strips + 31) / 32;
+    const bool ent = a.entropy != nullptr, top = a.k > 0;
+    if (top) {
+        for (int i = sl; i < words; i += PER) flag[tok][i] = 0;
+        __syncthreads();
+    }
+    const float thr = top && !a.first ? a.thr[tc] : -INFINITY;
+    // what the later steps need of the pieces before, ahead of the strips: from
+    // the barrier on wave w is part `sub` of token t
+    const int tk = w / WPT, sub = w % WPT;
+    const int64_t t = t0 + tk, tl = min(t, a.T - 1);
+    const bool live = t < a.T;
+    float4 before = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    uint64_t best = 0;                                     // the wave's best, sorted
+    float kth = -INFINITY;                                 // k logits, all of lower ids, are at least this
+    if (!a.first) {
+        before = a.run[tl];
+        if (top) {
+            kth = a.thr[tl];
+            if (sub == 0 && lane < a.k && a.best_i[tl * a.k + lane] >= 0)
+                best = key_of(a.best_z[tl * a.k + lane], a.best_i[tl * a.k + lane]);
+        }
+    }
+    // M, s, u of the thread's strips, maxima of SUB parts of them
+    float M = -INFINITY, s = 0.0f, u = 0.0f, tm[SUB];
+    auto join = [&](float m2, float s2, float u2) {        // (M, s, u) and another
+        const float n = fmaxf(M, m2);
+        const float d1 = fmaxf(M == n ? 0.0f : M - n, FLOOR), d2 = fmaxf(m2 == n ? 0.0f : m2 - n, FLOOR);
+        const float e1 = exp2_hw(d1 * LOG2E), e2 = exp2_hw(d2 * LOG2E);
+        u = __builtin_fmaf(e1, __builtin_fmaf(d1, s, u), e2 * __builtin_fmaf(d2, s2, u2));
+        s = __builtin_fmaf(e1, s, e2 * s2);
+        M = n;
+    };
+#pragma unroll
+    for (int j = 0; j < SUB; ++j) tm[j] = -INFINITY;
+    for (int i0 = sl; i0 < strips; i0 += PER * UN) {
+        float2 v[UN];
+        float vu[UN];
+#pragma unroll
+        for (int j = 0; j < UN; ++j) {
+            const int64_t i = min(i0 + PER * j, strips - 1) * a.T + tc;
+            v[j] = a.stats[i];
+            vu[j] = ent ? a.ustats[i] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < UN; ++j) {
+            const int i = i0 + PER * j;
+            if (i >= strips) break;
+            const float m = v[j].x, d = __builtin_fmaf(m, LOG2E, -(m * LOG2E));
+            tm[j % SUB] = fmaxf(tm[j % SUB], m);
+            join(m, __builtin_fmaf(-d * LN2, v[j].y, v[j].y), LN2 * __builtin_fmaf(-d, v[j].y, vu[j]));
+            if (top && m > thr) atomicOr(&flag[tok][i >> 5], 1u << (i & 31));
+        }
+    }
+    // over the token's threads: those of a wave, then the 16 waves, in a fixed order
+#pragma unroll
+    for (int m = TOK; m < 64; m <<= 1) {
+        const float m2 = __shfl_xor(M, m), s2 = __shfl_xor(s, m), u2 = __shfl_xor(u, m);
+        join(m2, s2, u2);
+    }
+    if (lane < TOK) {
+        red[0][w][tok] = M;
+        red[1][w][tok] = s;
+        red[2][w][tok] = u;
+    }
+    if (top)
+#pragma unroll
+        for (int j = 0; j < SUB; ++j) tmax[tok][sl * SUB + j] = tm[j];
+    __syncthreads();
+    M = red[0][lane & 15][tk];
+    s = red[1][lane & 15][tk];
+    u = red[2][lane & 15][tk];
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) {
+        const float m2 = __shfl_xor(M, m), s2 = __shfl_xor(s, m), u2 = __shfl_xor(u, m);
+        join(m2, s2, u2);
+    }
+    join(before.x, before.y, before.z);
+    const float ls = logf(s), lse = M + ls;
+    auto logp = [&](float z) {
+        const float q = z - lse;
+        return q > 0.0f ? 0.0f : q;
+    };
+    if (live && a.last && sub == 0) {
+        if (lane == 0) {
+            if (a.lse) a.lse[t] = lse;
+            if (ent) a.entropy[t] = ls - u / s;
+        }
+        if (lane < a.m) {
+            const int id = a.ids[t * a.m + lane];
+            a.logp[t * a.m + lane] = id >= 0 && id < a.V ? logp(a.zs[t * a.m + lane]) : 0.0f;
+        }
+    }
+    // More strips above the bound than k: a bound that k parts' maxima reach keeps
+    // most of them out (a first piece has no bound before: 75 strips of 1024 for k = 64).
+    int marked = 0;
+    float from = -INFINITY;
+    if (top) {
+        for (int i = lane; i < words; i += 64) marked += __popc(flag[tk][i]);
+        marked = (int)wave_total((float)marked);
+        if (marked > a.k) {
+            uint32_t o[MPARTS / 64], most = 0;
+#pragma unroll
+            for (int j = 0; j < MPARTS / 64; ++j) {
+                o[j] = order_of(tmax[tk][lane + 64 * j]);
+                most = max(most, o[j]);
+            }
+            const uint32_t r = reached_by(o, a.k, wave_top(most));
+            from = r > ORDER_MIN ? value_of(r) : -INFINITY;
+        }
+        if (lane == 0) bound[tk] = from;
+    }
+    // (a barrier for all: every part has read run before one writes it)
+    if (__syncthreads_or(marked > a.k)) {
+        for (int i = sl; i < words; i += PER) flag[tok][i] = 0;
+        __syncthreads();
+        const float least = bound[tok];
+#pragma unroll 8
+        for (int i = sl; i < strips; i += PER) {
+            const float m = a.stats[(int64_t)i * a.T + tc].x;
+            if (m > thr && m >= least) atomicOr(&flag[tok][i >> 5], 1u << (i & 31));
+        }
+        __syncthreads();
+    }
+    if (live && lane == 0 && sub == 0 && !a.last) a.run[t] = make_float4(M, s, u, 0.0f);
+    if (!top) return;
+    const float* zr = a.z + tl * a.vc;
+    const int cols = (int)min((int64_t)a.vc, a.V - a.c0);
+    int n = 0;
+    // f(logit of this lane, the strip's first column) for the wave's part of the listed strips, N in flight
+    auto strips_by = [&](int i0, auto n_c, auto&& f) {
+        constexpr int N = decltype(n_c)::value;
+        float z[N];
+        int col[N];
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            col[q] = __builtin_amdgcn_readfirstlane(list[w][min(i0 + q * WPT, n - 1)]) * 64;
+            z[q] = zr[min(col[q] + lane, cols - 1)];
+        }
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+            if (i0 + q * WPT < n) f(col[q] + lane < cols ? z[q] : -INFINITY, col[q], q);
+        return i0 + N * WPT;
+    };
+    auto each_strip = [&](auto&& f) {
+        int i0 = sub;
+        while (i0 + 4 * WPT < n) i0 = strips_by(i0, std::integral_constant<int, 16>{}, f);
+        if (i0 < n) strips_by(i0, std::integral_constant<int, 4>{}, f);
+    };
+    int gathered = 0;
+    auto put = [&](int n) {                                // the first n <= 64 gathered keys
+        if (n <= 32) {
+            // one at a time: the lanes it does not pass stay, the others move on
+            for (int j = 0; j < n; ++j) {
+                const uint64_t x = keys[w][j];
+                const uint32_t lo = __builtin_amdgcn_update_dpp(-1, (int)(uint32_t)best, 0x138, 0xf, 0xf, false);
+                const uint32_t hi = __builtin_amdgcn_update_dpp(-1, (int)(uint32_t)(best >> 32), 0x138, 0xf, 0xf, false);
+                const uint64_t before = ((uint64_t)hi << 32) | lo;         // the lane's before (wave_shr:1)
+                best = best > x ? best : before > x ? x : before;
+            }
+        } else {
+            const uint64_t x = sorted_keys(lane < n ? keys[w][lane] : 0);
+            best = merged_keys(best, __shfl((unsigned long long)x, 63 - lane));
+        }
+        const uint32_t o = __builtin_amdgcn_readlane((uint32_t)(best >> 32), a.k - 1);
+        if (o != 0) kth = fmaxf(kth, value_of(o));
+    };
+    for (int w0 = 0; w0 < words; w0 += MLIST) {
+        // the marked strips of MLIST words in a list, ascending
+        uint32_t bits = lane < MLIST && w0 + lane < words ? flag[tk][w0 + lane] : 0;
+        const int own = __popc(bits);
+        int at = own;                                      // running total over the lanes
+#pragma unroll
+        for (int d = 1; d < MLIST; d <<= 1) {
+            const int x = __shfl_up(at, d);
+            at += lane >= d ? x : 0;
+        }
+        n = __builtin_amdgcn_readlane(at, MLIST - 1);
+        at -= own;
+        while (bits) {
+            list[w][at++] = (uint16_t)((w0 + lane) * 32 + __ffs(bits) - 1);
+            bits &= bits - 1;
+        }
+        each_strip([&](float z, int col, int) {
+            const uint64_t mask = __ballot(z > kth && z >= from);
+            if (mask == 0) return;
+            if (z > kth && z >= from) keys[w][gathered + lanes_before(mask)] = key_of(z, a.c0 + col + lane);
+            gathered += __popcll(mask);
+            if (gathered < 64) return;
+            put(64);
+            gathered -= 64;
+            keys[w][lane] = keys[w][64 + lane];            // a wave's own LDS accesses are in order
+        });
+    }
+    if (gathered > 0) put(gathered);
+    if (WPT > 1) {
+        keys[w][lane] = best;
+        __syncthreads();
+        if (sub > 0) return;
+#pragma unroll
+        for (int i = 1; i < WPT; ++i) best = merged_keys(best, keys[w + i][63 - lane]);
+        const uint32_t o = __builtin_amdgcn_readlane((uint32_t)(best >> 32), a.k - 1);
+        kth = o != 0 ? value_of(o) : -INFINITY;
+    }
+    if (!live) return;
+    if (lane < a.k) {
+        const int id = best != 0 ? key_id(best) : -1;
+        const float z = best != 0 ? key_z(best) : -INFINITY;
+        if (a.last) {
+            a.top_ids[t * a.k + lane] = id;
+            a.top_logp[t * a.k + lane] = best != 0 ? logp(z) : -INFINITY;
+        } else {
+            a.best_z[t * a.k + lane] = z;
+            a.best_i[t * a.k + lane] = id;
+        }
+    }
+    if (lane == 0) a.thr[t] = kth;
 }
 
 // Backward: a token's constants of the epilogue above.
@@ -620,52 +1142,93 @@ unsigned product_grid(const HeadLogpArgs& a) {
 
 }  // namespace
 
-HeadLogpPlan head_logp_plan(int64_t T, int64_t H, int64_t V) {
+// The pieces of the forward.  Without alternatives a piece is as long as its sums
+// may be (640 MB).  With them a piece's logits have their place (4 bytes each, so
+// at most 640 MB again), and the first piece, of which all strips are kept, is one
+// round of tiles over the card, at least 4096 columns; every other is twice what
+// came before it, in whole rounds: a piece keeps about k (its length / the columns
+// before) strips of 64 of a token.
+HeadLogpPlan head_logp_plan(int64_t T, int64_t H, int64_t V, int k) {
     HeadLogpPlan p{};
-    constexpr int64_t CH = 16384;
-    int64_t most = ((int64_t)640 << 20) / (4 * (T > 0 ? T : 1));
-    if (most > ((int64_t)1 << 30) / H) most = ((int64_t)1 << 30) / H;
-    most = most / BN * BN;
-    if (most < BN) most = BN;
-    p.vc = most < V ? most : (V + BN - 1) / BN * BN;
-    p.pieces = (V + p.vc - 1) / p.vc;
-    p.pc = (p.vc + CH - 1) / CH;
-    p.nc = p.pc * p.pieces;
+    const int64_t n = T > 0 ? T : 1, mt = (n + BM - 1) / BM;
+    const int64_t bytes = k > 0 ? n * 4 : n * 12 / 64 + 1;
+    int64_t most = ((int64_t)640 << 20) / bytes;
+    most = std::min(most, ((int64_t)1 << 30) / H);                 // the reach of a buffer resource's offsets
+    most = std::min(most, (int64_t)LOGP_MAX_PIECE);
+    p.most = (int)std::max(most / BN * BN, (int64_t)BN);
+    p.round = (int)std::max((CUS / mt) * BN, (int64_t)BN);
+    p.first = k > 0 ? std::min(p.most, std::max(p.round, 4096)) : p.most;
+    p.ld = (int)std::min((int64_t)p.most, (V + BN - 1) / BN * BN);
     return p;
 }
 
-hipError_t launch_head_logprob_fwd(HeadLogpArgs a, const HeadLogpPlan& pl, hipStream_t st) {
-    a.bm = tile_rows(a.T);
-    a.vc = (int)pl.vc;
-    if (a.m > 0) hipLaunchKernelGGL(k_logp_given, grid_of((a.T * a.m + 3) / 4), dim3(256), 0, st, a);
+// Tokens few enough for their hidden states to stand in LDS while the weight goes
+// by.
+bool head_logp_few(int64_t T, int64_t H) { return T <= 64 && T * (2 * H + 16) <= FEW_BYTES; }
+
+static hipError_t launch_few(HeadLogpArgs a, hipStream_t st) {
+    const int64_t bytes = a.T * (2 * a.H + 16), tiles = (a.V + 15) / 16;
+    a.vc = (int)head_few_ld(a.V);
+    auto grid = [&](int per_cu, int waves) {
+        return dim3((unsigned)std::min<int64_t>((int64_t)CUS * per_cu, (tiles + waves - 1) / waves));
+    };
+    if (a.T <= 16 && bytes <= 20480) hipLaunchKernelGGL((k_head_few<1, 20480, 512>), grid(2, 8), dim3(512), 0, st, a);
+    else if (a.T <= 16 && bytes <= 67584) hipLaunchKernelGGL((k_head_few<1, 67584, 512>), grid(2, 8), dim3(512), 0, st, a);
+    else if (a.T <= 16) hipLaunchKernelGGL((k_head_few<1, FEW_BYTES, 1024>), grid(1, 16), dim3(1024), 0, st, a);
+    else if (a.T <= 32) hipLaunchKernelGGL((k_head_few<2, FEW_BYTES, 1024>), grid(1, 16), dim3(1024), 0, st, a);
+    else hipLaunchKernelGGL((k_head_few<4, FEW_BYTES, 1024>), grid(1, 16), dim3(1024), 0, st, a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
     RowsArgs r{};
     r.T = a.T;
     r.V = a.V;
     r.m = a.m;
     r.k = a.k;
     r.z = a.z;
-    r.ld = pl.vc;
-    r.nc = pl.nc;
-    r.pc = pl.pc;
-    r.part = a.part;
+    r.ld = a.vc;
+    r.nc = (a.V + FEW_CHUNK - 1) / FEW_CHUNK;
+    r.part = a.run;
     r.keys = a.keys;
-    r.zs = a.zs;
     r.ids = a.ids;
     r.logp = a.logp;
     r.lse = a.lse;
     r.entropy = a.entropy;
     r.top_ids = a.top_ids;
     r.top_logp = a.top_logp;
-    for (int64_t i = 0; i < pl.pieces; ++i) {
-        a.c0 = r.c0 = i * pl.vc;
-        r.n = a.V - r.c0 < pl.vc ? a.V - r.c0 : pl.vc;
-        r.chunk0 = i * pl.pc;
-        hipLaunchKernelGGL(k_head_z<false>, dim3(product_grid(a)), dim3(512), 0, st, a);
-        hipLaunchKernelGGL((k_rows_chunk<float, 16>), grid_of(a.T * pl.pc), dim3(TPB), 0, st, r);
-        const hipError_t err = hipGetLastError();
+    return launch_rows<float, FEW_CHUNK / (4 * TPB)>(r, st);
+}
+
+hipError_t launch_head_logprob_fwd(HeadLogpArgs a, const HeadLogpPlan& pl, hipStream_t st) {
+    if (head_logp_few(a.T, a.H)) return launch_few(a, st);
+    a.bm = tile_rows(a.T);
+    if (a.m > 0) hipLaunchKernelGGL(k_logp_given, grid_of((a.T * a.m + 3) / 4), dim3(256), 0, st, a);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    int64_t c0 = 0;
+    while (c0 < a.V) {
+        const int64_t left = (a.V - c0 + BN - 1) / BN * BN;
+        int64_t n = c0 == 0 ? pl.first : pl.most;
+        if (c0 > 0 && a.k > 0 && 2 * c0 < n) n = std::max(2 * c0 / pl.round * pl.round, (int64_t)pl.round);
+        n = std::min(n, left);
+        a.c0 = c0;
+        a.vc = (int)n;
+        a.first = c0 == 0;
+        a.last = c0 + n >= a.V;
+        const dim3 grid(product_grid(a));
+        if (a.k > 0) {
+            if (a.entropy) hipLaunchKernelGGL((k_head_z<TOP, true>), grid, dim3(512), 0, st, a);
+            else hipLaunchKernelGGL((k_head_z<TOP, false>), grid, dim3(512), 0, st, a);
+        } else {
+            if (a.entropy) hipLaunchKernelGGL((k_head_z<SUMS, true>), grid, dim3(512), 0, st, a);
+            else hipLaunchKernelGGL((k_head_z<SUMS, false>), grid, dim3(512), 0, st, a);
+        }
+        if (a.T >= 8192) hipLaunchKernelGGL(k_logp_merge<1>, dim3((unsigned)((a.T + 127) / 128 * 8)), dim3(1024), 0, st, a);
+        else hipLaunchKernelGGL(k_logp_merge<4>, dim3((unsigned)((a.T + 31) / 32 * 8)), dim3(1024), 0, st, a);
+        err = hipGetLastError();
         if (err != hipSuccess) return err;
+        c0 += n;
     }
-    return launch_join(r, st);
+    return hipSuccess;
 }
 
 hipError_t launch_head_logprob_bwd(HeadLogpArgs a, const HeadPlan& pl, hipStream_t st) {
@@ -688,7 +1251,7 @@ hipError_t launch_head_logprob_bwd(HeadLogpArgs a, const HeadPlan& pl, hipStream
     for (int i = 0; i < pl.pieces; ++i) {
         a.c0 = g.c0 = (int64_t)i * pl.vc;
         g.first = i == 0;
-        hipLaunchKernelGGL(k_head_z<true>, dim3(product_grid(a)), dim3(512), 0, st, a);
+        hipLaunchKernelGGL((k_head_z<GRAD, false>), dim3(product_grid(a)), dim3(512), 0, st, a);
         if (a.m > 0) hipLaunchKernelGGL(k_logp_clear, grid_of((a.T * a.m + 255) / 256), dim3(256), 0, st, a);
         hipError_t err = hipGetLastError();
         if (err != hipSuccess || (err = launch_head_grad(g, st)) != hipSuccess) return err;

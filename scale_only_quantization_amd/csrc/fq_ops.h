@@ -91,17 +91,16 @@ hipError_t launch_head_grad(const HeadArgs& a, hipStream_t st);
 // ------------------------------------------------ log probabilities of rows ---
 constexpr int LOGP_MAX_TOP = 64;
 constexpr int ROWS_TPB = 256;
+// keys that a chunk of a row keeps for its k best
+__host__ __device__ constexpr int rows_keys(int k) { return k > 32 ? 2 * k : 64; }
 struct RowsArgs {          // rows of logits in chunks of columns, then joined
     int64_t T, V;
     int m, k;              // given tokens and alternatives per row
-    const void* z;         // bf16 or fp32 logits [T, ld] of the columns c0 .. c0 + n - 1
+    const void* z;         // bf16 or fp32 logits [T, ld]
     int64_t ld;
-    int64_t c0, n;
-    int64_t nc;            // chunks of a whole row
-    int64_t chunk0, pc;    // first chunk and chunks of these columns
+    int64_t nc;            // chunks of a row
     float4* part;          // workspace [T, nc]: maximum, sum of e^(z - max), sum of e^(z - max) (z - max)
-    uint64_t* keys;        // workspace [T, nc, k], with k
-    const float* zs;       // nullable [T, m]: the given tokens' logits; else they are read from z
+    uint64_t* keys;        // workspace [T, nc, rows_keys(k)], with k
     const int32_t* ids;    // [T, m]
     float* logp;
     float* lse;            // nullable
@@ -143,22 +142,32 @@ struct HeadLogpArgs {
     uint16_t* grad;        // [T, H]
     // workspace
     float* zs;             // [T, m] the given tokens' logits
-    float* z;              // forward: [T, vc] logits of a piece
-    float4* part;          // forward
-    uint64_t* keys;        // forward
+    float* thr;            // forward [T]: the k-th best logit so far
+    float4* run;           // forward [T]: maximum in base 2, s and u so far; few tokens: of the chunks
+    uint64_t* keys;        // few tokens: of the chunks
+    float* best_z;         // forward [T, k]: the best so far
+    int32_t* best_i;
+    float2* stats;         // forward [vc / 64, T]: maximum and s of each strip
+    float* ustats;         // forward [vc / 64, T], with the entropy: u
+    float* z;              // forward [T, vc], with k: logits of a piece's strips above thr
     float4* rowc;          // backward [T]: lse log2 e, A + b (entropy), b
     uint16_t* p;           // backward [T, vc]
     float* g;              // backward [splits, T, H]
     float* ones;           // backward [T]
     // filled per launch
     int64_t c0;
-    int vc, bm;
+    int vc, bm, first, last;
 };
+constexpr int LOGP_MAX_PIECE = 131072;
+constexpr int FEW_BYTES = 132 * 1024, FEW_CHUNK = 4096;     // a few tokens: hidden states in LDS, columns of a chunk
+bool head_logp_few(int64_t T, int64_t H);
+inline int64_t head_few_ld(int64_t V) { return (V + 15) / 16 * 16; }
 struct HeadLogpPlan {
-    int64_t vc, pieces;    // entries of a piece (a multiple of 256), pieces
-    int64_t pc, nc;        // chunks of a piece and of all
+    int first, most;       // entries of the first piece and of the longest (multiples of 256)
+    int round;             // of a round of tiles over the card
+    int ld;                // of the longest piece that occurs
 };
-HeadLogpPlan head_logp_plan(int64_t T, int64_t H, int64_t V);
+HeadLogpPlan head_logp_plan(int64_t T, int64_t H, int64_t V, int k);
 hipError_t launch_head_logprob_fwd(HeadLogpArgs a, const HeadLogpPlan& pl, hipStream_t st);
 hipError_t launch_head_logprob_bwd(HeadLogpArgs a, const HeadPlan& pl, hipStream_t st);
 

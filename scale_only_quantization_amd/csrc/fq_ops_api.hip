@@ -232,13 +232,13 @@ RowsLayout rows_layout(const fq_logprob_desc* d) {
                                                   rows_chunk(d->tokens, d->vocab));
     RowsLayout y{};
     y.part = place(n * sizeof(float4));
-    y.keys = place(n * (size_t)d->top * 8);
+    y.keys = place(d->top > 0 ? n * (size_t)rows_keys(d->top) * 8 : 0);
     y.total = place.total;
     return y;
 }
 
 struct HeadLogpLayout {
-    size_t zs, z, part, keys, rowc, ones, p, g, total;
+    size_t zs, thr, run, keys, best_z, best_i, stats, ustats, z, rowc, ones, p, g, total;
 };
 HeadLogpLayout head_logp_layout(const fq_logprob_desc* d, bool grad) {
     Placer place;
@@ -251,11 +251,20 @@ HeadLogpLayout head_logp_layout(const fq_logprob_desc* d, bool grad) {
         y.ones = place(T * 4);
         y.p = place(T * (size_t)pl.vc * 2);
         y.g = place((size_t)pl.splits * T * (size_t)d->hidden * 4);
+    } else if (head_logp_few(d->tokens, d->hidden)) {
+        const size_t nc = (size_t)((d->vocab + FEW_CHUNK - 1) / FEW_CHUNK);
+        y.run = place(T * nc * sizeof(float4));
+        y.keys = place(d->top > 0 ? T * nc * (size_t)rows_keys(d->top) * 8 : 0);
+        y.z = place(T * (size_t)head_few_ld(d->vocab) * 4);
     } else {
-        const HeadLogpPlan pl = head_logp_plan(d->tokens, d->hidden, d->vocab);
-        y.z = place(T * (size_t)pl.vc * 4);
-        y.part = place(T * (size_t)pl.nc * sizeof(float4));
-        y.keys = place(T * (size_t)pl.nc * (size_t)d->top * 8);
+        const HeadLogpPlan pl = head_logp_plan(d->tokens, d->hidden, d->vocab, d->top);
+        y.thr = place(T * 4);
+        y.run = place(T * 16);
+        y.best_z = place(T * (size_t)d->top * 4);
+        y.best_i = place(T * (size_t)d->top * 4);
+        y.stats = place(T * (size_t)(pl.ld / 64) * 8);
+        y.ustats = place(T * (size_t)(pl.ld / 64) * 4);
+        y.z = place(d->top > 0 ? T * (size_t)pl.ld * 4 : 0);
     }
     y.total = place.total;
     return y;
@@ -284,12 +293,12 @@ int fq_logprob_fwd(const fq_logprob_desc* d, const void* logits, int64_t row_str
     char* ws = static_cast<char*>(workspace);
     RowsArgs a{};
     a.T = d->tokens;
-    a.V = a.n = d->vocab;
+    a.V = d->vocab;
     a.m = d->given;
     a.k = d->top;
     a.z = logits;
     a.ld = row_stride;
-    a.nc = a.pc = (d->vocab + rows_chunk(a.T, a.V) - 1) / rows_chunk(a.T, a.V);
+    a.nc = (d->vocab + rows_chunk(a.T, a.V) - 1) / rows_chunk(a.T, a.V);
     a.part = reinterpret_cast<float4*>(ws + y.part);
     a.keys = reinterpret_cast<uint64_t*>(ws + y.keys);
     a.ids = ids;
@@ -360,10 +369,15 @@ int fq_head_logprob_fwd(const fq_logprob_desc* d, const void* h, const void* w, 
     a.top_ids = top_ids;
     a.top_logp = top_logp;
     a.zs = reinterpret_cast<float*>(ws + y.zs);
-    a.z = reinterpret_cast<float*>(ws + y.z);
-    a.part = reinterpret_cast<float4*>(ws + y.part);
+    a.thr = reinterpret_cast<float*>(ws + y.thr);
+    a.run = reinterpret_cast<float4*>(ws + y.run);
     a.keys = reinterpret_cast<uint64_t*>(ws + y.keys);
-    FQ_TRY(launch_head_logprob_fwd(a, head_logp_plan(a.T, a.H, a.V), static_cast<hipStream_t>(stream)));
+    a.best_z = reinterpret_cast<float*>(ws + y.best_z);
+    a.best_i = reinterpret_cast<int32_t*>(ws + y.best_i);
+    a.stats = reinterpret_cast<float2*>(ws + y.stats);
+    a.ustats = reinterpret_cast<float*>(ws + y.ustats);
+    a.z = reinterpret_cast<float*>(ws + y.z);
+    FQ_TRY(launch_head_logprob_fwd(a, head_logp_plan(a.T, a.H, a.V, a.k), static_cast<hipStream_t>(stream)));
     return FQ_OK;
 }
 
