@@ -6,10 +6,10 @@
 //   norm = sqrt(sum g^2),  c = min(1, max / (norm + 1e-6)),  out = c g
 //
 // Each tensor is cut into chunks of GRAD_CHUNK elements, a block each; a launch
-// carries the descriptors of up to GRAD_LIST tensors in its arguments, so nothing
-// is copied to the device first and a call can be captured.  k_grad_sq leaves a
-// double per chunk, k_grad_norm adds them in a fixed order: no atomics, bitwise
-// deterministic.  Both passes are bound by HBM.
+// carries the descriptors of its tensors in its arguments, so nothing is copied to
+// the device first and a call can be captured.  k_grad_sq leaves a double per
+// chunk, k_grad_norm adds them in a fixed order: no atomics, bitwise deterministic.
+// Both passes are bound by HBM.
 #include "fq_common.h"
 #include "fq_ops.h"
 
@@ -21,16 +21,23 @@ constexpr int TPB = 256;
 // 16 bytes at any element's address (the hardware splits what is not aligned)
 typedef uint32_t words_any __attribute__((ext_vector_type(4), aligned(2)));
 
-// The tensor of block b: the last entry whose first block is not past it.
-__device__ __forceinline__ int find(const GradArgs& a, int64_t b) {
-    int lo = 0, hi = a.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.t[mid].blk0 <= b) lo = mid;
-        else hi = mid - 1;
+// The tensor of block b: the last whose first block is not past it.  One load of
+// 64 entries at a time and a count (halving takes a dependent load per step).
+template <typename ARGS>
+__device__ __forceinline__ int find(const ARGS& a, uint32_t b) {
+    const int lane = threadIdx.x & 63;
+    int i = 0;
+#pragma unroll
+    for (int j = 0; j < ARGS::LIST; j += 64) {
+        const int at = min(j + lane, ARGS::LIST - 1);
+        i += __popcll(__ballot(j + lane < a.n && a.blk0[at] <= b));
     }
-    return lo;
+    return i - 1;
 }
+__device__ __forceinline__ int64_t length(int64_t count) { return count & ~GRAD_BF16; }
+
+// what is read once, past the caches
+__device__ __forceinline__ words_any load_once(const words_any* p) { return __builtin_nontemporal_load(p); }
 
 template <int THREADS>
 __device__ __forceinline__ double block_sum(double v) {
@@ -67,16 +74,16 @@ __device__ __forceinline__ double sq_range(const void* p, int64_t lo, int64_t hi
     const char* g = static_cast<const char*>(p) + lo * SZ;
     const int n = (int)(hi - lo), nv = n / VEC;
     double acc = 0.0;
-    int i = threadIdx.x;
+    int i = threadIdx.x % THREADS;
     for (; i + 3 * THREADS < nv; i += 4 * THREADS) {
         words_any w[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) w[u] = reinterpret_cast<const words_any*>(g)[i + u * THREADS];
+        for (int u = 0; u < 4; ++u) w[u] = load_once(reinterpret_cast<const words_any*>(g) + i + u * THREADS);
 #pragma unroll
         for (int u = 0; u < 4; ++u) acc += sq_words(w[u], BF);
     }
     for (; i < nv; i += THREADS) acc += sq_words(reinterpret_cast<const words_any*>(g)[i], BF);
-    const int e = nv * VEC + threadIdx.x;
+    const int e = nv * VEC + threadIdx.x % THREADS;
     if (e < n) {
         const double x = BF ? bf_lo(reinterpret_cast<const uint16_t*>(g)[e]) : reinterpret_cast<const float*>(g)[e];
         acc += x * x;
@@ -84,13 +91,24 @@ __device__ __forceinline__ double sq_range(const void* p, int64_t lo, int64_t hi
     return acc;
 }
 
-__global__ __launch_bounds__(TPB) void k_grad_sq(GradArgs a) {
-    const int64_t b = block_id();
+__global__ __launch_bounds__(TPB) void k_grad_sq(GradSqArgs a) {
+    const uint32_t b = (uint32_t)block_id();
     if (b >= a.blocks) return;
-    const GradEntry& q = a.t[find(a, b)];
-    const int64_t lo = (b - q.blk0) * GRAD_CHUNK, hi = min(lo + GRAD_CHUNK, q.count);
-    const double s = block_sum<TPB>(q.bf ? sq_range<true, TPB>(q.g, lo, hi) : sq_range<false, TPB>(q.g, lo, hi));
+    const int i = find(a, b);
+    const int64_t lo = (int64_t)(b - a.blk0[i]) * GRAD_CHUNK, hi = min(lo + GRAD_CHUNK, length(a.count[i]));
+    const double s = block_sum<TPB>(a.count[i] < 0 ? sq_range<true, TPB>(a.g[i], lo, hi)
+                                                   : sq_range<false, TPB>(a.g[i], lo, hi));
     if (threadIdx.x == 0) a.part[b] = s;
+}
+
+// All tensors in one block, a wave per tensor in turn.
+__global__ __launch_bounds__(1024) void k_grad_norm_small(GradSqArgs a, float* norm) {
+    double acc = 0.0;
+    for (int i = threadIdx.x / WAVE; i < a.n; i += 1024 / WAVE)
+        acc += a.count[i] < 0 ? sq_range<true, WAVE>(a.g[i], 0, length(a.count[i]))
+                              : sq_range<false, WAVE>(a.g[i], 0, length(a.count[i]));
+    acc = block_sum<1024>(acc);
+    if (threadIdx.x == 0) norm[0] = (float)sqrt(acc);
 }
 
 __global__ __launch_bounds__(1024) void k_grad_norm(const double* part, int64_t n, float* norm) {
@@ -102,10 +120,10 @@ __global__ __launch_bounds__(1024) void k_grad_norm(const double* part, int64_t 
 }
 
 template <bool BF>
-__device__ __forceinline__ void scale_range(const GradEntry& q, float c, int64_t lo, int64_t hi) {
+__device__ __forceinline__ void scale_range(const void* from, void* to, float c, int64_t lo, int64_t hi) {
     constexpr int VEC = BF ? 8 : 4, SZ = BF ? 2 : 4;
-    const char* g = static_cast<const char*>(q.g) + lo * SZ;
-    char* o = static_cast<char*>(q.out) + lo * SZ;
+    const char* g = static_cast<const char*>(from) + lo * SZ;
+    char* o = static_cast<char*>(to) + lo * SZ;
     const int n = (int)(hi - lo), nv = n / VEC;
     auto scaled = [&](words_any w) {
 #pragma unroll
@@ -117,9 +135,9 @@ __device__ __forceinline__ void scale_range(const GradEntry& q, float c, int64_t
     for (; i + 3 * TPB < nv; i += 4 * TPB) {
         words_any w[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) w[u] = reinterpret_cast<const words_any*>(g)[i + u * TPB];
+        for (int u = 0; u < 4; ++u) w[u] = load_once(reinterpret_cast<const words_any*>(g) + i + u * TPB);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) reinterpret_cast<words_any*>(o)[i + u * TPB] = scaled(w[u]);
+        for (int u = 0; u < 4; ++u) __builtin_nontemporal_store(scaled(w[u]), reinterpret_cast<words_any*>(o) + i + u * TPB);
     }
     for (; i < nv; i += TPB) reinterpret_cast<words_any*>(o)[i] = scaled(reinterpret_cast<const words_any*>(g)[i]);
     const int e = nv * VEC + threadIdx.x;
@@ -133,22 +151,31 @@ __device__ __forceinline__ void scale_range(const GradEntry& q, float c, int64_t
     }
 }
 
-__global__ __launch_bounds__(TPB) void k_grad_clip(GradArgs a) {
-    const int64_t b = block_id();
+// From a tensor's last chunk to its first, as the tensors come: what the norm's
+// pass read last may still be in the memory-side cache.  Loads and stores past the
+// caches: 302 M elements in 437 us, 462 through them.
+__global__ __launch_bounds__(TPB) void k_grad_clip(GradClipArgs a) {
+    const uint32_t b = (uint32_t)block_id();
     if (b >= a.blocks) return;
     const double r = a.max_norm / ((double)a.norm[0] + 1.0e-6);
     const float c = r >= 1.0 ? 1.0f : (float)r;                // a NaN stays one
-    const GradEntry& q = a.t[find(a, b)];
-    if (c == 1.0f && q.g == q.out) return;
-    const int64_t lo = (b - q.blk0) * GRAD_CHUNK, hi = min(lo + GRAD_CHUNK, q.count);
-    if (q.bf) scale_range<true>(q, c, lo, hi);
-    else scale_range<false>(q, c, lo, hi);
+    const int i = find(a, b);
+    if (c == 1.0f && a.g[i] == a.out[i]) return;
+    const int64_t n = length(a.count[i]);
+    const int64_t lo = ((n - 1) / GRAD_CHUNK - (b - a.blk0[i])) * GRAD_CHUNK, hi = min(lo + GRAD_CHUNK, n);
+    if (a.count[i] < 0) scale_range<true>(a.g[i], a.out[i], c, lo, hi);
+    else scale_range<false>(a.g[i], a.out[i], c, lo, hi);
 }
 
 }  // namespace
 
-hipError_t launch_grad_sq(const GradArgs& a, hipStream_t st) {
+hipError_t launch_grad_sq(const GradSqArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(k_grad_sq, grid_of(a.blocks), dim3(TPB), 0, st, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_norm_small(const GradSqArgs& a, float* norm, hipStream_t st) {
+    hipLaunchKernelGGL(k_grad_norm_small, dim3(1), dim3(1024), 0, st, a, norm);
     return hipGetLastError();
 }
 
@@ -157,7 +184,7 @@ hipError_t launch_grad_norm(const double* part, int64_t n, float* norm, hipStrea
     return hipGetLastError();
 }
 
-hipError_t launch_grad_clip(const GradArgs& a, hipStream_t st) {
+hipError_t launch_grad_clip(const GradClipArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(k_grad_clip, grid_of(a.blocks), dim3(TPB), 0, st, a);
     return hipGetLastError();
 }

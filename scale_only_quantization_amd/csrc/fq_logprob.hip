@@ -134,6 +134,8 @@ __device__ __forceinline__ uint64_t merged_keys(uint64_t x, uint64_t reversed) {
     return x;
 }
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 // The best keys of a block, in LDS: appended in any order, cut down to the k
 // best by counting for each key how many are larger.
 struct Best {
@@ -236,6 +238,18 @@ struct Vec<float> {
     }
 };
 
+// A barrier that orders LDS accesses and leaves loads in flight.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// A load of what is read once: 622 MB in whole stretches of memory arrive at 7.0
+// TB/s so, at 6.2 through the caches.
+__device__ __forceinline__ uint4 past_caches(const uint4* p) {
+    const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+
 // The compiler is not to keep what it formed of these before (a second set of
 // registers for a chunk's unpacked elements halves the waves of a SIMD).
 template <int N>
@@ -265,7 +279,7 @@ __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
     uint4 v[NL];
 #pragma unroll
     for (int i = 0; i < NL; ++i)
-        v[i] = *reinterpret_cast<const uint4*>(src + min((i * TPB + (int)threadIdx.x) * VEC, end));
+        v[i] = past_caches(reinterpret_cast<const uint4*>(src + min((i * TPB + (int)threadIdx.x) * VEC, end)));
     if (left < CH) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
@@ -601,20 +615,124 @@ __global__ __launch_bounds__(256) void k_logp_given(HeadLogpArgs a) {
     if (lane == 0) a.zs[i] = acc;
 }
 
-// Logits of a few tokens, in fp32: the weight is read once, 16 rows by 32 columns
+// Logits of up to 8 tokens, in fp32: the weight is read once, a kilobyte of a row
+// per load, past the caches (a load of the matrix operand's shape, 16 rows of 64
+// bytes, arrives at 5.4 TB/s, these at 6.8), and multiplied with pairs of columns
+// in the vector unit: 4 operations a token for 16 bytes of a lane.  A block has a run
+// of the rows, its waves 4 of them at a time; the loads of the next GO chunks of
+// 512 columns are in flight while a wave multiplies, over the ends of rows too.
+// (One token of 2048 by 151936: 91 us; 108 through the caches.)
+constexpr int ROW_TPB = 512, ROW_N = 4;
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+template <int TT, int ROW_GO, int BYTES>
+__global__ __launch_bounds__(ROW_TPB) void k_head_rows(HeadLogpArgs a) {
+    __shared__ __attribute__((aligned(16))) uint16_t sh[BYTES / 2];
+    const int lane = threadIdx.x & 63, H = a.H, chunks = (H + 511) / 512, Hp = chunks * 512;
+    for (int i = threadIdx.x; i < TT * Hp / 8; i += ROW_TPB) {      // rows padded with zeros, tokens repeated
+        const int t = i / (Hp / 8), c = i - t * (Hp / 8);
+        const uint4 v = reinterpret_cast<const uint4*>(a.h + min((int64_t)t, a.T - 1) * H)[min(c, H / 8 - 1)];
+        reinterpret_cast<uint4*>(sh)[i] = c < H / 8 ? v : make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    const int64_t groups = (a.V + ROW_N - 1) / ROW_N, end = groups * (blockIdx.x + 1) / gridDim.x;
+    int64_t g = groups * blockIdx.x / gridDim.x + wave_id();
+    if (g >= end) return;
+    int64_t lg = g;                                        // the loads' place, a step ahead
+    int lc = 0;
+    auto load = [&](u32x4 (&v)[ROW_GO][ROW_N]) {
+        if (lg >= end) return;
+#pragma unroll
+        for (int j = 0; j < ROW_GO; ++j) {
+            const int col = (lc + j) * 512 + lane * 8, at = col < H ? col : 0;
+#pragma unroll
+            for (int r = 0; r < ROW_N; ++r)
+                v[j][r] = __builtin_nontemporal_load(
+                    reinterpret_cast<const u32x4*>(a.w + min(lg * ROW_N + r, a.V - 1) * H + at));
+        }
+        lc += ROW_GO;
+        if (lc >= chunks) {
+            lc = 0;
+            lg += ROW_TPB / 64;
+        }
+    };
+    float acc[ROW_N][TT];
+#pragma unroll
+    for (int r = 0; r < ROW_N; ++r)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[r][t] = 0.0f;
+    int c = 0;
+    auto multiply = [&](const u32x4 (&v)[ROW_GO][ROW_N]) {
+#pragma unroll
+        for (int j = 0; j < ROW_GO; ++j) {
+            if (c + j >= chunks) break;
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const u32x4 x = *reinterpret_cast<const u32x4*>(sh + t * Hp + (c + j) * 512 + lane * 8);
+#pragma unroll
+                for (int r = 0; r < ROW_N; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t p = v[j][r][e], q = x[e];
+                        acc[r][t] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2v, p),
+                                                                    __builtin_bit_cast(bf16x2v, q), acc[r][t], false);
+                    }
+            }
+        }
+        c += ROW_GO;
+        if (c < chunks) return;
+        c = 0;
+        // Over the lanes: rows 2 and 3 trade halves with rows 0 and 1, row 1 (3)
+        // quarters with row 0 (2), so that lanes 16 r .. 16 r + 15 have row r's
+        // sums, then moves inside 16 lanes; lane 16 r + 15 has the total.
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            float x[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[r][t]), __float_as_uint(acc[r + 2][t]),
+                                                                false, false);
+                x[r] = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+            }
+            const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(x[0]), __float_as_uint(x[1]), false, false);
+            float z = __uint_as_float(q[0]) + __uint_as_float(q[1]);
+            z += __uint_as_float(moved<0x111, 0xf>(__float_as_uint(z)));
+            z += __uint_as_float(moved<0x112, 0xf>(__float_as_uint(z)));
+            z += __uint_as_float(moved<0x114, 0xf>(__float_as_uint(z)));
+            z += __uint_as_float(moved<0x118, 0xf>(__float_as_uint(z)));
+            if ((lane & 15) == 15 && t < a.T) a.z[(int64_t)t * a.vc + g * ROW_N + (lane >> 4)] = z;
+#pragma unroll
+            for (int r = 0; r < ROW_N; ++r) acc[r][t] = 0.0f;
+        }
+        g += ROW_TPB / 64;
+    };
+    u32x4 v0[ROW_GO][ROW_N], v1[ROW_GO][ROW_N];
+    load(v0);
+    while (g < end) {
+        load(v1);
+        multiply(v0);
+        if (g >= end) break;
+        load(v0);
+        multiply(v1);
+    }
+}
+
+// Logits of more tokens: the weight is read once, 16 rows by 32 columns
 // a load (64 bytes of a row in neighbouring lanes, two loads a cache line), straight
 // into the matrix instruction's operand; the hidden states stand in LDS, rows 16
-// bytes apart from a multiple of the banks.  A wave takes every so many-th 16 rows
-// and has the loads of the next STEP columns in flight while it multiplies, over
-// the ends of rows too.
-constexpr int FEW_LOADS = 8, FEW_STEP = 32 * FEW_LOADS;
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-template <int NT, int BYTES, int THREADS>
-__global__ __launch_bounds__(THREADS) void k_head_few(HeadLogpArgs a) {
+// bytes apart from a multiple of the banks.  A block has a run of rows, 16 at a
+// time, its waves a share of the columns each, so that what the card reads at once
+// are a few whole stretches of memory, past the caches: for one token of 2048 by
+// 151936 118 us with whole rows to a wave, strided over the card (5.3 TB/s).  The
+// next rows' loads are in flight while a wave multiplies and the block adds its
+// waves' sums.
+constexpr int FEW_LOADS = 8, FEW_STEP = 32 * FEW_LOADS, FEW_TPB = 512, FEW_WAVES = FEW_TPB / 64;
+template <int NT, int BYTES>
+__global__ __launch_bounds__(FEW_TPB) void k_head_few(HeadLogpArgs a) {
     __shared__ __attribute__((aligned(16))) char sh[BYTES];
-    const int lane = threadIdx.x & 63, tok = lane & 15, kc = lane >> 4;
+    __shared__ __attribute__((aligned(16))) float red[FEW_WAVES][256];
+    const int lane = threadIdx.x & 63, tok = lane & 15, kc = lane >> 4, w = wave_id();
     const int T = (int)a.T, H = a.H, ldh = 2 * H + 16, chunks = H >> 3;
-    for (int i = threadIdx.x; i < T * chunks; i += THREADS) {
+    for (int i = threadIdx.x; i < T * chunks; i += FEW_TPB) {
         const int t = i / chunks, c = i - t * chunks;
         *reinterpret_cast<uint4*>(sh + t * ldh + c * 16) = reinterpret_cast<const uint4*>(a.h)[i];
     }
@@ -622,59 +740,67 @@ __global__ __launch_bounds__(THREADS) void k_head_few(HeadLogpArgs a) {
     const char* hb[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) hb[n] = sh + min(16 * n + tok, T - 1) * ldh + kc * 16;
-    const int64_t tiles = (a.V + 15) / 16, waves = (int64_t)gridDim.x * (THREADS / 64);
-    const int steps = (H + FEW_STEP - 1) / FEW_STEP;
-    int64_t tile = (int64_t)blockIdx.x * (THREADS / 64) + wave_id();
-    if (tile >= tiles) return;
+    const int64_t tiles = (a.V + 15) / 16, end = tiles * (blockIdx.x + 1) / gridDim.x;
+    int64_t tile = tiles * blockIdx.x / gridDim.x;
+    const int share = (H / FEW_WAVES + 31) / 32 * 32, k0 = w * share, k1 = min(k0 + share, H);
+    const int steps = (share + FEW_STEP - 1) / FEW_STEP;
     int64_t ltile = tile;                                  // the loads' place, a step ahead
-    int lstep = 0;
-    const uint16_t* lrow = a.w + min(ltile * 16 + tok, a.V - 1) * H + kc * 8;
+    int lk = k0;
     auto load = [&](bf16x8 (&v)[FEW_LOADS]) {
-        if (ltile >= tiles) return;
+        if (ltile >= end) return;
+        const uint16_t* row = a.w + min(ltile * 16 + tok, a.V - 1) * H + kc * 8;
 #pragma unroll
         for (int i = 0; i < FEW_LOADS; ++i) {
-            const int k = lstep * FEW_STEP + 32 * i;
-            v[i] = *reinterpret_cast<const bf16x8*>(lrow + (k < H ? k : 0));
+            const int k = lk + 32 * i;
+            const bf16x8* p = reinterpret_cast<const bf16x8*>(row + (k < k1 ? k : 0));
+            v[i] = NT == 1 ? __builtin_nontemporal_load(p) : *p;   // 2 to 4% each way
         }
-        if (++lstep == steps) {
-            lstep = 0;
-            ltile += waves;
-            lrow = a.w + min(ltile * 16 + tok, a.V - 1) * H + kc * 8;
+        lk += FEW_STEP;
+        if (lk >= k0 + steps * FEW_STEP) {
+            lk = k0;
+            ++ltile;
         }
     };
     f32x4 acc[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    int step = 0;
+    int k = k0;
     auto multiply = [&](const bf16x8 (&v)[FEW_LOADS]) {
 #pragma unroll
-        for (int i = 0; i < FEW_LOADS; ++i) {
-            const int k = step * FEW_STEP + 32 * i;
-            if (k < H)
+        for (int i = 0; i < FEW_LOADS; ++i)
+            if (k + 32 * i < k1)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        v[i], *reinterpret_cast<const bf16x8*>(hb[n] + 2 * k), acc[n], 0, 0, 0);
-        }
-        if (++step < steps) return;
-        step = 0;
+                        v[i], *reinterpret_cast<const bf16x8*>(hb[n] + 2 * (k + 32 * i)), acc[n], 0, 0, 0);
+        k += FEW_STEP;
+        if (k < k0 + steps * FEW_STEP) return;
+        k = k0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            if (16 * n + tok < T)
-                *reinterpret_cast<f32x4*>(a.z + (int64_t)(16 * n + tok) * a.vc + tile * 16 + 4 * kc) = acc[n];
+            *reinterpret_cast<f32x4*>(&red[w][4 * lane]) = acc[n];
             acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            lds_barrier();
+            // lane l's four sums are token l % 16, rows 4 (l / 16) and on
+            const int e = threadIdx.x, t = 16 * n + ((e >> 2) & 15);
+            if (e < 256 && t < T) {
+                float s = red[0][e];
+#pragma unroll
+                for (int i = 1; i < FEW_WAVES; ++i) s += red[i][e];
+                a.z[(int64_t)t * a.vc + tile * 16 + 4 * (e >> 6) + (e & 3)] = s;
+            }
+            lds_barrier();
         }
-        tile += waves;
+        ++tile;
     };
     bf16x8 v0[FEW_LOADS], v1[FEW_LOADS];
     load(v0);
-    while (true) {
+    while (tile < end) {
         load(v1);
         multiply(v0);
-        if (tile >= tiles) break;
+        if (tile >= end) break;
         load(v0);
         multiply(v1);
-        if (tile >= tiles) break;
     }
 }
 
@@ -1169,14 +1295,17 @@ bool head_logp_few(int64_t T, int64_t H) { return T <= 64 && T * (2 * H + 16) <=
 static hipError_t launch_few(HeadLogpArgs a, hipStream_t st) {
     const int64_t bytes = a.T * (2 * a.H + 16), tiles = (a.V + 15) / 16;
     a.vc = (int)head_few_ld(a.V);
-    auto grid = [&](int per_cu, int waves) {
-        return dim3((unsigned)std::min<int64_t>((int64_t)CUS * per_cu, (tiles + waves - 1) / waves));
-    };
-    if (a.T <= 16 && bytes <= 20480) hipLaunchKernelGGL((k_head_few<1, 20480, 512>), grid(2, 8), dim3(512), 0, st, a);
-    else if (a.T <= 16 && bytes <= 67584) hipLaunchKernelGGL((k_head_few<1, 67584, 512>), grid(2, 8), dim3(512), 0, st, a);
-    else if (a.T <= 16) hipLaunchKernelGGL((k_head_few<1, FEW_BYTES, 1024>), grid(1, 16), dim3(1024), 0, st, a);
-    else if (a.T <= 32) hipLaunchKernelGGL((k_head_few<2, FEW_BYTES, 1024>), grid(1, 16), dim3(1024), 0, st, a);
-    else hipLaunchKernelGGL((k_head_few<4, FEW_BYTES, 1024>), grid(1, 16), dim3(1024), 0, st, a);
+    auto grid = [&](int per_cu) { return dim3((unsigned)std::min<int64_t>((int64_t)CUS * per_cu, tiles)); };
+    const int64_t row = (a.H + 511) / 512 * 1024;          // bytes of a token's padded row
+    if (a.T == 1 && row <= 32768) hipLaunchKernelGGL((k_head_rows<1, 4, 32768>), grid(2), dim3(ROW_TPB), 0, st, a);
+    else if (a.T <= 2 && 2 * row <= 32768) hipLaunchKernelGGL((k_head_rows<2, 4, 32768>), grid(2), dim3(ROW_TPB), 0, st, a);
+    else if (a.T <= 4 && 4 * row <= 32768) hipLaunchKernelGGL((k_head_rows<4, 4, 32768>), grid(2), dim3(ROW_TPB), 0, st, a);
+    else if (a.T <= 8 && 8 * row <= 65536) hipLaunchKernelGGL((k_head_rows<8, 1, 65536>), grid(2), dim3(ROW_TPB), 0, st, a);
+    else if (a.T <= 16 && bytes <= 20480) hipLaunchKernelGGL((k_head_few<1, 20480>), grid(2), dim3(FEW_TPB), 0, st, a);
+    else if (a.T <= 16 && bytes <= 67584) hipLaunchKernelGGL((k_head_few<1, 67584>), grid(2), dim3(FEW_TPB), 0, st, a);
+    else if (a.T <= 16) hipLaunchKernelGGL((k_head_few<1, FEW_BYTES>), grid(1), dim3(FEW_TPB), 0, st, a);
+    else if (a.T <= 32) hipLaunchKernelGGL((k_head_few<2, FEW_BYTES>), grid(1), dim3(FEW_TPB), 0, st, a);
+    else hipLaunchKernelGGL((k_head_few<4, FEW_BYTES>), grid(1), dim3(FEW_TPB), 0, st, a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     RowsArgs r{};

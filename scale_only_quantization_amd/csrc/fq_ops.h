@@ -173,25 +173,36 @@ hipError_t launch_head_logprob_bwd(HeadLogpArgs a, const HeadPlan& pl, hipStream
 
 // ------------------------------------------------- the norm of many gradients ---
 constexpr int GRAD_CHUNK = 16384;                  // elements per block
-constexpr int GRAD_LIST = 96;                      // tensors per launch: their entries are kernel arguments (under 4 KB)
-struct GradEntry {
-    const void* g;
-    void* out;
-    int64_t count;
-    int64_t blk0;          // the tensor's first block of the launch
-    int32_t bf;            // bf16, else fp32
-};
-struct GradArgs {
-    GradEntry t[GRAD_LIST];
+// A launch carries its tensors in its arguments, under 4 KB of them.  `count` has
+// the type in its top bit (bf16: set); blk0 is a tensor's first block of the launch.
+constexpr int64_t GRAD_BF16 = INT64_MIN;
+struct GradSqArgs {
+    static constexpr int LIST = 192;
+    const void* g[LIST];
+    int64_t count[LIST];
+    uint32_t blk0[LIST];
     int n;
-    int64_t blocks;
-    double* part;          // norm: [blocks]
-    const float* norm;     // clip
+    uint32_t blocks;
+    double* part;          // [blocks]
+};
+struct GradClipArgs {
+    static constexpr int LIST = 136;
+    const void* g[LIST];
+    void* out[LIST];
+    int64_t count[LIST];
+    uint32_t blk0[LIST];
+    int n;
+    uint32_t blocks;
+    const float* norm;
     double max_norm;
 };
-hipError_t launch_grad_sq(const GradArgs& a, hipStream_t st);
+static_assert(sizeof(GradSqArgs) <= 4096 && sizeof(GradClipArgs) <= 4096, "kernel arguments");
+hipError_t launch_grad_sq(const GradSqArgs& a, hipStream_t st);
+hipError_t launch_grad_clip(const GradClipArgs& a, hipStream_t st);
+// tensors of few elements, and few of them, in one block: the norm itself
+constexpr int GRAD_SMALL = 1024, GRAD_SMALL_LIST = 64;
+hipError_t launch_grad_norm_small(const GradSqArgs& a, float* norm, hipStream_t st);
 hipError_t launch_grad_norm(const double* part, int64_t n, float* norm, hipStream_t st);
-hipError_t launch_grad_clip(const GradArgs& a, hipStream_t st);
 
 // ------------------------------------------------- packed 4-bit weights ---
 constexpr int PACKED_MAX_ROWS = 1024;

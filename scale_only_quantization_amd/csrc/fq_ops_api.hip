@@ -437,22 +437,44 @@ int check_grads(const fq_grad_tensor* t, int32_t n, bool out) {
 
 int64_t grad_chunks(int64_t count) { return (count + GRAD_CHUNK - 1) / GRAD_CHUNK; }
 
-// The tensors in launches of up to GRAD_LIST: f(args) of each, with its blocks' place among all.
-extern "C++" template <typename F>
-int each_list(const fq_grad_tensor* t, int32_t n, F&& f) {
-    GradArgs a{};
-    int64_t before = 0;
-    for (int32_t i = 0; i < n; ++i) {
-        if (t[i].count > 0) a.t[a.n++] = GradEntry{t[i].grad, t[i].out, t[i].count, a.blocks, t[i].dtype == FQ_BF16};
-        a.blocks += grad_chunks(t[i].count);
-        if (a.n == GRAD_LIST || (i == n - 1 && a.n > 0)) {
-            FQ_TRY(f(a, before));
-            before += a.blocks;
+extern "C++" {
+void put_out(GradSqArgs&, int, void*) {}
+void put_out(GradClipArgs& a, int i, void* out) { a.out[i] = out; }
+
+// The tensors in launches of up to LIST, the last first where a pass goes
+// backwards: f(args) of each.
+template <typename ARGS, typename F>
+int each_list(const fq_grad_tensor* t, int32_t n, bool backwards, F&& f) {
+    ARGS a{};
+    for (int32_t j = 0; j < n; ++j) {
+        const fq_grad_tensor& q = t[backwards ? n - 1 - j : j];
+        const int64_t chunks = grad_chunks(q.count);
+        if (chunks == 0) continue;
+        if (a.n == ARGS::LIST || a.blocks + chunks > UINT32_MAX) {
+            FQ_TRY(f(a));
             a.n = 0;
             a.blocks = 0;
         }
+        a.g[a.n] = q.grad;
+        put_out(a, a.n, q.out);
+        a.count[a.n] = q.count | (q.dtype == FQ_BF16 ? GRAD_BF16 : 0);
+        a.blk0[a.n] = a.blocks;
+        ++a.n;
+        a.blocks += (uint32_t)chunks;
     }
+    if (a.n > 0) FQ_TRY(f(a));
     return FQ_OK;
+}
+}  // extern "C++"
+
+// Short tensors, and few: one block reads them all, which saves a launch.
+bool grads_small(const fq_grad_tensor* t, int32_t n) {
+    int32_t with = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        if (t[i].count > GRAD_SMALL) return false;
+        with += t[i].count > 0;
+    }
+    return with > 0 && with <= GRAD_SMALL_LIST;
 }
 
 }  // namespace
@@ -474,12 +496,17 @@ int fq_grad_norm(const fq_grad_tensor* tensors, int32_t ntensors, float* norm, v
     if (workspace_bytes < need || (need && !workspace)) return FQ_E_WORKSPACE;
     double* part = static_cast<double*>(workspace);
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    s = each_list(tensors, ntensors, [&](GradArgs& a, int64_t before) {
-        a.part = part + before;
+    if (grads_small(tensors, ntensors))
+        return each_list<GradSqArgs>(tensors, ntensors, false,
+                                     [&](GradSqArgs& a) { return launch_grad_norm_small(a, norm, st); });
+    double* at = part;
+    s = each_list<GradSqArgs>(tensors, ntensors, false, [&](GradSqArgs& a) {
+        a.part = at;
+        at += a.blocks;
         return launch_grad_sq(a, st);
     });
     if (s != FQ_OK) return s;
-    FQ_TRY(launch_grad_norm(part, (int64_t)(need / sizeof(double)), norm, st));
+    FQ_TRY(launch_grad_norm(part, at - part, norm, st));
     return FQ_OK;
 }
 
@@ -489,7 +516,7 @@ int fq_grad_clip(const fq_grad_tensor* tensors, int32_t ntensors, float max_grad
     if (s != FQ_OK) return s;
     if (!norm || !std::isfinite(max_grad_norm) || max_grad_norm <= 0.0f) return FQ_E_INVALID;
     if (!aligned(norm, 4)) return FQ_E_ALIGN;
-    return each_list(tensors, ntensors, [&](GradArgs& a, int64_t) {
+    return each_list<GradClipArgs>(tensors, ntensors, true, [&](GradClipArgs& a) {
         a.norm = norm;
         a.max_norm = (double)max_grad_norm;
         return launch_grad_clip(a, static_cast<hipStream_t>(stream));

@@ -158,9 +158,9 @@ def _load():
                                           c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
         "fq_head_logprob_bwd": (c_int32, [POINTER(LogprobDesc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                           c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
-        "fq_grad_norm_workspace_size": (c_size_t, [POINTER(GradTensor), c_int32]),
-        "fq_grad_norm": (c_int32, [POINTER(GradTensor), c_int32, c_void_p, c_void_p, c_size_t, c_void_p]),
-        "fq_grad_clip": (c_int32, [POINTER(GradTensor), c_int32, ctypes.c_float, c_void_p, c_void_p]),
+        "fq_grad_norm_workspace_size": (c_size_t, [c_void_p, c_int32]),
+        "fq_grad_norm": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "fq_grad_clip": (c_int32, [c_void_p, c_int32, ctypes.c_float, c_void_p, c_void_p]),
         "fq_packed_matvec": (c_int32, [Q, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
                                        c_void_p, c_void_p, c_void_p, c_void_p]),
         "fq_packed_expert_workspace_size": (c_size_t, [L]),
@@ -599,6 +599,7 @@ class GradList:
             e.grad = _expect(n, "a gradient", g, g.dtype, g.shape, self.device)
             e.out = _expect(n, "an output", o, g.dtype, g.shape, self.device)
             e.count, e.dtype = g.numel(), FQ_F32 if g.dtype is _F32 else FQ_BF16
+        self.args = ctypes.addressof(self.tensors), len(self.grads)
 
 
 def grad_list(grads, outs=None) -> GradList:
@@ -606,7 +607,7 @@ def grad_list(grads, outs=None) -> GradList:
 
 
 def grad_norm_workspace_size(g: GradList) -> int:
-    return _lib.fq_grad_norm_workspace_size(g.tensors, len(g.tensors))
+    return _lib.fq_grad_norm_workspace_size(*g.args)
 
 
 def grad_norm(g: GradList, norm, workspace=None, stream=None):
@@ -614,16 +615,14 @@ def grad_norm(g: GradList, norm, workspace=None, stream=None):
     n = "grad_norm"
     dev = _device_of(n, norm) if g.device is None else g.device
     ws, nb = _scratch(n, workspace, dev)
-    _call(n, _lib.fq_grad_norm, dev, stream, g.tensors, len(g.tensors), _expect(n, "norm", norm, _F32, (1,), dev), ws,
-          nb)
+    _call(n, _lib.fq_grad_norm, dev, stream, *g.args, _expect(n, "norm", norm, _F32, (1,), dev), ws, nb)
 
 
 def grad_clip(g: GradList, max_grad_norm: float, norm, stream=None):
     """Scale the list's gradients by min(1, max_grad_norm / (norm + 1e-6)) into its outputs (fq_grad_clip)."""
     n = "grad_clip"
     dev = _device_of(n, norm) if g.device is None else g.device
-    _call(n, _lib.fq_grad_clip, dev, stream, g.tensors, len(g.tensors), max_grad_norm,
-          _expect(n, "norm", norm, _F32, (1,), dev))
+    _call(n, _lib.fq_grad_clip, dev, stream, *g.args, max_grad_norm, _expect(n, "norm", norm, _F32, (1,), dev))
 
 
 def _scale_shape(q: QDesc, E, N, K):
