@@ -44,9 +44,9 @@ __device__ __forceinline__ uint64_t key_of(float z, int64_t col) {
 __device__ __forceinline__ int32_t key_id(uint64_t key) { return (int32_t)~(uint32_t)key; }
 __device__ __forceinline__ float key_z(uint64_t key) { return value_of((uint32_t)(key >> 32)); }
 
-// lanes below this one in a mask
-__device__ __forceinline__ int lanes_before(uint64_t mask) {
-    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+// lanes below this one in a mask, and `from`
+__device__ __forceinline__ int lanes_before(uint64_t mask, int from) {
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, from));
 }
 
 // Wave reductions by moves inside the vector unit (row_shr 1, 2, 4, 8, then
@@ -78,7 +78,7 @@ __device__ __forceinline__ float wave_total(float x) {
 
 // A bound that at least `want` of the wave's 64 N numbers reach, near the largest
 // such: steps down from the largest, `top`, until enough reach it, then halves
-// until exactly `want` do, or 2^12 is left between the bounds.  Counting is one
+// until an eighth more than `want` do, or 2^12 is left between the bounds.  Counting is one
 // comparison and a population count of its mask, without the lanes' exchange
 // that a sort needs (21 steps of two moves through LDS).
 template <int N>
@@ -98,7 +98,7 @@ __device__ __forceinline__ uint32_t reached_by(const uint32_t (&o)[N], int want,
         if (d == 0) lo = 0;
         c = count(lo);
     }
-    while (c > want && hi - lo > (1u << 12)) {
+    while (c > want + (want >> 3) && hi - lo > (1u << 12)) {
         const uint32_t mid = lo + (hi - lo) / 2;
         const int n = count(mid);
         if (n >= want) {
@@ -138,8 +138,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // The best keys of a block, in LDS: appended in any order, cut down to the k
 // best by counting for each key how many are larger.
+template <int N>
 struct Best {
-    static constexpr int CAP = 768;
+    static constexpr int CAP = 2 * N + 256;
     __attribute__((aligned(16))) uint64_t key[CAP];
     uint64_t kth;          // keys below it cannot be among the k best
     int count;
@@ -158,7 +159,7 @@ struct Best {
     // room for one more key per thread?  All threads call it, between their pushes.
     __device__ __forceinline__ bool full() {
         __syncthreads();
-        const bool f = count > CAP - TPB;
+        const bool f = count > CAP - N;
         __syncthreads();
         return f;
     }
@@ -168,7 +169,7 @@ struct Best {
         int r[Q];
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            mine[q] = (int)threadIdx.x + q * TPB < n ? key[threadIdx.x + q * TPB] : 0;
+            mine[q] = (int)threadIdx.x + q * N < n ? key[threadIdx.x + q * N] : 0;
             r[q] = 0;
         }
         const int to = wave_id() * WAVE < n ? n : 0;               // a wave without keys has nothing to count
@@ -199,8 +200,8 @@ struct Best {
     __device__ void cut(int k) {
         __syncthreads();
         const int n = min(count, CAP);
-        if (n <= TPB) rank<1>(n, k);
-        else rank<CAP / TPB>(n, k);
+        if (n <= N) rank<1>(n, k);
+        else rank<(CAP + N - 1) / N>(n, k);
         if (threadIdx.x == 0) count = min(n, k);
         __syncthreads();
     }
@@ -250,8 +251,9 @@ __device__ __forceinline__ uint4 past_caches(const uint4* p) {
     return make_uint4(v.x, v.y, v.z, v.w);
 }
 
-// The compiler is not to keep what it formed of these before (a second set of
-// registers for a chunk's unpacked elements halves the waves of a SIMD).
+// The compiler is not to keep what it formed of these before: a second set of
+// registers for a chunk's unpacked elements takes a third of the instructions away
+// and half of a SIMD's waves (2048 rows of 151936: 171 us so, 125 with the words).
 template <int N>
 __device__ __forceinline__ void opaque(uint4 (&v)[N]) {
 #pragma unroll
@@ -259,14 +261,17 @@ __device__ __forceinline__ void opaque(uint4 (&v)[N]) {
 }
 
 // A chunk: NL vectors per thread.  Its alternatives are the entries that reach a
-// bound which k threads' maxima reach: about 73 of 16384 for k = 64, kept
-// unsorted, at most rows_keys(k) of them.
+// bound which k threads' maxima reach: about 75 of 16384 for k = 64, kept
+// unsorted, at most rows_keys(k) of them.  Bound by the vector unit: 8 operations
+// an element, one of them an exponential (512 threads and 32768 columns a block:
+// 137 us for 2048 rows of 151936 and 64 alternatives where these take 128).
 template <typename IN, int NL, bool ENT>
 __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
-    constexpr int VEC = Vec<IN>::N, CH = NL * VEC * TPB, WAVES = TPB / 64;
-    __shared__ Best best;
+    constexpr int VEC = Vec<IN>::N, THREADS = TPB, CH = NL * VEC * THREADS, WAVES = THREADS / 64;
+    typedef Best<THREADS> Top;
+    __shared__ Top best;
     __shared__ float red[2][WAVES];
-    __shared__ uint32_t maxima[TPB];
+    __shared__ uint32_t maxima[THREADS], bound;
     __shared__ int found[WAVES];
     const int64_t t = (int64_t)blockIdx.z * ROWS_Y + blockIdx.y, c = blockIdx.x;
     if (t >= a.T) return;
@@ -279,23 +284,20 @@ __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
     uint4 v[NL];
 #pragma unroll
     for (int i = 0; i < NL; ++i)
-        v[i] = past_caches(reinterpret_cast<const uint4*>(src + min((i * TPB + (int)threadIdx.x) * VEC, end)));
+        v[i] = past_caches(reinterpret_cast<const uint4*>(src + min((i * THREADS + (int)threadIdx.x) * VEC, end)));
     if (left < CH) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const int n = left - (i * TPB + (int)threadIdx.x) * VEC;
+            const int n = left - (i * THREADS + (int)threadIdx.x) * VEC;
             if (n < VEC) v[i] = Vec<IN>::cut(v[i], n);
         }
     }
     float tm = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NL; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) tm = fmaxf(tm, Vec<IN>::get(v[i], e));
+    for (int i = 0; i < NL * VEC; ++i) tm = fmaxf(tm, Vec<IN>::get(v[i / VEC], i % VEC));
     maxima[threadIdx.x] = order_of(tm);
     best.clear();
     __syncthreads();
-    // every wave for itself: the chunk's maximum and the bound
     uint32_t o[WAVES], most = 0;
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) {
@@ -304,63 +306,21 @@ __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
     }
     most = wave_top(most);
     const float M = value_of(most);
-    if (a.k > 0) {
+    if (a.k > 0 && w == 0) {                                       // the others go on to the sums
         const uint32_t r = reached_by(o, a.k, most);
-        const float thr = r > ORDER_MIN ? value_of(r) : -0x1.fffffep+127f;   // -inf is no alternative
-        // a wave's own part of the list, counted in a scalar
-        constexpr int PART = Best::CAP / WAVES;
-        int mine = 0;
-        opaque(v);
-#pragma unroll
-        for (int i = 0; i < NL; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float x = Vec<IN>::get(v[i], e);
-                const uint64_t mask = __ballot(x >= thr);
-                if (mask != 0) {
-                    const int at = mine + lanes_before(mask);
-                    if (x >= thr && at < PART)
-                        best.key[w * PART + at] = key_of(x, lo + (i * TPB + (int)threadIdx.x) * VEC + e);
-                    mine += __popcll(mask);
-                }
-            }
-        if (lane == 0) found[w] = mine;
-        __syncthreads();
-        const int cap = rows_keys(a.k);
-        int total = 0, base = 0;
-#pragma unroll
-        for (int i = 0; i < WAVES; ++i) {
-            base += i < w ? found[i] : 0;
-            total += found[i];
-        }
-        uint64_t* out = a.keys + (t * a.nc + c) * cap;
-        if (total <= cap) {                                        // cap <= PART: no part is cut off
-            for (int i = lane; i < mine; i += 64) out[base + i] = best.key[w * PART + i];
-            for (int i = total + threadIdx.x; i < cap; i += TPB) out[i] = 0;
-        } else {                                                   // many equal ones: again, cut down on the way
-            for (int col = threadIdx.x; col < CH; col += TPB) {
-                const float x = col < left ? Vec<IN>::one(src[col]) : -INFINITY;
-                const uint64_t key = key_of(x, lo + col);
-                best.push(x >= thr && key >= best.kth, key);
-                if (total > Best::CAP && best.full()) best.cut(a.k);
-            }
-            best.cut(a.k);
-            for (int i = threadIdx.x; i < cap; i += TPB) out[i] = i < best.count ? best.key[i] : 0;
-        }
+        if (lane == 0) bound = r;
     }
     // the frame is M log2 e, rounded; its rounding d is taken off at the end
     const float m = M == -INFINITY ? 0.0f : M, f = m * LOG2E, d = __builtin_fmaf(m, LOG2E, -f);
     float s = 0.0f, u = 0.0f;
     opaque(v);
 #pragma unroll
-    for (int i = 0; i < NL; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float l = __builtin_fmaf(Vec<IN>::get(v[i], e), LOG2E, -f);
-            const float x = exp2_hw(l);
-            s += x;
-            if (ENT) u = __builtin_fmaf(x, fmaxf(l, FLOOR2), u);
-        }
+    for (int i = 0; i < NL * VEC; ++i) {
+        const float l = __builtin_fmaf(Vec<IN>::get(v[i / VEC], i % VEC), LOG2E, -f);
+        const float x = exp2_hw(l);
+        s += x;
+        if (ENT) u = __builtin_fmaf(x, fmaxf(l, FLOOR2), u);
+    }
     s = wave_total(s);
     if (ENT) u = wave_total(u);
     if (lane == 0) {
@@ -377,6 +337,56 @@ __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
         }
         a.part[t * a.nc + c] = make_float4(M, __builtin_fmaf(-d * LN2, s, s), LN2 * __builtin_fmaf(-d, s, u), 0.0f);
     }
+    if (a.k > 0) {
+        const uint32_t r = bound;
+        const float thr = r > ORDER_MIN ? value_of(r) : -0x1.fffffep+127f;   // -inf is no alternative
+        // A wave's own part of the list, counted in a scalar: logit and column, of
+        // which the key is formed at the end.  A part that overflows writes its
+        // last place again and is not used.
+        constexpr int PART = Top::CAP / WAVES;
+        uint64_t* part = best.key + w * PART;
+        int mine = 0;
+        opaque(v);
+#pragma unroll
+        for (int i = 0; i < NL * VEC; ++i) {
+            const float z = Vec<IN>::get(v[i / VEC], i % VEC);
+            const bool in = z >= thr;
+            const uint64_t mask = __ballot(in);
+            if (mask != 0) {
+                const int at = min(lanes_before(mask, mine), PART - 1);
+                if (in)
+                    part[at] = ((uint64_t)__float_as_uint(z) << 32) |
+                               (uint32_t)((int)threadIdx.x * VEC + i / VEC * THREADS * VEC + i % VEC);
+                mine += __popcll(mask);
+            }
+        }
+        if (lane == 0) found[w] = mine;
+        __syncthreads();
+        const int cap = rows_keys(a.k);
+        int total = 0, base = 0, most = 0;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+            base += i < w ? found[i] : 0;
+            total += found[i];
+            most = max(most, found[i]);
+        }
+        uint64_t* out = a.keys + (t * a.nc + c) * cap;
+        if (total <= cap && most <= PART) {
+            for (int i = lane; i < mine; i += 64)
+                out[base + i] = key_of(__uint_as_float((uint32_t)(part[i] >> 32)), lo + (uint32_t)part[i]);
+            for (int i = total + threadIdx.x; i < cap; i += THREADS) out[i] = 0;
+        } else {                                                   // many equal ones: again, cut down on the way
+            __syncthreads();
+            for (int col = threadIdx.x; col < CH; col += THREADS) {
+                const float x = col < left ? Vec<IN>::one(src[col]) : -INFINITY;
+                const uint64_t key = key_of(x, lo + col);
+                best.push(x >= thr && key >= best.kth, key);
+                if (total > Top::CAP && best.full()) best.cut(a.k);
+            }
+            best.cut(a.k);
+            for (int i = threadIdx.x; i < cap; i += THREADS) out[i] = i < best.count ? best.key[i] : 0;
+        }
+    }
 }
 
 // The chunks of a row.  Keys come in batches of 8 a thread, of which those are
@@ -384,7 +394,8 @@ __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
 template <typename IN>
 __global__ __launch_bounds__(TPB) void k_rows_join(RowsArgs a) {
     constexpr int WAVES = TPB / 64, PER = 8;
-    __shared__ Best best;
+    typedef Best<TPB> Top;
+    __shared__ Top best;
     __shared__ float red[3][WAVES];
     __shared__ uint32_t maxima[TPB];
     const int64_t t = block_id();
@@ -454,7 +465,7 @@ __global__ __launch_bounds__(TPB) void k_rows_join(RowsArgs a) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) best.push(x[i] >= from, x[i]);
         __syncthreads();
-        if (best.count > Best::CAP) {                              // many equal ones: again, cut down on the way
+        if (best.count > Top::CAP) {                              // many equal ones: again, cut down on the way
             __syncthreads();
             if (threadIdx.x == 0) best.count = before;
             __syncthreads();
@@ -564,10 +575,11 @@ __global__ __launch_bounds__(TPB) void k_logp_bwd(LogpBwdArgs a) {
 
 }  // namespace
 
-// A block's columns: 16384 of bf16, or 4096 where the rows are too few for the
-// card's blocks.
+// A block's columns: 16384 of bf16, or 4096 where that leaves CUs without one
+// (one row of 151936, 20 alternatives: 12 us with 4096; 32 rows 13.6 with 16384 and
+// 14.8 with 4096, 128 rows and 64 alternatives 20 and 48).
 int64_t rows_chunk(int64_t T, int64_t V) {
-    return T * ((V + 16383) / 16384) >= 512 ? 16384 : 4096;
+    return T * ((V + 16383) / 16384) >= CUS ? 16384 : 4096;
 }
 
 template <typename IN, int NL>
@@ -1164,7 +1176,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
         each_strip([&](float z, int col, int) {
             const uint64_t mask = __ballot(z > kth && z >= from);
             if (mask == 0) return;
-            if (z > kth && z >= from) keys[w][gathered + lanes_before(mask)] = key_of(z, a.c0 + col + lane);
+            if (z > kth && z >= from) keys[w][lanes_before(mask, gathered)] = key_of(z, a.c0 + col + lane);
             gathered += __popcll(mask);
             if (gathered < 64) return;
             put(64);
