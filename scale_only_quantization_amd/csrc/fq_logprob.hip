@@ -605,26 +605,20 @@ hipError_t launch_logprob_bwd(const LogpBwdArgs& a, hipStream_t st) {
 // ---------------------------------------------------------- from hidden states --
 namespace {
 
-// Logits of the given tokens: a wave per token and slot.
-__global__ __launch_bounds__(256) void k_logp_given(HeadLogpArgs a) {
-    const int64_t i = block_id() * 4 + wave_id();
-    if (i >= a.T * a.m) return;
-    const int lane = threadIdx.x & 63;
-    const int id = __builtin_amdgcn_readfirstlane(a.ids[i]);
+// The wave's logit of token t and id, by all its lanes.
+__device__ __forceinline__ float dot_of(const HeadLogpArgs& a, int64_t t, int id) {
+    const uint4* hr = reinterpret_cast<const uint4*>(a.h + t * a.H);
+    const uint4* wr = reinterpret_cast<const uint4*>(a.w + (int64_t)id * a.H);
     float acc = 0.0f;
-    if (id >= 0 && id < a.V) {
-        const uint4* hr = reinterpret_cast<const uint4*>(a.h + i / a.m * a.H);
-        const uint4* wr = reinterpret_cast<const uint4*>(a.w + (int64_t)id * a.H);
-        for (int c = lane; c < (a.H >> 3); c += 64) {
-            float x[8], y[8];
-            unpack8(hr[c], x);
-            unpack8(wr[c], y);
+#pragma unroll 4
+    for (int c = threadIdx.x & 63; c < (a.H >> 3); c += 64) {
+        float x[8], y[8];
+        unpack8(hr[c], x);
+        unpack8(wr[c], y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc = __builtin_fmaf(x[e], y[e], acc);
-        }
+        for (int e = 0; e < 8; ++e) acc = __builtin_fmaf(x[e], y[e], acc);
     }
-    acc = wave_sum(acc);
-    if (lane == 0) a.zs[i] = acc;
+    return wave_total(acc);
 }
 
 // Logits of up to 8 tokens, in fp32: the weight is read once, a kilobyte of a row
@@ -1078,11 +1072,13 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
             if (a.lse) a.lse[t] = lse;
             if (ent) a.entropy[t] = ls - u / s;
         }
-        if (lane < a.m) {
-            const int id = a.ids[t * a.m + lane];
-            a.logp[t * a.m + lane] = id >= 0 && id < a.V ? logp(a.zs[t * a.m + lane]) : 0.0f;
-        }
     }
+    if (live && a.last)
+        for (int j = sub; j < a.m; j += WPT) {
+            const int id = __builtin_amdgcn_readfirstlane(a.ids[t * a.m + j]);
+            const float x = id >= 0 && id < a.V ? logp(dot_of(a, t, id)) : 0.0f;
+            if (lane == 0) a.logp[t * a.m + j] = x;
+        }
     // More strips above the bound than k: a bound that k parts' maxima reach keeps
     // most of them out (a first piece has no bound before: 75 strips of 1024 for k = 64).
     int marked = 0;
@@ -1209,18 +1205,28 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
     if (lane == 0) a.thr[t] = kth;
 }
 
-// Backward: a token's constants of the epilogue above.
+// Backward: a token's constants of the epilogue above and its given tokens'
+// logits, by WPT waves.
+template <int WPT>
 __global__ __launch_bounds__(256) void k_logp_rowc(HeadLogpArgs a) {
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int lane = threadIdx.x & 63, w = wave_id(), sub = w % WPT;
+    const int64_t t = block_id() * (4 / WPT) + w / WPT;
     if (t >= a.T) return;
-    float A = 0.0f;
-    for (int j = 0; j < a.m; ++j) {
-        const int id = a.ids[t * a.m + j];
-        A += id >= 0 && id < a.V ? a.dlogp[t * a.m + j] : 0.0f;
+    const int id = lane < a.m ? a.ids[t * a.m + lane] : -1;
+    const bool in = id >= 0 && id < a.V;
+    if (sub == 0) {
+        const float A = wave_total(in ? a.dlogp[t * a.m + lane] : 0.0f);
+        const float b = a.dent ? a.dent[t] : 0.0f, H = a.dent ? a.entropy[t] : 0.0f;
+        if (lane == 0) {
+            a.rowc[t] = make_float4(a.lse[t] * LOG2E, __builtin_fmaf(b, H, A), b, 0.0f);
+            a.ones[t] = 1.0f;
+        }
     }
-    const float b = a.dent ? a.dent[t] : 0.0f, H = a.dent ? a.entropy[t] : 0.0f;
-    a.rowc[t] = make_float4(a.lse[t] * LOG2E, __builtin_fmaf(b, H, A), b, 0.0f);
-    a.ones[t] = 1.0f;
+    for (int j = sub; j < a.m; j += WPT) {
+        const int one = __builtin_amdgcn_readlane(in ? id : -1, j);
+        const float z = one >= 0 ? dot_of(a, t, one) : 0.0f;
+        if (lane == 0) a.zs[t * a.m + j] = z;
+    }
 }
 
 // The given tokens' entries of P are zero: their share is added in fp32 at the end.
@@ -1342,9 +1348,6 @@ static hipError_t launch_few(HeadLogpArgs a, hipStream_t st) {
 hipError_t launch_head_logprob_fwd(HeadLogpArgs a, const HeadLogpPlan& pl, hipStream_t st) {
     if (head_logp_few(a.T, a.H)) return launch_few(a, st);
     a.bm = tile_rows(a.T);
-    if (a.m > 0) hipLaunchKernelGGL(k_logp_given, grid_of((a.T * a.m + 3) / 4), dim3(256), 0, st, a);
-    hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
     int64_t c0 = 0;
     while (c0 < a.V) {
         const int64_t left = (a.V - c0 + BN - 1) / BN * BN;
@@ -1365,7 +1368,7 @@ hipError_t launch_head_logprob_fwd(HeadLogpArgs a, const HeadLogpPlan& pl, hipSt
         }
         if (a.T >= 8192) hipLaunchKernelGGL(k_logp_merge<1>, dim3((unsigned)((a.T + 127) / 128 * 8)), dim3(1024), 0, st, a);
         else hipLaunchKernelGGL(k_logp_merge<4>, dim3((unsigned)((a.T + 31) / 32 * 8)), dim3(1024), 0, st, a);
-        err = hipGetLastError();
+        const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
         c0 += n;
     }
@@ -1375,8 +1378,8 @@ hipError_t launch_head_logprob_fwd(HeadLogpArgs a, const HeadLogpPlan& pl, hipSt
 hipError_t launch_head_logprob_bwd(HeadLogpArgs a, const HeadPlan& pl, hipStream_t st) {
     a.bm = tile_rows(a.T);
     a.vc = pl.vc;
-    if (a.m > 0) hipLaunchKernelGGL(k_logp_given, grid_of((a.T * a.m + 3) / 4), dim3(256), 0, st, a);
-    hipLaunchKernelGGL(k_logp_rowc, dim3((unsigned)((a.T + 255) / 256)), dim3(256), 0, st, a);
+    if (a.m > 1) hipLaunchKernelGGL(k_logp_rowc<4>, grid_of(a.T), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL(k_logp_rowc<1>, grid_of((a.T + 3) / 4), dim3(256), 0, st, a);
     HeadArgs g{};
     g.T = a.T;
     g.H = a.H;
