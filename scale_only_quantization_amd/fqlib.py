@@ -584,7 +584,8 @@ def head_logprob_bwd(d: LogprobDesc, h, w, lse, grad, ids=None, dlogp=None, entr
 
 class GradList:
     """Gradients (fp32 or bf16, any shapes) and the places of their clipped values (the gradients themselves
-    without outs), as fq_grad_norm and fq_grad_clip take them.  Keeps the tensors."""
+    without outs), as fq_grad_norm and fq_grad_clip take them.  Keeps the tensors; a place may overlap nothing but
+    its own gradient, so a tensor is listed once."""
 
     def __init__(self, grads, outs=None):
         n = "grad_list"
@@ -599,6 +600,16 @@ class GradList:
             e.grad = _expect(n, "a gradient", g, g.dtype, g.shape, self.device)
             e.out = _expect(n, "an output", o, g.dtype, g.shape, self.device)
             e.count, e.dtype = g.numel(), FQ_F32 if g.dtype is _F32 else FQ_BF16
+        # an output may be its own gradient, and overlap nothing else: blocks write in any order
+        spans = [(e.out, e.out + e.count * o.element_size(), True) for e, o in zip(self.tensors, self.outs) if e.count]
+        spans += [(e.grad, e.grad + e.count * g.element_size(), False) for e, g in zip(self.tensors, self.grads)
+                  if e.count and e.grad != e.out]
+        all_end = out_end = 0
+        for lo, hi, out in sorted(spans):
+            if lo < (all_end if out else out_end):
+                raise ValueError(f"{n}: an output overlaps another tensor of the list")
+            all_end = max(all_end, hi)
+            out_end = max(out_end, hi) if out else out_end
         self.args = ctypes.addressof(self.tensors), len(self.grads)
 
 

@@ -195,3 +195,39 @@ def test_rows_of_logits():
     full = _strided((3, 64), bf)
     full.t = full.t[:, :61]
     assert F._rows("x", "logits", full, (3, 61), 0)[1] == 64
+
+
+def test_grad_list_refuses_overlaps():
+    f, bf = torch.float32, torch.bfloat16
+
+    class Fake:
+        """A contiguous view of a buffer, said to be on GPU 0."""
+        is_cuda = True
+
+        def __init__(self, t):
+            self.t = t
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+        def get_device(self):
+            return 0
+
+    buf, other = torch.zeros(100), torch.zeros(100)
+    v = lambda lo, hi, b=buf: Fake(b[lo:hi])  # noqa: E731
+    F.grad_list([v(0, 10), v(10, 20), v(20, 20), v(25, 100)])
+    F.grad_list([v(0, 10), v(5, 15)], [v(0, 10, other), v(10, 20, other)])          # gradients that share memory
+    F.grad_list([v(0, 10), v(10, 20)], [v(0, 10, other), v(10, 20)])                # one of them in place
+    for g, o in (([v(0, 10), v(0, 10)], None), ([v(0, 10), v(9, 20)], None), ([v(0, 10)], [v(5, 15)]),
+                 ([v(0, 10), v(20, 30)], [v(50, 60), v(0, 10)]), ([v(0, 10), v(20, 30)], [v(50, 60), v(55, 65)]),
+                 ([v(0, 50), v(60, 70)], [v(0, 50), v(10, 20)])):
+        with pytest.raises(ValueError, match="overlaps"):
+            F.grad_list(g, o)
+    with pytest.raises(ValueError, match="gradients must be"):
+        F.grad_list([Fake(torch.zeros(4, dtype=torch.float64))])
+    with pytest.raises(ValueError, match="output"):
+        F.grad_list([v(0, 10)], [Fake(torch.zeros(10, dtype=bf))])
+    with pytest.raises(ValueError, match="output"):
+        F.grad_list([v(0, 10)], [v(0, 9, other)])
+    with pytest.raises(ValueError, match="contiguous"):
+        F.grad_list([Fake(torch.zeros((4, 4), dtype=f).t()[1:])])
