@@ -940,6 +940,15 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
                         acc[ti][tj][v] = -exp2_hw(l) * __builtin_fmaf(b, l, c);
                     }
                 past(0.0f);
+                // the one given token's entry, if it lies in these 64 columns: its share is added in fp32 at the end
+                const int own = __float_as_int(rc[row].w) - (int)(a.c0 + (int64_t)tn * BN + wn * 64);
+                if (__any((unsigned)own < 64u)) {
+#pragma unroll
+                    for (int tj = 0; tj < WTN; ++tj)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v)
+                            if (own == tj * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) acc[ti][tj][v] = 0.0f;
+                }
 #pragma unroll
                 for (int tj = 0; tj < WTN; ++tj)
 #pragma unroll
@@ -1218,7 +1227,8 @@ __global__ __launch_bounds__(256) void k_logp_rowc(HeadLogpArgs a) {
         const float A = wave_total(in ? a.dlogp[t * a.m + lane] : 0.0f);
         const float b = a.dent ? a.dent[t] : 0.0f, H = a.dent ? a.entropy[t] : 0.0f;
         if (lane == 0) {
-            a.rowc[t] = make_float4(a.lse[t] * LOG2E, __builtin_fmaf(b, H, A), b, 0.0f);
+            a.rowc[t] = make_float4(a.lse[t] * LOG2E, __builtin_fmaf(b, H, A), b,
+                                    __int_as_float(a.m == 1 && in ? id : -1));
             a.ones[t] = 1.0f;
         }
     }
@@ -1229,7 +1239,8 @@ __global__ __launch_bounds__(256) void k_logp_rowc(HeadLogpArgs a) {
     }
 }
 
-// The given tokens' entries of P are zero: their share is added in fp32 at the end.
+// Several given tokens' entries of P are zero (a single one's is made so in the
+// epilogue, which saves a launch): their share is added in fp32 at the end.
 __global__ __launch_bounds__(256) void k_logp_clear(HeadLogpArgs a) {
     const int64_t i = block_id() * 256 + threadIdx.x;
     if (i >= a.T * a.m) return;
@@ -1237,7 +1248,9 @@ __global__ __launch_bounds__(256) void k_logp_clear(HeadLogpArgs a) {
     if (id >= a.c0 && id < a.V && id - a.c0 < a.vc) a.p[i / a.m * a.vc + (id - a.c0)] = 0;
 }
 
-// dh = sum of the splits + sum_j coef_j w_id_j: a block per token
+// dh = sum of the splits + sum_j coef_j w_id_j: a block per token, VEC columns per
+// thread (4 where there are several splits, for more loads in flight).
+template <int VEC>
 __global__ __launch_bounds__(256) void k_logp_out(HeadLogpArgs a, int splits) {
     __shared__ int sid[64];
     __shared__ float scoef[64];
@@ -1254,22 +1267,34 @@ __global__ __launch_bounds__(256) void k_logp_out(HeadLogpArgs a, int splits) {
         scoef[j] = in ? a.dlogp[t * a.m + j] - (first ? exp2_hw(l) * __builtin_fmaf(rc.z * LN2, l, rc.y) : 0.0f) : 0.0f;
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < (a.H >> 3); c += 256) {
-        float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-        for (int s = 0; s < splits; ++s) {
-            const float4* g = reinterpret_cast<const float4*>(a.g + ((int64_t)s * a.T + t) * a.H) + 2 * c;
-            const float4 x = g[0], y = g[1];
-            o[0] += x.x; o[1] += x.y; o[2] += x.z; o[3] += x.w;
-            o[4] += y.x; o[5] += y.y; o[6] += y.z; o[7] += y.w;
-        }
-        for (int j = 0; j < a.m; ++j) {
-            float x[8];
-            unpack8(reinterpret_cast<const uint4*>(a.w + (int64_t)sid[j] * a.H)[c], x);
+    typedef uint32_t words __attribute__((ext_vector_type(VEC / 2)));
+    for (int c = threadIdx.x; c < a.H / VEC; c += 256) {
+        float o[VEC];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __builtin_fmaf(scoef[j], x[e], o[e]);
+        for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
+#pragma unroll 16
+        for (int s = 0; s < splits; ++s) {
+            const float4* g = reinterpret_cast<const float4*>(a.g + ((int64_t)s * a.T + t) * a.H + VEC * c);
+#pragma unroll
+            for (int i = 0; i < VEC / 4; ++i) {
+                const float4 x = g[i];
+                o[4 * i] += x.x; o[4 * i + 1] += x.y; o[4 * i + 2] += x.z; o[4 * i + 3] += x.w;
+            }
         }
-        reinterpret_cast<uint4*>(a.grad + t * a.H)[c] = pack8(o);
+#pragma unroll 4
+        for (int j = 0; j < a.m; ++j) {
+            const float k = scoef[j];
+            const words x = reinterpret_cast<const words*>(a.w + (int64_t)sid[j] * a.H)[c];
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) {
+                o[2 * i] = __builtin_fmaf(k, bf_lo(x[i]), o[2 * i]);
+                o[2 * i + 1] = __builtin_fmaf(k, bf_hi(x[i]), o[2 * i + 1]);
+            }
+        }
+        words r;
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) r[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
+        reinterpret_cast<words*>(a.grad + t * a.H)[c] = r;
     }
 }
 
@@ -1396,11 +1421,12 @@ hipError_t launch_head_logprob_bwd(HeadLogpArgs a, const HeadPlan& pl, hipStream
         a.c0 = g.c0 = (int64_t)i * pl.vc;
         g.first = i == 0;
         hipLaunchKernelGGL((k_head_z<GRAD, false>), dim3(product_grid(a)), dim3(512), 0, st, a);
-        if (a.m > 0) hipLaunchKernelGGL(k_logp_clear, grid_of((a.T * a.m + 255) / 256), dim3(256), 0, st, a);
+        if (a.m > 1) hipLaunchKernelGGL(k_logp_clear, grid_of((a.T * a.m + 255) / 256), dim3(256), 0, st, a);
         hipError_t err = hipGetLastError();
         if (err != hipSuccess || (err = launch_head_grad(g, st)) != hipSuccess) return err;
     }
-    hipLaunchKernelGGL(k_logp_out, grid_of(a.T), dim3(256), 0, st, a, pl.splits);
+    if (pl.splits > a.m + 1) hipLaunchKernelGGL(k_logp_out<4>, grid_of(a.T), dim3(256), 0, st, a, pl.splits);
+    else hipLaunchKernelGGL(k_logp_out<8>, grid_of(a.T), dim3(256), 0, st, a, pl.splits);
     return hipGetLastError();
 }
 
