@@ -7,10 +7,26 @@
 //   dL/dz = sum_j a_j [v = id_j] - p (A + b (log p + entropy)),  A = sum_j a_j
 //
 // A row is cut into chunks that a block holds in registers (each logit is read
-// once); a chunk leaves its maximum, s and u and its k best entries, and k_rows_join
-// combines the chunks of a row.  An entry is a key of 64 bits, the logit's order
-// above the id's complement: keys are distinct, and the largest key is the
-// largest logit, the lowest id among equal ones, in whatever order keys are met.
+// once); a chunk leaves its maximum, s and u and the entries that can be among the
+// k best, and k_rows_join combines the chunks of a row.  An entry is a key of 64
+// bits, the logit's order above the id's complement: keys are distinct, and the
+// largest key is the largest logit, the lowest id among equal ones, in whatever
+// order keys are met.
+//
+// From hidden states the logits z = h W^T come from
+//   k_head_rows, k_head_few   a few tokens: the weight read once, fp32 logits, then
+//       the kernels above on them
+//   k_head_z   more: the output layer's tile product over pieces of the vocabulary,
+//       whose epilogue leaves for a token's strips of 64 columns m, s and u, and
+//       stores a strip's logits only where its maximum is above the k-th best of the
+//       pieces before; k_logp_merge joins a piece's strips to the tokens' running
+//       sums and alternatives.  In the backward it leaves dL/dz in bf16, which the
+//       loss's second product multiplies with the weight.
+// 16384 tokens of hidden 2048, 151936 entries, 64 alternatives: 8.1-8.4 ms, of
+// which the products 7.4 (1380 TFLOP/s; a library product of that size 1357 to
+// 1398) and the 16 merges 0.7; 2048 tokens 1.05-1.08 ms; 333 x 1024 x 32003 44 us,
+// one tile per CU, 33 in the product, whose two stages leave each load's latency
+// bare.  The gradient of 2048 tokens 1.94-2.03 ms, half in each product.
 #include <algorithm>
 
 #include "fq_head_product.h"
@@ -971,23 +987,23 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
     product(la, lb, acc, smem, (t1 - t0 + per - 1) / per, a.H / BK, wr, next, nti, epilogue);
 }
 
-// A piece joins its tokens' running sums and alternatives: 16 / WPT tokens per
-// block, first 64 WPT threads per token over the strips of 64 columns, then WPT
+// A piece joins its tokens' running sums and alternatives: TOK tokens per block,
+// first 64 WPT threads per token over the strips of 64 columns, then WPT
 // waves per token over the strips that can hold an alternative.  A wave's best are
 // its lanes' keys in descending order; logits above the k-th are gathered in LDS
 // and put in 64 at a time by a sort and a merge, the last few one at a time.
 // Sums are joined in frames of z itself: a strip's base-2 frame, m log2 e rounded,
 // is known exactly with its rounding d, and s and u are brought from it to m.
 constexpr int MWORDS = LOGP_MAX_PIECE / 64 / 32, MLIST = 16, MPARTS = 256;
-template <int WPT>
-__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void k_logp_merge(HeadLogpArgs a) {
-    constexpr int TOK = 16 / WPT, PER = 1024 / TOK, SUB = MPARTS / PER, UN = 8;
-    __shared__ float red[3][16][TOK];
+template <int WPT, int TOK>
+__global__ __launch_bounds__(64 * WPT * TOK) __attribute__((amdgpu_waves_per_eu(8))) void k_logp_merge(HeadLogpArgs a) {
+    constexpr int WAVES = WPT * TOK, PER = 64 * WPT, SUB = MPARTS / PER, UN = 8;
+    __shared__ float red[3][WAVES][TOK];
     __shared__ float tmax[TOK][MPARTS];
     __shared__ uint32_t flag[TOK][MWORDS];
-    __shared__ uint16_t list[16][MLIST * 32];
+    __shared__ uint16_t list[WAVES][MLIST * 32];
     __shared__ float bound[TOK];
-    __shared__ uint64_t keys[16][128];
+    __shared__ uint64_t keys[WAVES][128];
     const int tok = threadIdx.x & (TOK - 1), sl = threadIdx.x / TOK, lane = threadIdx.x & 63, w = wave_id();
     // An XCD has a run of neighbouring tokens: their strips lie in the same cache lines.
     const int group = xcd_tile(blockIdx.x, gridDim.x, (int)((a.T + TOK - 1) / TOK));
@@ -1047,7 +1063,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
             if (top && m > thr) atomicOr(&flag[tok][i >> 5], 1u << (i & 31));
         }
     }
-    // over the token's threads: those of a wave, then the 16 waves, in a fixed order
+    // over the token's threads: those of a wave, then the block's waves, in a fixed order
 #pragma unroll
     for (int m = TOK; m < 64; m <<= 1) {
         const float m2 = __shfl_xor(M, m), s2 = __shfl_xor(s, m), u2 = __shfl_xor(u, m);
@@ -1062,11 +1078,11 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
 #pragma unroll
         for (int j = 0; j < SUB; ++j) tmax[tok][sl * SUB + j] = tm[j];
     __syncthreads();
-    M = red[0][lane & 15][tk];
-    s = red[1][lane & 15][tk];
-    u = red[2][lane & 15][tk];
+    M = red[0][lane % WAVES][tk];
+    s = red[1][lane % WAVES][tk];
+    u = red[2][lane % WAVES][tk];
 #pragma unroll
-    for (int m = 1; m < 16; m <<= 1) {
+    for (int m = 1; m < WAVES; m <<= 1) {
         const float m2 = __shfl_xor(M, m), s2 = __shfl_xor(s, m), u2 = __shfl_xor(u, m);
         join(m2, s2, u2);
     }
@@ -1249,7 +1265,8 @@ __global__ __launch_bounds__(256) void k_logp_clear(HeadLogpArgs a) {
 }
 
 // dh = sum of the splits + sum_j coef_j w_id_j: a block per token, VEC columns per
-// thread (4 where there are several splits, for more loads in flight).
+// thread: 4 where there are many splits, for more loads in flight (333 rows of 1024,
+// 32 splits: 9.2 us and 9.6; 2048 of 2048, 4 splits: 18.7 and 16.0).
 template <int VEC>
 __global__ __launch_bounds__(256) void k_logp_out(HeadLogpArgs a, int splits) {
     __shared__ int sid[64];
@@ -1391,8 +1408,14 @@ hipError_t launch_head_logprob_fwd(HeadLogpArgs a, const HeadLogpPlan& pl, hipSt
             if (a.entropy) hipLaunchKernelGGL((k_head_z<SUMS, true>), grid, dim3(512), 0, st, a);
             else hipLaunchKernelGGL((k_head_z<SUMS, false>), grid, dim3(512), 0, st, a);
         }
-        if (a.T >= 8192) hipLaunchKernelGGL(k_logp_merge<1>, dim3((unsigned)((a.T + 127) / 128 * 8)), dim3(1024), 0, st, a);
-        else hipLaunchKernelGGL(k_logp_merge<4>, dim3((unsigned)((a.T + 31) / 32 * 8)), dim3(1024), 0, st, a);
+        auto merge = [&](auto kernel, int wpt, int tok) {
+            const unsigned groups = (unsigned)((a.T + tok - 1) / tok);
+            hipLaunchKernelGGL(kernel, dim3((groups + 7) / 8 * 8), dim3(64 * wpt * tok), 0, st, a);
+        };
+        // a wave per token where tokens fill the card, else two (16384 tokens: 8070
+        // us and 8290; 4096 of hidden 512: 955 and 961; 2048: 1090 and 1080; 333: 47 and 44)
+        if (a.T >= 4096) merge(k_logp_merge<1, 4>, 1, 4);
+        else merge(k_logp_merge<2, 4>, 2, 4);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
         c0 += n;
@@ -1425,7 +1448,7 @@ hipError_t launch_head_logprob_bwd(HeadLogpArgs a, const HeadPlan& pl, hipStream
         hipError_t err = hipGetLastError();
         if (err != hipSuccess || (err = launch_head_grad(g, st)) != hipSuccess) return err;
     }
-    if (pl.splits > a.m + 1) hipLaunchKernelGGL(k_logp_out<4>, grid_of(a.T), dim3(256), 0, st, a, pl.splits);
+    if (pl.splits >= 16) hipLaunchKernelGGL(k_logp_out<4>, grid_of(a.T), dim3(256), 0, st, a, pl.splits);
     else hipLaunchKernelGGL(k_logp_out<8>, grid_of(a.T), dim3(256), 0, st, a, pl.splits);
     return hipGetLastError();
 }
