@@ -997,7 +997,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
 constexpr int MWORDS = LOGP_MAX_PIECE / 64 / 32, MLIST = 16, MPARTS = 256;
 template <int WPT, int TOK>
 __global__ __launch_bounds__(64 * WPT * TOK) __attribute__((amdgpu_waves_per_eu(8))) void k_logp_merge(HeadLogpArgs a) {
-    constexpr int WAVES = WPT * TOK, PER = 64 * WPT, SUB = MPARTS / PER, UN = 8;
+    constexpr int WAVES = WPT * TOK, PER = 64 * WPT, SUB = MPARTS / PER, UN = 4;
     __shared__ float red[3][WAVES][TOK];
     __shared__ float tmax[TOK][MPARTS];
     __shared__ uint32_t flag[TOK][MWORDS];
