@@ -536,9 +536,9 @@ int fq_logprob_bwd(const fq_logprob_desc* d, const void* logits, int64_t row_str
                    int64_t grad_stride, void* stream);
 /* The same from h: device bf16 [tokens, hidden] and w: device bf16 [vocab,
  * hidden], both 16-B aligned.  with_grad: the size for the backward instead of
- * the forward; at most about 640 MB for a piece of the vocabulary beside 8 bytes
- * per token, alternative and 64 vocabulary entries (forward) or fp32 sums of the
- * gradient (backward), or what one piece of 256 entries takes. */
+ * the forward.  Forward: at most about 680 MB for the logits and sums of a piece of
+ * the vocabulary (or what 256 entries of it take), and 20 bytes per token and 8 per
+ * alternative.  Backward: about fq_head_loss_workspace_size's. */
 size_t fq_head_logprob_workspace_size(const fq_logprob_desc* d, int32_t with_grad);
 int fq_head_logprob_fwd(const fq_logprob_desc* d, const void* h, const void* w, const int32_t* ids, float* logp,
                         float* lse, float* entropy, int32_t* top_ids, float* top_logp, void* workspace,

@@ -1349,8 +1349,12 @@ HeadLogpPlan head_logp_plan(int64_t T, int64_t H, int64_t V, int k) {
 }
 
 // Tokens few enough for their hidden states to stand in LDS while the weight goes
-// by.
-bool head_logp_few(int64_t T, int64_t H) { return T <= 64 && T * (2 * H + 16) <= FEW_BYTES; }
+// by, and for the logits of the whole vocabulary to stand in the workspace.
+bool head_logp_few(int64_t T, int64_t H, int64_t V, int k) {
+    const int64_t chunks = (V + FEW_CHUNK - 1) / FEW_CHUNK;
+    return T <= 64 && T * (2 * H + 16) <= FEW_BYTES &&
+           T * (head_few_ld(V) * 4 + chunks * (16 + (k > 0 ? rows_keys(k) * 8 : 0))) <= ((int64_t)640 << 20);
+}
 
 static hipError_t launch_few(HeadLogpArgs a, hipStream_t st) {
     const int64_t bytes = a.T * (2 * a.H + 16), tiles = (a.V + 15) / 16;
@@ -1388,7 +1392,7 @@ static hipError_t launch_few(HeadLogpArgs a, hipStream_t st) {
 }
 
 hipError_t launch_head_logprob_fwd(HeadLogpArgs a, const HeadLogpPlan& pl, hipStream_t st) {
-    if (head_logp_few(a.T, a.H)) return launch_few(a, st);
+    if (head_logp_few(a.T, a.H, a.V, a.k)) return launch_few(a, st);
     a.bm = tile_rows(a.T);
     int64_t c0 = 0;
     while (c0 < a.V) {

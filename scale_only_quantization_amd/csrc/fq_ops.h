@@ -160,8 +160,8 @@ struct HeadLogpArgs {
 };
 constexpr int LOGP_MAX_PIECE = 131072;
 constexpr int FEW_BYTES = 132 * 1024, FEW_CHUNK = 4096;     // a few tokens: hidden states in LDS, columns of a chunk
-bool head_logp_few(int64_t T, int64_t H);
 inline int64_t head_few_ld(int64_t V) { return (V + 15) / 16 * 16; }
+bool head_logp_few(int64_t T, int64_t H, int64_t V, int k);
 struct HeadLogpPlan {
     int first, most;       // entries of the first piece and of the longest (multiples of 256)
     int round;             // of a round of tiles over the card

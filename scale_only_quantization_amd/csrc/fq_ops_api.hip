@@ -244,14 +244,14 @@ HeadLogpLayout head_logp_layout(const fq_logprob_desc* d, bool grad) {
     Placer place;
     HeadLogpLayout y{};
     const size_t T = (size_t)d->tokens;
-    y.zs = place(T * (size_t)d->given * 4);
     if (grad) {
+        y.zs = place(T * (size_t)d->given * 4);
         const HeadPlan pl = head_plan(d->tokens, d->hidden, d->vocab);
         y.rowc = place(T * 16);
         y.ones = place(T * 4);
         y.p = place(T * (size_t)pl.vc * 2);
         y.g = place((size_t)pl.splits * T * (size_t)d->hidden * 4);
-    } else if (head_logp_few(d->tokens, d->hidden)) {
+    } else if (head_logp_few(d->tokens, d->hidden, d->vocab, d->top)) {
         const size_t nc = (size_t)((d->vocab + FEW_CHUNK - 1) / FEW_CHUNK);
         y.run = place(T * nc * sizeof(float4));
         y.keys = place(d->top > 0 ? T * nc * (size_t)rows_keys(d->top) * 8 : 0);
@@ -368,7 +368,6 @@ int fq_head_logprob_fwd(const fq_logprob_desc* d, const void* h, const void* w, 
     a.logp = logp;
     a.top_ids = top_ids;
     a.top_logp = top_logp;
-    a.zs = reinterpret_cast<float*>(ws + y.zs);
     a.thr = reinterpret_cast<float*>(ws + y.thr);
     a.run = reinterpret_cast<float4*>(ws + y.run);
     a.keys = reinterpret_cast<uint64_t*>(ws + y.keys);

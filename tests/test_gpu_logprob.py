@@ -279,7 +279,7 @@ HEAD = [(1, 64, 1, 1, 1), (1, 64, 300, 1, 20), (1, 2048, 20011, 1, 20), (2, 128,
         (33, 192, 4096, 64, 64), (65, 128, 40001, 1, 64), (100, 64, 255, 1, 33), (257, 192, 1000, 3, 5),
         (16, 2048, 5001, 1, 20), (9, 4096, 3001, 1, 20), (32, 2048, 3001, 1, 5), (64, 1024, 3003, 2, 64),
         (1, 16384, 300, 1, 1), (4, 16384, 301, 0, 3), (333, 1024, 32003, 1, 64), (700, 128, 33000, 1, 64), (1030, 64, 20000, 0, 1), (513, 256, 9001, 1, 0),
-        (2100, 64, 100000, 1, 64)]
+        (2100, 64, 100000, 1, 64), (40, 64, 4200000, 1, 64)]
 
 
 @pytest.mark.parametrize("T,H,V,m,k", HEAD)

@@ -103,11 +103,12 @@ def test_workspace_sizes():
     for d in (F.logprob_desc(4, 100), F.logprob_desc(4, 100, hidden=100), F.logprob_desc(4, 100, 0, 65, hidden=128)):
         assert F.head_logprob_workspace_size(d) == 0 and F.head_logprob_workspace_size(d, True) == 0
     # a piece of about 640 MB, whatever the sizes, and what the header adds to it
-    for T, H, V, k in ((1, 2048, 151936, 64), (64, 2048, 151936, 20), (2048, 2048, 151936, 64), (16384, 2048, 151936, 64),
-                       (100000, 4096, 151936, 64)):
+    for T, H, V, k in ((1, 2048, 151936, 64), (64, 1024, 151936, 20), (64, 2048, 151936, 20), (2048, 2048, 151936, 64),
+                       (16384, 2048, 151936, 64), (16384, 2048, 151936, 0), (100000, 4096, 151936, 64), (1, 64, 1 << 30, 64),
+                       (64, 64, (1 << 31) - 1, 64), (300, 64, (1 << 31) - 1, 0), ((1 << 24) - 1, 64, 1000, 64)):
         d = F.logprob_desc(T, V, 1, k, H)
         size = F.head_logprob_workspace_size(d)
-        assert size <= (640 << 20) + T * ((V // 64 + 256) * 16 + k * 8 * (V // 64 + 1) + 4096), (T, size)
+        assert size <= max(680 << 20, T * 256 * 5) + T * (20 + 8 * k) + 4096, (T, size)
         assert F.head_logprob_workspace_size(d, True) <= F.head_loss_workspace_size(F.head_desc(T, H, V, 0)) + T * 64 + 4096
 
 
