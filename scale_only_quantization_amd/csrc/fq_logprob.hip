@@ -22,11 +22,11 @@
 //       pieces before; k_logp_merge joins a piece's strips to the tokens' running
 //       sums and alternatives.  In the backward it leaves dL/dz in bf16, which the
 //       loss's second product multiplies with the weight.
-// 16384 tokens of hidden 2048, 151936 entries, 64 alternatives: 8.1-8.4 ms, of
+// 16384 tokens of hidden 2048, 151936 entries, 64 alternatives: 8.0-8.2 ms, of
 // which the products 7.4 (1380 TFLOP/s; a library product of that size 1357 to
-// 1398) and the 16 merges 0.7; 2048 tokens 1.05-1.08 ms; 333 x 1024 x 32003 44 us,
-// one tile per CU, 33 in the product, whose two stages leave each load's latency
-// bare.  The gradient of 2048 tokens 1.94-2.03 ms, half in each product.
+// 1398) and the 16 merges 0.6-0.75; 2048 tokens 1.05-1.08 ms; 333 x 1024 x 32003
+// 43-47 us, one tile per CU, 33 in the product, whose two stages leave each load's
+// latency bare.  The gradient of 2048 tokens 1.94-2.03 ms, half in each product.
 #include <algorithm>
 
 #include "fq_head_product.h"
@@ -279,8 +279,9 @@ __device__ __forceinline__ void opaque(uint4 (&v)[N]) {
 // A chunk: NL vectors per thread.  Its alternatives are the entries that reach a
 // bound which k threads' maxima reach: about 75 of 16384 for k = 64, kept
 // unsorted, at most rows_keys(k) of them.  Bound by the vector unit: 8 operations
-// an element, one of them an exponential (512 threads and 32768 columns a block:
-// 137 us for 2048 rows of 151936 and 64 alternatives where these take 128).
+// an element, one of them an exponential: 2048 rows of 151936 with 64 alternatives
+// 110-120 us and 12.5 for the join, 98 without alternatives (with 512 threads and
+// 32768 columns a block 9 more).
 template <typename IN, int NL, bool ENT>
 __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
     constexpr int VEC = Vec<IN>::N, THREADS = TPB, CH = NL * VEC * THREADS, WAVES = THREADS / 64;
@@ -743,10 +744,9 @@ __global__ __launch_bounds__(ROW_TPB) void k_head_rows(HeadLogpArgs a) {
 // into the matrix instruction's operand; the hidden states stand in LDS, rows 16
 // bytes apart from a multiple of the banks.  A block has a run of rows, 16 at a
 // time, its waves a share of the columns each, so that what the card reads at once
-// are a few whole stretches of memory, past the caches: for one token of 2048 by
-// 151936 118 us with whole rows to a wave, strided over the card (5.3 TB/s).  The
-// next rows' loads are in flight while a wave multiplies and the block adds its
-// waves' sums.
+// are a few whole stretches of memory, past the caches (5.4 TB/s; 5.3 with whole
+// rows to a wave, strided over the card).  The next rows' loads are in flight while
+// a wave multiplies and the block adds its waves' sums.
 constexpr int FEW_LOADS = 8, FEW_STEP = 32 * FEW_LOADS, FEW_TPB = 512, FEW_WAVES = FEW_TPB / 64;
 template <int NT, int BYTES>
 __global__ __launch_bounds__(FEW_TPB) void k_head_few(HeadLogpArgs a) {
@@ -1361,11 +1361,14 @@ static hipError_t launch_few(HeadLogpArgs a, hipStream_t st) {
     a.vc = (int)head_few_ld(a.V);
     auto grid = [&](int per_cu) { return dim3((unsigned)std::min<int64_t>((int64_t)CUS * per_cu, tiles)); };
     const int64_t row = (a.H + 511) / 512 * 1024;          // bytes of a token's padded row
+    // 2048 by 151936, with 20 alternatives, by rows of the weight and by the matrix
+    // operand: 1 token 103 and 130 us, 8 tokens 120 and 136, 16 tokens 172 and 146; 1
+    // token in the form for 8: 112, 4: 116 and not 110
     if (a.T == 1 && row <= 32768) hipLaunchKernelGGL((k_head_rows<1, 4, 32768>), grid(2), dim3(ROW_TPB), 0, st, a);
     else if (a.T <= 2 && 2 * row <= 32768) hipLaunchKernelGGL((k_head_rows<2, 4, 32768>), grid(2), dim3(ROW_TPB), 0, st, a);
     else if (a.T <= 4 && 4 * row <= 32768) hipLaunchKernelGGL((k_head_rows<4, 4, 32768>), grid(2), dim3(ROW_TPB), 0, st, a);
     else if (a.T <= 8 && 8 * row <= 65536) hipLaunchKernelGGL((k_head_rows<8, 1, 65536>), grid(2), dim3(ROW_TPB), 0, st, a);
-    else if (a.T <= 16 && bytes <= 20480) hipLaunchKernelGGL((k_head_few<1, 20480>), grid(2), dim3(FEW_TPB), 0, st, a);
+    // two blocks a CU where LDS holds the hidden states twice (16 of 2048: 146 us and 155)
     else if (a.T <= 16 && bytes <= 67584) hipLaunchKernelGGL((k_head_few<1, 67584>), grid(2), dim3(FEW_TPB), 0, st, a);
     else if (a.T <= 16) hipLaunchKernelGGL((k_head_few<1, FEW_BYTES>), grid(1), dim3(FEW_TPB), 0, st, a);
     else if (a.T <= 32) hipLaunchKernelGGL((k_head_few<2, FEW_BYTES>), grid(1), dim3(FEW_TPB), 0, st, a);
