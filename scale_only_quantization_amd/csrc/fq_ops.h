@@ -199,8 +199,9 @@ struct GradClipArgs {
 static_assert(sizeof(GradSqArgs) <= 4096 && sizeof(GradClipArgs) <= 4096, "kernel arguments");
 hipError_t launch_grad_sq(const GradSqArgs& a, hipStream_t st);
 hipError_t launch_grad_clip(const GradClipArgs& a, hipStream_t st);
-// tensors of few elements, and few of them, in one block: the norm itself
-constexpr int GRAD_SMALL = 1024, GRAD_SMALL_LIST = 64;
+// few tensors of few elements, and few in all, in one block: the norm itself (64 of
+// 128: 3.5 us, 4.3 in two launches; 32 of 1024: 3.3 and 4.3; 64 of 1024: 4.7 and 4.3)
+constexpr int GRAD_SMALL = 1024, GRAD_SMALL_LIST = 64, GRAD_SMALL_ALL = 32 * 1024;
 hipError_t launch_grad_norm_small(const GradSqArgs& a, float* norm, hipStream_t st);
 hipError_t launch_grad_norm(const double* part, int64_t n, float* norm, hipStream_t st);
 

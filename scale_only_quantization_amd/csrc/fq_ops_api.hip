@@ -469,11 +469,13 @@ int each_list(const fq_grad_tensor* t, int32_t n, bool backwards, F&& f) {
 // Short tensors, and few: one block reads them all, which saves a launch.
 bool grads_small(const fq_grad_tensor* t, int32_t n) {
     int32_t with = 0;
+    int64_t all = 0;
     for (int32_t i = 0; i < n; ++i) {
         if (t[i].count > GRAD_SMALL) return false;
         with += t[i].count > 0;
+        all += t[i].count;
     }
-    return with > 0 && with <= GRAD_SMALL_LIST;
+    return with > 0 && with <= GRAD_SMALL_LIST && all <= GRAD_SMALL_ALL;
 }
 
 }  // namespace

@@ -46,9 +46,17 @@ SPECS = {
     "all empty": [(0, False, 0)] * 3,
     "offsets": [(n, bf, o) for n in (7, 8, 9, 255, 4097) for bf in (False, True) for o in (0, 1, 2, 3, 5, 7)],
     "chunks": [(16384, False, 0), (16385, True, 0), (16383, False, 1), (32768, True, 3), (163847, False, 0)],
+    "short": [(1024, i % 2 == 0, i % 3) for i in range(32)],
+    "short, one more element": [(1024, i % 2 == 0, i % 3) for i in range(32)] + [(1, False, 0)],
+    "64 short": [(512, i % 2 == 0, i % 3) for i in range(64)] + [(0, False, 0)],
+    "65 short": [(500, i % 2 == 0, i % 3) for i in range(65)],
     "95": [(100 + i, i % 2 == 0, i % 4) for i in range(95)],
     "96": [(100 + i, i % 2 == 0, i % 4) for i in range(96)],
     "97": [(100 + i, i % 2 == 0, i % 4) for i in range(97)],
+    "136": [(2000 + i, i % 2 == 0, i % 4) for i in range(136)],
+    "137": [(2000 + i, i % 2 == 0, i % 4) for i in range(137)],
+    "192": [(2000 + i, i % 2 == 0, i % 4) for i in range(192)],
+    "193": [(2000 + i, i % 2 == 0, i % 4) for i in range(193)],
     "500 with empty ones": [((i * 37) % 301, i % 3 == 0, i % 3) for i in range(500)],
     "long": [(128 * 1536 * 128, False, 0), (3_000_001, True, 1), (128, False, 0)],
 }
