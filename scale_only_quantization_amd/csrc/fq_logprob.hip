@@ -43,6 +43,7 @@ dim3 rows_grid(int64_t chunks, int64_t T) {
 }
 constexpr float FLOOR = -200.0f;          // e^FLOOR is 0 in fp32: keeps 0 times -inf out of sums
 constexpr float FLOOR2 = -300.0f;         // and 2^FLOOR2
+constexpr float FAR = 0x1p125f;           // from here on a frame times log2 e is past fp32
 constexpr float PAST = -1e30f;            // a column past the vocabulary: below what a sum can hold, and finite
 
 // The order of a logit as a whole number: 0 is below all of them.
@@ -328,15 +329,24 @@ __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
         if (lane == 0) bound = r;
     }
     // the frame is M log2 e, rounded; its rounding d is taken off at the end
-    const float m = M == -INFINITY ? 0.0f : M, f = m * LOG2E, d = __builtin_fmaf(m, LOG2E, -f);
-    float s = 0.0f, u = 0.0f;
+    const float m = M == -INFINITY ? 0.0f : M;
+    float f = m * LOG2E, d = __builtin_fmaf(m, LOG2E, -f), s = 0.0f, u = 0.0f;
     opaque(v);
+    if (fabsf(m) >= FAR && fabsf(m) < INFINITY) {                  // e.g. a chunk of masks of the type's lowest value:
+        d = 0.0f;                                                  // what differs from M is 2^101 and more below it
 #pragma unroll
-    for (int i = 0; i < NL * VEC; ++i) {
-        const float l = __builtin_fmaf(Vec<IN>::get(v[i / VEC], i % VEC), LOG2E, -f);
-        const float x = exp2_hw(l);
-        s += x;
-        if (ENT) u = __builtin_fmaf(x, fmaxf(l, FLOOR2), u);
+        for (int i = 0; i < NL * VEC; ++i) {
+            const float z = Vec<IN>::get(v[i / VEC], i % VEC);
+            s += z == M ? 1.0f : z <= M ? 0.0f : z;                // (a NaN stays one)
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NL * VEC; ++i) {
+            const float l = __builtin_fmaf(Vec<IN>::get(v[i / VEC], i % VEC), LOG2E, -f);
+            const float x = exp2_hw(l);
+            s += x;
+            if (ENT) u = __builtin_fmaf(x, fmaxf(l, FLOOR2), u);
+        }
     }
     s = wave_total(s);
     if (ENT) u = wave_total(u);
@@ -511,8 +521,8 @@ __global__ __launch_bounds__(TPB) void k_rows_join(RowsArgs a) {
         if (a.lse) a.lse[t] = lse;
         if (a.entropy) a.entropy[t] = none ? 0.0f : ls - u / s;
     }
-    auto logp = [&](float z) {
-        const float q = none ? -INFINITY : z - lse;
+    auto logp = [&](float z) {                                     // z - f first: lse may be far from 0
+        const float q = none ? -INFINITY : z - f - ls;
         return q > 0.0f ? 0.0f : q;
     };
     if ((int)threadIdx.x < a.m) a.logp[t * a.m + threadIdx.x] = given ? logp(zg) : 0.0f;

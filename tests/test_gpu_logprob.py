@@ -163,6 +163,45 @@ def test_logits_of_every_kind(V, many):
         assert np.array_equal(x, np.tile(x[:len(KINDS)], (z.shape[0] // len(KINDS),) + (1,) * (x.ndim - 1))), n
 
 
+@pytest.mark.parametrize("V", [300, 5000, 40001])
+@pytest.mark.parametrize("many", [False, True])
+def test_logits_masked_by_the_lowest_value(V, many):
+    """Masks of the type's lowest value over whole chunks, over all of a row but a few entries, over a whole row, with
+    ruled-out entries among them; and entries at the other end of the type's range."""
+    rng = np.random.default_rng(V + 7)
+    low = -3.3895313892515355e38
+    z = np.full((6, V), low)
+    z[0, V // 2:V // 2 + 7] = rng.standard_normal(7)             # chunks of nothing but masks beside one with entries
+    z[1, :2] = rng.standard_normal(2) * 1e4
+    z[3, V // 3:] = -np.inf                                       # (2: a row of masks)
+    z[4, rng.choice(V, 9, replace=False)] = -low
+    z[5] = 2.0 ** 126 * (1 + rng.integers(0, 2, V) / 128)
+    z = bf16_rne(np.tile(z, (100 if many else 1, 1)).astype(np.float32))
+    ids = np.stack([np.zeros(len(z)), np.full(len(z), V // 2), np.full(len(z), V - 1)], 1).astype(np.int32)
+    got = _logits_fwd(z, ids, 64)
+    zz = z.astype(np.float64)
+    near = np.arange(len(z)) % 6 < 2
+    _check_forward({n: v[to_dev(near)] for n, v in got.items()}, zz[near], ids[near], 64, what=f"V={V}")
+    # far rows: what is below the maximum is 2^118 and more below it, so p is uniform over the n largest (float64
+    # loses log n beside the maximum, so it is taken apart here); counts below 2^24 are exact, a logarithm of fp32
+    # is within 2 ulps
+    far = ~near
+    ref = O.forward(zz[far], ids[far], 64)
+    top = zz[far].max(-1, keepdims=True)
+    n = (zz[far] == top).sum(-1)
+    with np.errstate(over="ignore"):
+        lp = (zz[far] - top - np.log(n)[:, None]).astype(np.float32).astype(np.float64)    # past fp32: -inf
+    lse, ent = from_dev(got["lse"])[far], from_dev(got["entropy"])[far]
+    assert np.array_equal(lse, z[far].max(-1))
+    assert np.all(np.abs(ent - np.log(n)) <= 4 * H32 * np.log(n))
+    assert np.array_equal(from_dev(got["top_ids"])[far], ref["top_ids"])
+    lt = np.where(ref["top_ids"] >= 0, np.take_along_axis(lp, np.maximum(ref["top_ids"], 0), 1), -np.inf)
+    for x, r in ((from_dev(got["logp"])[far], np.take_along_axis(lp, ids[far], 1)), (from_dev(got["top_logp"])[far], lt)):
+        finite = np.isfinite(r)
+        assert np.array_equal(x[~finite], r[~finite])
+        assert np.all(np.abs(x[finite] - r[finite]) <= 8 * H32 * np.abs(r[finite]))
+
+
 def test_logits_nan_stays_in_its_row():
     rng = np.random.default_rng(5)
     z = bf16_rne(rng.standard_normal((3, 9000)).astype(np.float32))
