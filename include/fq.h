@@ -494,7 +494,8 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
  * top_logp and top_ids are valid teacher_topk_logits / teacher_topk_ids of
  * fq_head_loss and fq_distill_loss (a shift by lse does not change their
  * softmax).  Logits may be -inf (ruled-out tokens: p = 0); a row of nothing
- * else has lse and logp -inf, entropy 0 and gradient 0.
+ * else has lse and logp -inf, entropy 0 and gradient 0.  A row with a NaN or +inf has
+ * lse, logp, entropy and gradient NaN.
  * The gradient, with a_j = dL/dlogp_j (ids inside the vocabulary), A = sum_j a_j
  * and b = dL/dentropy; top_ids and top_logp pass none:
  *     dL/dz_v = sum_j a_j [v = id_j] - p_v (A + b (log p_v + entropy))
@@ -502,7 +503,10 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
  * Sums are fp32; bitwise deterministic.  From hidden states z is an fp32 sum, so
  * two ids whose logits differ by less than its error may change places; in the
  * gradient's product dL/dz is rounded to bf16, except the given tokens', which
- * are added in fp32. */
+ * are added in fp32.  The gradient's p = e^(z - lse) is as good as lse, rounded to
+ * fp32 (a relative error of |lse| 2^-24); from logits, a row whose lse is below
+ * -2^125 is taken as one of nothing but masks (of the type's lowest value) and has
+ * gradient 0. */
 typedef struct {
     int64_t tokens;            /* rows, >= 0, < 2^24                                  */
     int64_t hidden;            /* fq_head_logprob_*: a multiple of 64, 64 .. 16384; fq_logprob_*: 0 */

@@ -556,7 +556,8 @@ __global__ __launch_bounds__(TPB) void k_logp_bwd(LogpBwdArgs a) {
     for (int j = 0; j < a.m; ++j) A += sa[j];
     const float lse = a.lse[t];
     const float bb = a.dent ? a.dent[t] : 0.0f, H = a.dent ? a.entropy[t] : 0.0f;
-    const bool none = lse == -INFINITY;
+    const bool none = lse <= -FAR;                                 // nothing but masks
+    if (lse != lse) A = lse;                                       // a row with a NaN has no gradient but that
     auto grad = [&](float z) {
         const float lp = none ? FLOOR : fmaxf(z - lse, FLOOR);
         const float p = exp2_hw(lp * LOG2E);
@@ -1253,7 +1254,8 @@ __global__ __launch_bounds__(256) void k_logp_rowc(HeadLogpArgs a) {
         const float A = wave_total(in ? a.dlogp[t * a.m + lane] : 0.0f);
         const float b = a.dent ? a.dent[t] : 0.0f, H = a.dent ? a.entropy[t] : 0.0f;
         if (lane == 0) {
-            a.rowc[t] = make_float4(a.lse[t] * LOG2E, __builtin_fmaf(b, H, A), b,
+            const float lse = a.lse[t];                            // (a NaN: the row's gradient is one)
+            a.rowc[t] = make_float4(lse * LOG2E, lse == lse ? __builtin_fmaf(b, H, A) : lse, b,
                                     __int_as_float(a.m == 1 && in ? id : -1));
             a.ones[t] = 1.0f;
         }

@@ -257,6 +257,66 @@ def test_logits_gradient(T, V, m, ent, place):
     assert np.all(from_dev(gbuf)[:, V:] == (5.0 if place == "own" else 3.0))       # what lies beyond the vocabulary
 
 
+@pytest.mark.parametrize("m,ent", [(0, True), (1, False), (2, True)])
+def test_logits_gradient_of_masks_and_nan(m, ent):
+    """Rows of the type's lowest value have gradient 0 like ruled-out ones, a row with a NaN is NaN throughout, and the
+    rows beside them are what they are alone."""
+    F, T_ = _F(), torch()
+    rng = np.random.default_rng(17 + m)
+    V = 9001
+    z = bf16_rne((rng.standard_normal((5, V)) * 2).astype(np.float32))
+    z[1] = bf16_rne(np.full(V, -3.3895313892515355e38, np.float32))
+    z[2, 8000] = np.inf if m == 1 else np.nan
+    z[3] = -np.inf
+    ids = np.tile(np.array([8000, 3][:m], np.int32), (5, 1)) if m else None
+    dl, de = rng.standard_normal((5, m)).astype(np.float32), rng.standard_normal(5).astype(np.float32)
+
+    def grad(rows):
+        fwd = _logits_fwd(z[rows], None, 0)
+        g = T_.full((len(rows), V + 7), 9.0, dtype=T_.bfloat16, device="cuda")[:, :V]
+        zb = _padded(z[rows], 8, 0.0)[1]
+        F.logprob_bwd(F.logprob_desc(len(rows), V, given=m), zb, fwd["lse"], g, ids=to_dev(ids[rows]) if m else None,
+                      dlogp=to_dev(dl[rows]) if m else None, entropy=fwd["entropy"] if ent else None,
+                      dentropy=to_dev(de[rows]) if ent else None)
+        T_.cuda.synchronize()
+        return from_dev(g)
+
+    got = grad([0, 1, 2, 3, 4])
+    assert np.all(got[[1, 3]] == 0.0)
+    assert np.all(np.isnan(got[2]))
+    assert np.array_equal(got[[0, 4]], grad([0, 4])) and np.all(np.isfinite(got[[0, 4]])) and np.any(got[0] != 0.0)
+
+
+@pytest.mark.parametrize("T,m", [(3, 1), (20, 1), (70, 2), (300, 0)])
+def test_head_nan_stays_in_its_row(T, m):
+    """A NaN in a token's hidden state: its lse, entropy and gradient are NaN, ids stay in range, the others as alone."""
+    F, T_ = _F(), torch()
+    H, V, bad = 128, 5003, T // 2
+    h, w, ids, _ = _hidden(T, T, H, V, m)
+    rng = np.random.default_rng(1)
+    dl, de = to_dev(rng.standard_normal((T, m)).astype(np.float32)), to_dev(rng.standard_normal(T).astype(np.float32))
+
+    def run(h):
+        fwd = _head_fwd(h, w, ids, 5)
+        g = T_.empty((T, H), dtype=T_.bfloat16, device="cuda")
+        d = F.logprob_desc(T, V, given=m, hidden=H)
+        F.head_logprob_bwd(d, to_dev_bf16(h), to_dev_bf16(w), fwd["lse"], g, ids=to_dev(ids) if m else None,
+                           dlogp=dl if m else None, entropy=fwd["entropy"], dentropy=de,
+                           workspace=_workspace(F.head_logprob_workspace_size(d, True)))
+        T_.cuda.synchronize()
+        return {n: from_dev(v) for n, v in dict(fwd, g=g).items() if v is not None}
+
+    good = run(h)
+    h = h.copy()
+    h[bad, 7] = np.nan
+    got = run(h)
+    assert np.isnan(got["lse"][bad]) and np.isnan(got["entropy"][bad]) and np.all(np.isnan(got["g"][bad]))
+    assert np.all((got["top_ids"][bad] >= -1) & (got["top_ids"][bad] < V))
+    rest = np.arange(T) != bad
+    for n in good:
+        assert np.array_equal(got[n][rest], good[n][rest]), n
+
+
 def test_logits_past_4gb():
     """Offsets past 32 bits, in bytes and in elements; the last rows are checked."""
     F, T_ = _F(), torch()
