@@ -494,8 +494,8 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
  * top_logp and top_ids are valid teacher_topk_logits / teacher_topk_ids of
  * fq_head_loss and fq_distill_loss (a shift by lse does not change their
  * softmax).  Logits may be -inf (ruled-out tokens: p = 0); a row of nothing
- * else has lse and logp -inf, entropy 0 and gradient 0.  A row with a NaN or +inf has
- * lse, logp, entropy and gradient NaN.
+ * else has lse and logp -inf, entropy 0 and gradient 0.  A row with a NaN or
+ * +inf has lse, logp, entropy and gradient NaN.
  * The gradient, with a_j = dL/dlogp_j (ids inside the vocabulary), A = sum_j a_j
  * and b = dL/dentropy; top_ids and top_logp pass none:
  *     dL/dz_v = sum_j a_j [v = id_j] - p_v (A + b (log p_v + entropy))
