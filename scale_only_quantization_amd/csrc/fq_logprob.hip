@@ -22,11 +22,11 @@
 //       pieces before; k_logp_merge joins a piece's strips to the tokens' running
 //       sums and alternatives.  In the backward it leaves dL/dz in bf16, which the
 //       loss's second product multiplies with the weight.
-// 16384 tokens of hidden 2048, 151936 entries, 64 alternatives: 8.0-8.2 ms, of
+// 16384 tokens of hidden 2048, 151936 entries, 64 alternatives: 8.0-8.4 ms, of
 // which the products 7.4 (1380 TFLOP/s; a library product of that size 1357 to
-// 1398) and the 16 merges 0.6-0.75; 2048 tokens 1.05-1.08 ms; 333 x 1024 x 32003
+// 1398) and the 16 merges 0.6-0.75; 2048 tokens 1.05-1.10 ms; 333 x 1024 x 32003
 // 43-47 us, one tile per CU, 33 in the product, whose two stages leave each load's
-// latency bare.  The gradient of 2048 tokens 1.94-2.03 ms, half in each product.
+// latency bare.  The gradient of 2048 tokens 1.94-2.06 ms, half in each product.
 #include <algorithm>
 
 #include "fq_head_product.h"
