@@ -43,7 +43,11 @@ dim3 rows_grid(int64_t chunks, int64_t T) {
 }
 constexpr float FLOOR = -200.0f;          // e^FLOOR is 0 in fp32: keeps 0 times -inf out of sums
 constexpr float FLOOR2 = -300.0f;         // and 2^FLOOR2
-constexpr float FAR = 0x1p125f;           // from here on a frame times log2 e is past fp32
+// A chunk's frame in base 2, f = M log2 e, is rounded by d, up to half an ulp of f,
+// and the largest entry enters the sum as 2^d.  A correction to first order is as
+// good as fp32 while (d ln 2)^2 / 2 is below half an ulp: d <= 2^-12, |M| < 2^12.
+constexpr float FAR = 0x1p12f;
+constexpr float MASKS = -0x1p125f;        // a row whose lse is below it has nothing but masks of the type's lowest value
 constexpr float PAST = -1e30f;            // a column past the vocabulary: below what a sum can hold, and finite
 
 // The order of a logit as a whole number: 0 is below all of them.
@@ -328,25 +332,24 @@ __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
         const uint32_t r = reached_by(o, a.k, most);
         if (lane == 0) bound = r;
     }
-    // the frame is M log2 e, rounded; its rounding d is taken off at the end
+    // the frame is M log2 e, rounded; its rounding d is taken off at the end.  Far from
+    // 0 (a chunk of finite masks) the distance to M comes first, one operation more
     const float m = M == -INFINITY ? 0.0f : M;
-    float f = m * LOG2E, d = __builtin_fmaf(m, LOG2E, -f), s = 0.0f, u = 0.0f;
+    const bool far = fabsf(m) >= FAR;
+    const float f = m * LOG2E, d = far ? 0.0f : __builtin_fmaf(m, LOG2E, -f);
+    float s = 0.0f, u = 0.0f;
+    auto add = [&](float l) {
+        const float x = exp2_hw(l);
+        s += x;
+        if (ENT) u = __builtin_fmaf(x, fmaxf(l, FLOOR2), u);
+    };
     opaque(v);
-    if (fabsf(m) >= FAR && fabsf(m) < INFINITY) {                  // e.g. a chunk of masks of the type's lowest value:
-        d = 0.0f;                                                  // what differs from M is 2^101 and more below it
+    if (far) {
 #pragma unroll
-        for (int i = 0; i < NL * VEC; ++i) {
-            const float z = Vec<IN>::get(v[i / VEC], i % VEC);
-            s += z == M ? 1.0f : z <= M ? 0.0f : z;                // (a NaN stays one)
-        }
+        for (int i = 0; i < NL * VEC; ++i) add((Vec<IN>::get(v[i / VEC], i % VEC) - m) * LOG2E);
     } else {
 #pragma unroll
-        for (int i = 0; i < NL * VEC; ++i) {
-            const float l = __builtin_fmaf(Vec<IN>::get(v[i / VEC], i % VEC), LOG2E, -f);
-            const float x = exp2_hw(l);
-            s += x;
-            if (ENT) u = __builtin_fmaf(x, fmaxf(l, FLOOR2), u);
-        }
+        for (int i = 0; i < NL * VEC; ++i) add(__builtin_fmaf(Vec<IN>::get(v[i / VEC], i % VEC), LOG2E, -f));
     }
     s = wave_total(s);
     if (ENT) u = wave_total(u);
@@ -556,7 +559,7 @@ __global__ __launch_bounds__(TPB) void k_logp_bwd(LogpBwdArgs a) {
     for (int j = 0; j < a.m; ++j) A += sa[j];
     const float lse = a.lse[t];
     const float bb = a.dent ? a.dent[t] : 0.0f, H = a.dent ? a.entropy[t] : 0.0f;
-    const bool none = lse <= -FAR;                                 // nothing but masks
+    const bool none = lse <= MASKS;
     if (lse != lse) A = lse;                                       // a row with a NaN has no gradient but that
     auto grad = [&](float z) {
         const float lp = none ? FLOOR : fmaxf(z - lse, FLOOR);

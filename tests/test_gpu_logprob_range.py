@@ -1,0 +1,109 @@
+"""Log probabilities over the whole range of logits: masks of any finite size over chunks and over rows, logits far
+from 0, infinities, and hidden states that lie on no grid."""
+import numpy as np
+import pytest
+
+from oracle.numerics import bf16_rne
+from tests.fq_testutil import from_dev, to_dev, to_dev_bf16, torch
+from tests.test_gpu_logprob import _head_fwd, _hidden, _logits_fwd, _padded, _workspace
+
+pytestmark = pytest.mark.gpu
+H32 = 2.0 ** -24          # half an ulp of fp32, relative
+H16 = 2.0 ** -8           # of bf16
+LOWEST = 3.3895313892515355e38
+
+
+def _F():
+    from scale_only_quantization_amd import fqlib
+    return fqlib
+
+
+def _bf(z):
+    with np.errstate(over="ignore"):
+        return bf16_rne(np.asarray(z, np.float32))
+
+
+def _ref(z, ids, k):
+    """The definitions in float64, from the distance to the largest logit, so that log n is not lost beside it."""
+    z = np.asarray(z, np.float64)
+    M = z.max(-1, keepdims=True)
+    none = M == -np.inf
+    with np.errstate(invalid="ignore", divide="ignore"):
+        d = np.where(none, -np.inf, z - np.where(none, 0.0, M))
+        ls = np.log(np.exp(d).sum(-1, keepdims=True))
+        lp = np.where(none, -np.inf, d - ls)
+        p = np.exp(lp)
+        out = dict(M=M[:, 0], ls=ls[:, 0], lse=np.where(none, -np.inf, M + ls)[:, 0], lp=lp, p=p, none=none[:, 0],
+                   entropy=-np.where(p > 0, p * lp, 0.0).sum(-1), spread=np.where(p > 0, -p * d, 0.0).sum(-1))
+    if ids is not None:
+        ok = (ids >= 0) & (ids < z.shape[1])
+        out["logp"] = np.where(ok, np.take_along_axis(lp, np.where(ok, ids, 0).astype(np.int64), 1), 0.0)
+    if k:
+        order = np.argsort(-z, axis=-1, kind="stable")[:, :k]
+        there = np.take_along_axis(z, order, 1) > -np.inf
+        out["top_ids"] = np.where(there, order, -1)
+        out["top_logp"] = np.where(there, np.take_along_axis(lp, order, 1), -np.inf)
+    return out
+
+
+def _check(got, z, ids, k, zerr=0.0, what=""):
+    """An element enters the sums by three roundings and the exponential's ulp; a frame's rounding is taken off to
+    2^-26; at most 128 sequential additions and 32 of trees and chunks: as the tests near 0, and not in terms of |z|.
+    Only lse itself is a number of the size of z: one rounding of it, and one of the largest logit plus its log sum.
+    zerr: how well the logits are known."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        r = _ref(z, ids, k)
+        rel = (160 + 8 + 4 + 2 * r["spread"]) * H32 + 2 * zerr
+        lse, ent = from_dev(got["lse"]).astype(np.float64), from_dev(got["entropy"]).astype(np.float64)
+        assert np.all(np.isneginf(lse[r["none"]])) and np.all(ent[r["none"]] == 0.0), what
+        live = ~r["none"]
+        t = rel + 4 * H32 * np.abs(r["ls"]) + 2 * H32 * np.abs(r["lse"])
+        bad = live & ~(np.abs(lse - r["lse"]) <= t)
+        assert not bad.any(), (what, "lse", np.nonzero(bad)[0][:8], lse[bad][:8], r["lse"][bad][:8])
+        t = rel * (1 + 2 * r["spread"]) + 4 * H32 * (r["spread"] + r["entropy"] + 1)
+        bad = live & ~(np.abs(ent - r["entropy"]) <= t)
+        assert not bad.any(), (what, "entropy", np.nonzero(bad)[0][:8], ent[bad][:8], r["entropy"][bad][:8])
+        for n in ("logp", "top_logp"):
+            if n not in r:
+                continue
+            x, y = from_dev(got[n]).astype(np.float64), r[n]
+            y32 = y.astype(np.float32)
+            inf = np.isinf(y32)
+            assert np.array_equal(x[inf], y32[inf].astype(np.float64)), (what, n)
+            t = (rel + 4 * H32 * np.abs(r["ls"]))[:, None] + 3 * H32 * np.abs(np.where(inf, 0.0, y))
+            bad = ~inf & ~(np.abs(x - y) <= t)
+            assert not bad.any() and np.all(x <= 0.0), (what, n, np.argwhere(bad)[:6], x[bad][:6], y[bad][:6])
+        if k:
+            assert np.array_equal(from_dev(got["top_ids"]), r["top_ids"]), (what, "ids")
+    return r
+
+
+SIZES = (1e4, 1e5, 1e7, 1e9, 1e10, 1e12, 1e15, 1e18, 1e20, 1e25, 1e30, 1e35, 1e37, LOWEST)
+
+
+def _masked(size, V, rng):
+    """Rows masked by -size: all but a stretch, all but the last entry, half of them, all; rows about +size, and a few
+    entries there."""
+    z = np.full((7, V), -size)
+    z[0, V // 2:V // 2 + 7] = rng.standard_normal(7)
+    z[1, V - 1] = 1.0
+    keep = rng.random(V) < 0.5
+    z[2, keep] = rng.standard_normal(keep.sum())
+    z[4] = size
+    z[5] = rng.standard_normal(V) * 2
+    z[5, rng.choice(V, 9, replace=False)] = size
+    z[6, V // 3:] = -np.inf
+    return z
+
+
+@pytest.mark.parametrize("V", [300, 5000, 40001])
+@pytest.mark.parametrize("many", [False, True])
+def test_logits_masked_by_finite_values(V, many):
+    """Masks of any size over whole chunks beside live ones, and over whole rows; long chunks and short ones."""
+    rng = np.random.default_rng(V + 11)
+    z = np.concatenate([_masked(s, V, rng) for s in SIZES])
+    z = _bf(np.tile(z, (6 if many else 1, 1)))
+    n = 256 if many else 25                                          # 25 rows of 40001 are short chunks
+    ids = np.stack([np.zeros(len(z)), np.full(len(z), V // 2), np.full(len(z), V - 1)], 1).astype(np.int32)
+    for r in range(0, len(z), n):
+        _check(_logits_fwd(z[r:r + n], ids[r:r + n], 20), z[r:r + n], ids[r:r + n], 20, what=(V, r))
