@@ -365,7 +365,9 @@ __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
             s += red[0][i];
             u += red[1][i];
         }
-        a.part[t * a.nc + c] = make_float4(M, __builtin_fmaf(-d * LN2, s, s), LN2 * __builtin_fmaf(-d, s, u), 0.0f);
+        // terms 2^(l + d') and their l: both sums times 2^-d, and the second's frame moved by d
+        const float g = __builtin_fmaf(-d, LN2, 1.0f);
+        a.part[t * a.nc + c] = make_float4(M, g * s, g * LN2 * __builtin_fmaf(-d, s, u), 0.0f);
     }
     if (a.k > 0) {
         const uint32_t r = bound;

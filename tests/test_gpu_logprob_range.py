@@ -107,3 +107,24 @@ def test_logits_masked_by_finite_values(V, many):
     ids = np.stack([np.zeros(len(z)), np.full(len(z), V // 2), np.full(len(z), V - 1)], 1).astype(np.int32)
     for r in range(0, len(z), n):
         _check(_logits_fwd(z[r:r + n], ids[r:r + n], 20), z[r:r + n], ids[r:r + n], 20, what=(V, r))
+
+
+def _offset(T, H, V, m, base, seed=0):
+    """Hidden states and weight whose logits stand about `base`, exact in fp32 (steps of 2^-12, below 2^12)."""
+    h, w, ids, _ = _hidden(T + V + seed, T, H, V, m, spread=2.0 ** -12 * 1024 * np.sqrt(H))
+    h[:, -1] = 32.0
+    w[:, -1] = _bf(base / 32.0)
+    z = h.astype(np.float64) @ w.astype(np.float64).T
+    assert np.abs(z).max() < 4096 and np.array_equal(z * 4096, np.rint(z * 4096))
+    return h, w, ids, z
+
+
+BASES = (-3500.0, -1000.0, 500.0, 1500.0, 2500.0, 3000.0, 3500.0)
+
+
+@pytest.mark.parametrize("T", [1, 5, 20])
+@pytest.mark.parametrize("base", BASES)
+def test_hidden_states_of_a_few_tokens_with_logits_far_from_0(T, base):
+    """The frame's rounding is up to 2^-12 here: it is taken off both sums, the entropy's too."""
+    h, w, ids, z = _offset(T, 64, 9001, 2, base)
+    _check(_head_fwd(h, w, ids, 20), z, ids, 20, what=(T, base))
