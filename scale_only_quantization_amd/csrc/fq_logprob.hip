@@ -1104,8 +1104,8 @@ __global__ __launch_bounds__(64 * WPT * TOK) __attribute__((amdgpu_waves_per_eu(
     }
     join(before.x, before.y, before.z);
     const float ls = logf(s), lse = M + ls;
-    auto logp = [&](float z) {
-        const float q = z - lse;
+    auto logp = [&](float z) {                             // z - M first: lse may be far from 0
+        const float q = z - M - ls;
         return q > 0.0f ? 0.0f : q;
     };
     if (live && a.last && sub == 0) {
