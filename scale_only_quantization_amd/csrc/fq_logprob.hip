@@ -843,8 +843,8 @@ __global__ __launch_bounds__(FEW_TPB) void k_head_few(HeadLogpArgs a) {
 }
 
 // The tile product of the output layer's loss with other epilogues.
-//   SUMS  of each token's 64 columns of a wave: the maximum m, s = sum 2^x with
-//         x = z log2 e - m log2 e, and with ENT u = sum 2^x x
+//   SUMS  of each token's 64 columns of a wave: the maximum m, s = sum e^(z - m), and
+//         with ENT u = sum e^(z - m) (z - m)
 //   TOP   these, and the 64 logits themselves where m is above the token's bound,
 //         the k-th best logit of the pieces before: of a long row that is seldom
 //   GRAD  P = -p (A + b (log p + entropy)) in bf16
@@ -941,18 +941,31 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
                             }
                     }
                 }
-                const float f = m * LOG2E;
+                // far from 0 the distance to m comes first (always so: 16384 tokens 8140 -> 8240 us)
+                const bool far = __any(fabsf(m) >= FAR);
+                const float f = m * LOG2E, d = far ? 0.0f : __builtin_fmaf(m, LOG2E, -f);
                 float s = 0.0f, u = 0.0f;
+                auto add = [&](float x) {
+                    const float e = exp2_hw(x);
+                    s += e;
+                    if (ENT) u = __builtin_fmaf(e, x, u);
+                };
+                if (far) {
 #pragma unroll
-                for (int tj = 0; tj < WTN; ++tj)
+                    for (int tj = 0; tj < WTN; ++tj)
 #pragma unroll
-                    for (int v = 0; v < 16; ++v) {
-                        const float x = __builtin_fmaf(acc[ti][tj][v], LOG2E, -f), e = exp2_hw(x);
-                        s += e;
-                        if (ENT) u = __builtin_fmaf(e, x, u);
-                    }
+                        for (int v = 0; v < 16; ++v) add((acc[ti][tj][v] - m) * LOG2E);
+                } else {
+#pragma unroll
+                    for (int tj = 0; tj < WTN; ++tj)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v) add(__builtin_fmaf(acc[ti][tj][v], LOG2E, -f));
+                }
                 s += xor32(s);
                 if (ENT) u += xor32(u);
+                const float g = __builtin_fmaf(-d, LN2, 1.0f);                        // as in a chunk of rows
+                if (ENT) u = g * LN2 * __builtin_fmaf(-d, s, u);
+                s *= g;
                 const int64_t o = ((int64_t)tn * 4 + wn) * a.T + m0 + row;
                 if (lane < 32 && row < rows) {
                     a.stats[o] = make_float2(m, s);
@@ -1008,8 +1021,6 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
 // waves per token over the strips that can hold an alternative.  A wave's best are
 // its lanes' keys in descending order; logits above the k-th are gathered in LDS
 // and put in 64 at a time by a sort and a merge, the last few one at a time.
-// Sums are joined in frames of z itself: a strip's base-2 frame, m log2 e rounded,
-// is known exactly with its rounding d, and s and u are brought from it to m.
 constexpr int MWORDS = LOGP_MAX_PIECE / 64 / 32, MLIST = 16, MPARTS = 256;
 template <int WPT, int TOK>
 __global__ __launch_bounds__(64 * WPT * TOK) __attribute__((amdgpu_waves_per_eu(8))) void k_logp_merge(HeadLogpArgs a) {
@@ -1073,9 +1084,9 @@ __global__ __launch_bounds__(64 * WPT * TOK) __attribute__((amdgpu_waves_per_eu(
         for (int j = 0; j < UN; ++j) {
             const int i = i0 + PER * j;
             if (i >= strips) break;
-            const float m = v[j].x, d = __builtin_fmaf(m, LOG2E, -(m * LOG2E));
+            const float m = v[j].x;
             tm[j % SUB] = fmaxf(tm[j % SUB], m);
-            join(m, __builtin_fmaf(-d * LN2, v[j].y, v[j].y), LN2 * __builtin_fmaf(-d, v[j].y, vu[j]));
+            join(m, v[j].y, vu[j]);
             if (top && m > thr) atomicOr(&flag[tok][i >> 5], 1u << (i & 31));
         }
     }

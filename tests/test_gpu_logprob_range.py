@@ -136,3 +136,56 @@ def test_log_probabilities_of_hidden_states_with_logits_far_from_0(T, base):
     """They are as exact as near 0, where lse is rounded by 2^-13."""
     h, w, ids, z = _offset(T, 64, 9001, 2, base)
     _check(_head_fwd(h, w, ids, 20), z, ids, 20, what=(T, base), sums=False)
+
+
+def _kinds(H, V, size, seed):
+    """12 hidden states and a weight whose logits are exact: general ones; the same with two thirds of the vocabulary, in
+    one piece and scattered, masked by -size; every logit -size; every logit +size; the first half -size, 0 beyond; +size
+    at 9 entries, 0 elsewhere."""
+    h, w, _, _ = _hidden(seed, 12, H, V, 0)
+    rng = np.random.default_rng(seed)
+    w[:, :4] = 0.0
+    h[:, :4] = 0.0
+    masked = np.arange(V) < V // 2
+    masked[V // 2:] = rng.random(V - V // 2) < 0.3
+    w[masked] = 0.0                                       # so that -size is not rounded with what is left
+    w[masked, 0] = -size
+    w[:, 1] = size
+    w[:V // 2, 2] = -size
+    w[rng.choice(V, 9, replace=False), 3] = size
+    h[2:4, 0] = 1.0
+    h[4:] = 0.0
+    h[4:6, 1], h[6:8, 1], h[8:10, 2], h[10:, 3] = -1.0, 1.0, 1.0, 1.0
+    w = _bf(w)
+    return h, w, h.astype(np.float64) @ w.astype(np.float64).T
+
+
+def _tiled(T, h, w, z, k, what):
+    """The rows of h repeated to T: the first ones against the definitions, the others equal to them."""
+    n = len(h)
+    ids = np.stack([np.arange(n) * 7, z.shape[1] - 1 - np.arange(n)], 1).astype(np.int32)
+    tile = lambda x: np.concatenate([np.tile(x, (T // n,) + (1,) * (x.ndim - 1)), x[:T % n]])  # noqa: E731
+    got = _head_fwd(tile(h), w, tile(ids), k)
+    _check({name: None if v is None else v[:n] for name, v in got.items()}, z, ids, k, what=what)
+    for name, v in got.items():
+        if v is not None:
+            x = from_dev(v)
+            assert np.array_equal(x, tile(x[:n])), (what, name)
+
+
+@pytest.mark.parametrize("T", [12, 72, 300, 4104])
+@pytest.mark.parametrize("V", [1000, 20001])
+@pytest.mark.parametrize("size", [1e4, 1e7, 1e9, 1e10, 1e15, 1e20, 1e29])
+def test_hidden_states_masked_by_finite_values(T, V, size):
+    """Whole strips and whole rows of masks, in every form (few tokens, one and two waves a token)."""
+    h, w, z = _kinds(128, V, size, V)
+    _tiled(T, h, w, z, 20, (T, V, size))
+    if T > 12:
+        _tiled(T, h, w, z, 0, (T, V, size, "no alternatives"))
+
+
+@pytest.mark.parametrize("T", [72, 300])
+@pytest.mark.parametrize("base", BASES)
+def test_sums_of_hidden_states_with_logits_far_from_0(T, base):
+    h, w, ids, z = _offset(T, 64, 9001, 2, base)
+    _check(_head_fwd(h, w, ids, 20), z, ids, 20, what=(T, base))
