@@ -943,18 +943,19 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
                 }
                 // far from 0 the distance to m comes first (always so: 16384 tokens 8140 -> 8240 us)
                 const bool far = __any(fabsf(m) >= FAR);
-                const float f = m * LOG2E, d = far ? 0.0f : __builtin_fmaf(m, LOG2E, -f);
+                const float mf = m == -INFINITY ? 0.0f : m;                           // a strip of nothing but -inf has s = 0
+                const float f = mf * LOG2E, d = far ? 0.0f : __builtin_fmaf(mf, LOG2E, -f);
                 float s = 0.0f, u = 0.0f;
                 auto add = [&](float x) {
                     const float e = exp2_hw(x);
                     s += e;
-                    if (ENT) u = __builtin_fmaf(e, x, u);
+                    if (ENT) u = __builtin_fmaf(e, fmaxf(x, FLOOR2), u);
                 };
                 if (far) {
 #pragma unroll
                     for (int tj = 0; tj < WTN; ++tj)
 #pragma unroll
-                        for (int v = 0; v < 16; ++v) add((acc[ti][tj][v] - m) * LOG2E);
+                        for (int v = 0; v < 16; ++v) add((acc[ti][tj][v] - mf) * LOG2E);
                 } else {
 #pragma unroll
                     for (int tj = 0; tj < WTN; ++tj)
@@ -1114,15 +1115,16 @@ __global__ __launch_bounds__(64 * WPT * TOK) __attribute__((amdgpu_waves_per_eu(
         join(m2, s2, u2);
     }
     join(before.x, before.y, before.z);
-    const float ls = logf(s), lse = M + ls;
+    const bool none = M == -INFINITY && s == 0.0f;         // every logit is -inf
+    const float ls = logf(s), lse = none ? -INFINITY : M + ls;
     auto logp = [&](float z) {                             // z - M first: lse may be far from 0
-        const float q = z - M - ls;
+        const float q = none ? -INFINITY : z - M - ls;
         return q > 0.0f ? 0.0f : q;
     };
     if (live && a.last && sub == 0) {
         if (lane == 0) {
             if (a.lse) a.lse[t] = lse;
-            if (ent) a.entropy[t] = ls - u / s;
+            if (ent) a.entropy[t] = none ? 0.0f : ls - u / s;
         }
     }
     if (live && a.last)

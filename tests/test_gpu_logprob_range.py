@@ -189,3 +189,23 @@ def test_hidden_states_masked_by_finite_values(T, V, size):
 def test_sums_of_hidden_states_with_logits_far_from_0(T, base):
     h, w, ids, z = _offset(T, 64, 9001, 2, base)
     _check(_head_fwd(h, w, ids, 20), z, ids, 20, what=(T, base))
+
+
+@pytest.mark.parametrize("T", [12, 72, 300, 4104])
+@pytest.mark.parametrize("V", [1024, 20480])
+@pytest.mark.parametrize("how", ["some", "strips", "all but one", "all"])
+def test_hidden_states_with_ruled_out_entries(T, V, how):
+    """Logits of -inf (a weight of -inf where every hidden state is 1): in the midst of others, over whole strips and
+    pieces, all but one, all."""
+    h, w, _, z = _hidden(V, 12, 512, V, 0)
+    rng = np.random.default_rng(V)
+    out = dict(some=rng.random(V) < 0.3, strips=np.arange(V) // 200 % 2 == 0)
+    out["all"] = np.ones(V, bool)
+    out["all but one"] = np.arange(V) != V - 2
+    h[:, 7], w[:, 7] = 1.0, 0.0
+    z = h.astype(np.float64) @ w.astype(np.float64).T
+    w[out[how], 7] = -np.inf
+    z[:, out[how]] = -np.inf
+    _tiled(T, h, w, z, 20, (T, V, how))
+    if T > 12:
+        _tiled(T, h, w, z, 0, (T, V, how, "no alternatives"))
