@@ -48,7 +48,6 @@ constexpr float FLOOR2 = -300.0f;         // and 2^FLOOR2
 // good as fp32 while (d ln 2)^2 / 2 is below half an ulp: d <= 2^-12, |M| < 2^12.
 constexpr float FAR = 0x1p12f;
 constexpr float MASKS = -0x1p125f;        // a row whose lse is below it has nothing but masks of the type's lowest value
-constexpr float PAST = -1e30f;            // a column past the vocabulary: below what a sum can hold, and finite
 
 // The order of a logit as a whole number: 0 is below all of them.
 __device__ __forceinline__ uint32_t order_of(float z) {
@@ -916,7 +915,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
                 }
             };
             if constexpr (MODE != GRAD) {
-                past(PAST);
+                past(-INFINITY);
                 float m = acc[ti][0][0];
 #pragma unroll
                 for (int tj = 0; tj < WTN; ++tj)

@@ -209,3 +209,16 @@ def test_hidden_states_with_ruled_out_entries(T, V, how):
     _tiled(T, h, w, z, 20, (T, V, how))
     if T > 12:
         _tiled(T, h, w, z, 0, (T, V, how, "no alternatives"))
+
+
+@pytest.mark.parametrize("T", [72, 300])
+@pytest.mark.parametrize("V", [1000, 20001, 65])
+@pytest.mark.parametrize("size", [1e30, 1e32, LOWEST, np.inf])
+def test_columns_past_the_vocabulary_are_below_every_logit(T, V, size):
+    """A vocabulary that ends inside a strip, with rows of nothing but large masks or ruled-out entries."""
+    h, w, z = _kinds(128, V, 1.0 if np.isinf(size) else size, V)
+    if np.isinf(size):
+        h[:, 7], w[:, 7] = 1.0, -np.inf
+        z = np.full_like(z, -np.inf)
+    _tiled(T, h, w, z, 20, (T, V, size))
+    _tiled(T, h, w, z, 0, (T, V, size, "no alternatives"))
