@@ -702,7 +702,7 @@ __global__ __launch_bounds__(ROW_TPB) void k_head_rows(HeadLogpArgs a) {
     auto multiply = [&](const u32x4 (&v)[ROW_GO][ROW_N]) {
 #pragma unroll
         for (int j = 0; j < ROW_GO; ++j) {
-            if (c + j >= chunks) break;
+            if ((c + j) * 512 + lane * 8 >= H) break;              // (past the row the weight's may be infinite)
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
                 const u32x4 x = *reinterpret_cast<const u32x4*>(sh + t * Hp + (c + j) * 512 + lane * 8);

@@ -222,3 +222,17 @@ def test_columns_past_the_vocabulary_are_below_every_logit(T, V, size):
         z = np.full_like(z, -np.inf)
     _tiled(T, h, w, z, 20, (T, V, size))
     _tiled(T, h, w, z, 0, (T, V, size, "no alternatives"))
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 8, 12])
+@pytest.mark.parametrize("H", [64, 320, 576])
+def test_ruled_out_entries_of_rows_that_end_inside_512_columns(T, H):
+    """A weight of -inf in a row's first columns, which stand in for those past its end."""
+    h, w, _, _ = _hidden(T, T, H, 3001, 0)
+    h[:, 2], w[:, 2] = 1.0, 0.0
+    z = h.astype(np.float64) @ w.astype(np.float64).T
+    out = np.random.default_rng(T).random(3001) < 0.5
+    w[out, 2] = -np.inf
+    z[:, out] = -np.inf
+    ids = np.arange(T, dtype=np.int32)[:, None]
+    _check(_head_fwd(h, w, ids, 20), z, ids, 20, what=(T, H))
