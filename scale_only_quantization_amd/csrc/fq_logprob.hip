@@ -47,7 +47,10 @@ constexpr float FLOOR2 = -300.0f;         // and 2^FLOOR2
 // and the largest entry enters the sum as 2^d.  A correction to first order is as
 // good as fp32 while (d ln 2)^2 / 2 is below half an ulp: d <= 2^-12, |M| < 2^12.
 constexpr float FAR = 0x1p12f;
-constexpr float MASKS = -0x1p125f;        // a row whose lse is below it has nothing but masks of the type's lowest value
+// A row whose lse is below it has nothing but masks: in the gradients p = e^(z - lse),
+// and an fp32 number of that size no longer holds the log of their number beside
+// them (each would have p = 1).
+constexpr float MASKS = -0x1p20f;
 
 // The order of a logit as a whole number: 0 is below all of them.
 __device__ __forceinline__ uint32_t order_of(float z) {

@@ -236,3 +236,54 @@ def test_ruled_out_entries_of_rows_that_end_inside_512_columns(T, H):
     z[:, out] = -np.inf
     ids = np.arange(T, dtype=np.int32)[:, None]
     _check(_head_fwd(h, w, ids, 20), z, ids, 20, what=(T, H))
+
+
+def _grad_ref(z, ids, dl, de):
+    """d L / d z, p and the size of what p is multiplied by, from the distance to the largest logit; rows below -2^20 have
+    gradient 0."""
+    r = _ref(z, None, 0)
+    T, V = z.shape
+    live = (r["lse"] > -2.0 ** 20)[:, None]
+    p = np.where(live, r["p"], 0.0)
+    lp = np.where(p > 0, r["lp"], 0.0)
+    g, A, size = np.zeros((T, V)), np.zeros(T), np.zeros(T)
+    if dl is not None:
+        for t in range(T):
+            for i, a in zip(ids[t], dl[t].astype(np.float64)):
+                if 0 <= i < V and live[t]:
+                    A[t] += a
+                    size[t] += abs(a)
+                    g[t, i] += a
+    f, a = np.broadcast_to(A[:, None], (T, V)), np.broadcast_to(size[:, None], (T, V))
+    if de is not None:
+        b, H = de.astype(np.float64)[:, None], r["entropy"][:, None]
+        f, a = f + b * (lp + H), a + np.abs(b) * (np.abs(lp) + H + 1)
+    with np.errstate(invalid="ignore"):
+        err = np.where(live[:, 0], np.abs(r["lse"]), 0.0)[:, None] * 2 * H32    # of log p, in lse
+        # log p: also its own rounding and the product with log2 e; what p is multiplied by: an error like log p's and sums
+        perr = np.expm1(err + (3 * np.abs(lp) + 16) * H32)
+    return r, g - p * f, p, p * a * 3 * perr + 2.0 ** -126 * 30 * a
+
+
+@pytest.mark.parametrize("V", [300, 20001])
+@pytest.mark.parametrize("m,ent", [(0, True), (1, False), (2, True)])
+def test_logits_gradient_masked_by_finite_values(V, m, ent):
+    """Masks of any size beside live entries, and rows of nothing else, through forward and backward."""
+    F, T_ = _F(), torch()
+    rng = np.random.default_rng(V + m)
+    z = _bf(np.concatenate([_masked(s, V, rng)[[0, 1, 2, 3]] for s in SIZES]))
+    T = len(z)
+    ids = rng.integers(0, V, (T, m)).astype(np.int32)
+    dl, de = rng.standard_normal((T, m)).astype(np.float32), rng.standard_normal(T).astype(np.float32)
+    fwd = _logits_fwd(z, None, 0)
+    grad = T_.full((T, (V + 7) // 8 * 8), 9.0, dtype=T_.bfloat16, device="cuda")[:, :V]
+    F.logprob_bwd(F.logprob_desc(T, V, given=m), _padded(z, 0, 0.0)[1], fwd["lse"], grad, ids=to_dev(ids) if m else None,
+                  dlogp=to_dev(dl) if m else None, entropy=fwd["entropy"] if ent else None,
+                  dentropy=to_dev(de) if ent else None)
+    T_.cuda.synchronize()
+    got = from_dev(grad).astype(np.float64)
+    _, ref, _, tol = _grad_ref(z.astype(np.float64), ids, dl if m else None, de if ent else None)
+    bad = ~(np.abs(got - ref) <= H16 * np.abs(ref) * 1.001 + tol)
+    assert not bad.any(), (np.argwhere(bad)[:6], got[bad][:6], ref[bad][:6])
+    whole = np.arange(T) % 4 == 3
+    assert np.all(got[whole & (np.repeat(SIZES, 4) > 2.0 ** 20)] == 0.0)
