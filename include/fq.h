@@ -504,10 +504,11 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
  * two ids whose logits differ by less than its error may change places; in the
  * gradient's product dL/dz is rounded to bf16, except the given tokens', which
  * are added in fp32.  The gradient's p = e^(z - lse) is as good as lse, rounded to
- * fp32: relative errors up to e^(|lse| 2^-24) - 1 for |lse| <= 2^20.  From logits, a
+ * fp32: relative errors up to e^(|lse| 2^-24) - 1 for |lse| <= 2^20.  A
  * row whose lse is below -2^20 is taken as one of nothing but (finite) masks and has
  * gradient 0.  Above 2^20 lse does not hold the log of a number of equal logits: each
- * of n that share the largest place has p = 1. */
+ * of n that share the largest place has p = 1.  From hidden states the gradient takes
+ * finite weights (0 times an infinite one is NaN). */
 typedef struct {
     int64_t tokens;            /* rows, >= 0, < 2^24                                  */
     int64_t hidden;            /* fq_head_logprob_*: a multiple of 64, 64 .. 16384; fq_logprob_*: 0 */

@@ -844,6 +844,12 @@ __global__ __launch_bounds__(FEW_TPB) void k_head_few(HeadLogpArgs a) {
     }
 }
 
+// log2 p of a logit, the distance first: of logits far from 0 a frame in base 2 is
+// rounded by more than lse is.  At most 0, as lse may come from sums in another order.
+__device__ __forceinline__ float log2_p(float z, float lse) {
+    return __builtin_amdgcn_fmed3f((z - lse) * LOG2E, FLOOR2, 0.0f);
+}
+
 // The tile product of the output layer's loss with other epilogues.
 //   SUMS  of each token's 64 columns of a wave: the maximum m, s = sum e^(z - m), and
 //         with ENT u = sum e^(z - m) (z - m)
@@ -979,12 +985,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
                                                              (int64_t)(rows - 1) * a.vc * 2 + BN * 2);
                 const __attribute__((address_space(3))) float4* rc =
                     reinterpret_cast<const __attribute__((address_space(3))) float4*>(consts);
-                const float f = rc[row].x, c = rc[row].y, b = rc[row].z * LN2;
+                const float lse = rc[row].x, c = rc[row].y, b = rc[row].z * LN2;
 #pragma unroll
                 for (int tj = 0; tj < WTN; ++tj)
 #pragma unroll
                     for (int v = 0; v < 16; ++v) {
-                        const float l = fmaxf(__builtin_fmaf(acc[ti][tj][v], LOG2E, -f), FLOOR2);   // log2 p
+                        const float l = log2_p(acc[ti][tj][v], lse);
                         acc[ti][tj][v] = -exp2_hw(l) * __builtin_fmaf(b, l, c);
                     }
                 past(0.0f);
@@ -1275,8 +1281,9 @@ __global__ __launch_bounds__(256) void k_logp_rowc(HeadLogpArgs a) {
         const float b = a.dent ? a.dent[t] : 0.0f, H = a.dent ? a.entropy[t] : 0.0f;
         if (lane == 0) {
             const float lse = a.lse[t];                            // (a NaN: the row's gradient is one)
-            a.rowc[t] = make_float4(lse * LOG2E, lse == lse ? __builtin_fmaf(b, H, A) : lse, b,
-                                    __int_as_float(a.m == 1 && in ? id : -1));
+            const float4 rc = lse <= MASKS ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                           : make_float4(lse, lse == lse ? __builtin_fmaf(b, H, A) : lse, b, 0.0f);
+            a.rowc[t] = make_float4(rc.x, rc.y, rc.z, __int_as_float(a.m == 1 && in ? id : -1));
             a.ones[t] = 1.0f;
         }
     }
@@ -1311,9 +1318,9 @@ __global__ __launch_bounds__(256) void k_logp_out(HeadLogpArgs a, int splits) {
         bool first = in;
         for (int l = 0; l < j; ++l) first &= a.ids[t * a.m + l] != id;
         const float4 rc = a.rowc[t];
-        const float l = __builtin_fmaf(a.zs[t * a.m + j], LOG2E, -rc.x);
+        const float l = log2_p(a.zs[t * a.m + j], rc.x);
         sid[j] = in ? id : 0;
-        scoef[j] = in ? a.dlogp[t * a.m + j] - (first ? exp2_hw(l) * __builtin_fmaf(rc.z * LN2, l, rc.y) : 0.0f) : 0.0f;
+        scoef[j] = in && !(a.lse[t] <= MASKS) ? a.dlogp[t * a.m + j] - (first ? exp2_hw(l) * __builtin_fmaf(rc.z * LN2, l, rc.y) : 0.0f) : 0.0f;
     }
     __syncthreads();
     typedef uint32_t words __attribute__((ext_vector_type(VEC / 2)));

@@ -150,7 +150,7 @@ struct HeadLogpArgs {
     float2* stats;         // forward [vc / 64, T]: maximum and s of each strip
     float* ustats;         // forward [vc / 64, T], with the entropy: u
     float* z;              // forward [T, vc], with k: logits of a piece's strips above thr
-    float4* rowc;          // backward [T]: lse log2 e, A + b (entropy), b
+    float4* rowc;          // backward [T]: lse, A + b entropy, b (0 of a row of masks); the bits of the one given id or of -1
     uint16_t* p;           // backward [T, vc]
     float* g;              // backward [splits, T, H]
     float* ones;           // backward [T]

@@ -259,7 +259,8 @@ def _grad_ref(z, ids, dl, de):
         b, H = de.astype(np.float64)[:, None], r["entropy"][:, None]
         f, a = f + b * (lp + H), a + np.abs(b) * (np.abs(lp) + H + 1)
     with np.errstate(invalid="ignore"):
-        err = np.where(live[:, 0], np.abs(r["lse"]), 0.0)[:, None] * 2 * H32    # of log p, in lse
+        # of log p, in lse; past 2^20 entries are the largest or far below it
+        err = np.where(np.abs(r["lse"]) <= 2.0 ** 20, np.abs(r["lse"]), 0.0)[:, None] * 2 * H32
         # log p: also its own rounding and the product with log2 e; what p is multiplied by: an error like log p's and sums
         perr = np.expm1(err + (3 * np.abs(lp) + 16) * H32)
     return r, g - p * f, p, p * a * 3 * perr + 2.0 ** -126 * 30 * a
@@ -287,3 +288,80 @@ def test_logits_gradient_masked_by_finite_values(V, m, ent):
     assert not bad.any(), (np.argwhere(bad)[:6], got[bad][:6], ref[bad][:6])
     whole = np.arange(T) % 4 == 3
     assert np.all(got[whole & (np.repeat(SIZES, 4) > 2.0 ** 20)] == 0.0)
+
+
+def _head_grad_check(h, w, z, ids, T, what):
+    """The gradient of the rows of h, repeated to T, from their forward's lse and entropy; z exact."""
+    F, T_ = _F(), torch()
+    n, V, H, m = len(h), z.shape[1], h.shape[1], ids.shape[1]
+    rng = np.random.default_rng(T + V)
+    dl, de = rng.standard_normal((n, m)).astype(np.float32), rng.standard_normal(n).astype(np.float32)
+    tile = lambda x: np.concatenate([np.tile(x, (T // n, 1)), x[:T % n]])  # noqa: E731
+    fwd = _head_fwd(tile(h), w, None, 0)
+    d = F.logprob_desc(T, V, given=m, hidden=H)
+    g = T_.full((T, H), 9.0, dtype=T_.bfloat16, device="cuda")
+    F.head_logprob_bwd(d, to_dev_bf16(tile(h)), to_dev_bf16(w), fwd["lse"], g, ids=to_dev(tile(ids)),
+                       dlogp=to_dev(tile(dl)), entropy=fwd["entropy"], dentropy=to_dev(tile(de[:, None])[:, 0]),
+                       workspace=_workspace(F.head_logprob_workspace_size(d, True)))
+    T_.cuda.synchronize()
+    got = from_dev(g)
+    assert np.array_equal(got, tile(got[:n])), what
+    got = got[:n].astype(np.float64)
+    _, dz, p, tol = _grad_ref(z, ids, dl, de)
+    aw = np.abs(w.astype(np.float64))
+    ref = dz @ w.astype(np.float64)
+    given = np.zeros(z.shape, bool)
+    for t in range(n):
+        given[t, ids[t][(ids[t] >= 0) & (ids[t] < V)]] = True
+    part = np.where(p > 0, np.abs(dz), 0.0)
+    # the result's rounding, that of dL/dz beside the given tokens, and fp32 sums
+    tol = (H16 * (np.abs(ref) + np.where(given, 0.0, part) @ aw) * 1.001 + tol @ aw + (V / 64 + 64) * H32 * (np.abs(dz) @ aw)
+           + (V / 64 + 64) * H32 * (p @ aw) * np.abs(dl).sum(-1, keepdims=True))
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), (what, np.argwhere(bad)[:6], got[bad][:6], ref[bad][:6], tol[bad][:6])
+    return got
+
+
+@pytest.mark.parametrize("T", [12, 300])
+@pytest.mark.parametrize("m", [1, 3])
+@pytest.mark.parametrize("size", [1e4, 1e7, 1e9, 1e10, 1e20, 1e30, 1e37])
+def test_hidden_states_gradient_masked_by_finite_values(T, m, size):
+    """Masked entries beside live ones, rows of nothing but masks, and one entry far above all others."""
+    h, w, z = _kinds(128, 5003, size, 3)
+    one = int(np.argmax(w[:, 3]))
+    w[:, 3] = 0.0
+    w[one, 3] = _bf(size)
+    h[6:8], z = h[10:], None                                         # (no row of equal logits past 2^20)
+    z = h.astype(np.float64) @ w.astype(np.float64).T
+    rng = np.random.default_rng(m)
+    ids = rng.integers(0, 5003, (12, m)).astype(np.int32)
+    ids[6, 0] = one
+    got = _head_grad_check(h, w, z, ids, T, (T, m, size))
+    if size > 2.0 ** 20:
+        assert np.all(got[4:6] == 0.0)
+
+
+@pytest.mark.parametrize("T", [12, 300])
+@pytest.mark.parametrize("m", [1, 3])
+@pytest.mark.parametrize("base", [-3500.0, -1000.0, 1500.0, 3500.0])
+def test_hidden_states_gradient_far_from_0(T, m, base):
+    h, w, ids, z = _offset(12, 64, 5003, m, base)
+    _head_grad_check(h, w, z, ids, T, (T, m, base))
+
+
+@pytest.mark.parametrize("m", [1, 2])
+def test_hidden_states_gradient_of_logits_past_fp32(m):
+    """Finite hidden states and weights whose logits are -inf in fp32: some of a row, a given one among them (p = 0), and
+    all of a row (gradient 0)."""
+    h, w, _, _ = _hidden(4, 12, 128, 2000, 0)
+    h[:, 0], h[8:] = 2.0 ** 100, 0.0
+    h[8:, 1] = 2.0 ** 100
+    w[:, 0] = np.where(np.arange(2000) % 3 == 0, -2.0 ** 60, 0.0)
+    w[:, 1] = -2.0 ** 60
+    h[:8, 1] = 0.0
+    z = h.astype(np.float64) @ w.astype(np.float64).T
+    z = np.where(z < -1e39, -np.inf, z)
+    ids = np.tile(np.array([[3, 4][:m]], np.int32), (12, 1))
+    got = _head_grad_check(h, w, z, ids, 12, m)
+    assert np.all(got[8:] == 0.0)
+    _head_grad_check(h, w, z, ids, 300, m)
