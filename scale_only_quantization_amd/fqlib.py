@@ -589,7 +589,8 @@ class GradList:
 
     def __init__(self, grads, outs=None):
         n = "grad_list"
-        self.grads, self.outs = list(grads), list(grads if outs is None else outs)
+        self.grads = list(grads)                                        # once: a generator is used up by it
+        self.outs = list(self.grads if outs is None else outs)
         if len(self.grads) != len(self.outs):
             raise ValueError(f"{n}: {len(self.grads)} gradients and {len(self.outs)} outputs")
         self.device = _device_of(n, self.grads[0]) if self.grads else None
