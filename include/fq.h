@@ -501,14 +501,15 @@ int fq_head_loss(const fq_head_desc* d, const void* h, const void* w, const floa
  *     dL/dz_v = sum_j a_j [v = id_j] - p_v (A + b (log p_v + entropy))
  *     dL/dh = sum_v dL/dz_v w_v
  * Sums are fp32; bitwise deterministic.  From hidden states z is an fp32 sum, so
- * two ids whose logits differ by less than its error may change places; in the
- * gradient's product dL/dz is rounded to bf16, except the given tokens', which
- * are added in fp32.  The gradient's p = e^(z - lse) is as good as lse, rounded to
- * fp32: relative errors up to e^(|lse| 2^-24) - 1 for |lse| <= 2^20.  A
- * row whose lse is below -2^20 is taken as one of nothing but (finite) masks and has
- * gradient 0.  Above 2^20 lse does not hold the log of a number of equal logits: each
- * of n that share the largest place has p = 1.  From hidden states the gradient takes
- * finite weights (0 times an infinite one is NaN). */
+ * two ids whose logits differ by less than its error may change places, and a given
+ * token's logit may be a sum in another order than the same token's among the top
+ * ones; in the gradient's product dL/dz is rounded to bf16, except the given
+ * tokens', which are added in fp32.  The gradient's p = e^(z - lse) is as good as
+ * lse, rounded to fp32: relative errors up to e^(|lse| 2^-24) - 1 for |lse| <= 2^20.
+ * A row whose lse is below -2^20 is taken as one of nothing but (finite) masks and
+ * has gradient 0.  Above 2^20 lse does not hold the log of a number of equal logits:
+ * each of n that share the largest place has p = 1.  From hidden states the gradient
+ * takes finite weights (0 times an infinite one is NaN). */
 typedef struct {
     int64_t tokens;            /* rows, >= 0, < 2^24                                  */
     int64_t hidden;            /* fq_head_logprob_*: a multiple of 64, 64 .. 16384; fq_logprob_*: 0 */
@@ -516,7 +517,9 @@ typedef struct {
     int32_t given;             /* given tokens per row, 0 .. 64                       */
     int32_t top;               /* most likely tokens per row, 0 .. min(64, vocab)     */
 } fq_logprob_desc;
-/* Bytes of fq_logprob_fwd's device workspace (256-B aligned); 0 on a bad descriptor. */
+/* Bytes of fq_logprob_fwd's device workspace (256-B aligned); 0 on a bad descriptor.
+ * Here and below fewer tokens may need more (they are cut finer or go another way):
+ * a workspace for several counts has the largest of their sizes. */
 size_t fq_logprob_workspace_size(const fq_logprob_desc* d);
 /* logits: device bf16 [tokens, row_stride], 16-B aligned, of each row the first
  *   vocab elements; row_stride >= vocab, a multiple of 8.

@@ -365,3 +365,77 @@ def test_hidden_states_gradient_of_logits_past_fp32(m):
     got = _head_grad_check(h, w, z, ids, 12, m)
     assert np.all(got[8:] == 0.0)
     _head_grad_check(h, w, z, ids, 300, m)
+
+
+def _general(T, H, V, seed):
+    """bf16 normal values on no grid, and how well fp32 knows a logit: a product enters at most 32 additions inside a
+    matrix instruction, or H / 64 of a lane's and 6 of the lanes', then one per instruction of its wave, H / 16 at most;
+    each has an error of an ulp (two halves) at most."""
+    rng = np.random.default_rng(seed)
+    h, w = _bf(rng.standard_normal((T, H))), _bf(rng.standard_normal((V, H)) * 2 / np.sqrt(H))
+    h[:, :4] *= 8
+    hd, wd = h.astype(np.float64), w.astype(np.float64)
+    return h, w, hd @ wd.T, (64 + H / 8) * H32 * (np.abs(hd) @ np.abs(wd).T).max(-1)
+
+
+FORMS = [(1, 2048), (2, 320), (4, 2048), (8, 1024), (12, 2048), (30, 512), (64, 512), (40, 2048), (300, 192), (300, 2048)]
+
+
+@pytest.mark.parametrize("T,H", FORMS)
+def test_hidden_states_on_no_grid(T, H):
+    """Every form on general values: the products' own rounding is in the results.  Alternatives are compared by what
+    their logits are, as neighbours may change places."""
+    V, k = 5003, 20
+    h, w, z, zerr = _general(T, H, V, T + H)
+    top = np.argsort(-z, axis=-1, kind="stable")
+    ids = np.concatenate([top[:, :2], top[:, V // 2:V // 2 + 1]], 1).astype(np.int32)
+    got = _head_fwd(h, w, ids, k)
+    r = _check({n: v for n, v in got.items() if n != "top_ids" and n != "top_logp"}, z, ids, 0, zerr=zerr, what=(T, H))
+    tid, tlp = from_dev(got["top_ids"]), from_dev(got["top_logp"]).astype(np.float64)
+    assert np.all((tid >= 0) & (tid < V)) and all(len(set(row)) == k for row in tid)
+    at = np.take_along_axis(z, tid.astype(np.int64), 1)
+    kth = np.take_along_axis(z, top[:, k - 1:k], 1)
+    assert np.all(at >= kth - 2 * zerr[:, None]) and np.all(np.diff(at, axis=1) <= 2 * zerr[:, None])
+    sure = np.take_along_axis(z, top[:, :k], 1) > kth + 2 * zerr[:, None]
+    assert all(set(top[t, :k][sure[t]]) <= set(tid[t]) for t in range(T))
+    tol = ((160 + 8 + 4 + 2 * r["spread"]) * H32 + 2 * zerr)[:, None] + 8 * H32 * (np.abs(r["ls"])[:, None] + np.abs(tlp))
+    assert np.all(np.abs(tlp - np.take_along_axis(r["lp"], tid.astype(np.int64), 1)) <= tol)
+    # a given token and the same one among the alternatives: two sums of one logit
+    lp = from_dev(got["logp"]).astype(np.float64)
+    for j in range(2):
+        t, at = np.nonzero(tid == ids[:, j:j + 1])
+        assert np.all(np.abs(lp[t, j] - tlp[t, at]) <= 2 * zerr[t] + 4 * H32 * np.abs(lp[t, j]))
+
+
+@pytest.mark.parametrize("T,H", FORMS)
+@pytest.mark.parametrize("m,ent", [(1, True), (2, False)])
+def test_hidden_states_gradient_on_no_grid(T, H, m, ent):
+    F, T_ = _F(), torch()
+    V = 5003
+    h, w, z, zerr = _general(T, H, V, T + H + 1)
+    rng = np.random.default_rng(T)
+    ids = rng.integers(0, V, (T, m)).astype(np.int32)
+    ids[::2, 0] = np.argmax(z, -1)[::2]
+    dl = rng.standard_normal((T, m)).astype(np.float32)
+    de = rng.standard_normal(T).astype(np.float32) if ent else None
+    fwd = _head_fwd(h, w, None, 0)
+    d = F.logprob_desc(T, V, given=m, hidden=H)
+    g = T_.full((T, H), 9.0, dtype=T_.bfloat16, device="cuda")
+    F.head_logprob_bwd(d, to_dev_bf16(h), to_dev_bf16(w), fwd["lse"], g, ids=to_dev(ids), dlogp=to_dev(dl),
+                       entropy=fwd["entropy"] if ent else None, dentropy=to_dev(de) if ent else None,
+                       workspace=_workspace(F.head_logprob_workspace_size(d, True)))
+    T_.cuda.synchronize()
+    got = from_dev(g).astype(np.float64)
+    r, dz, p, tol = _grad_ref(z, ids, dl, de)
+    W, aw = w.astype(np.float64), np.abs(w.astype(np.float64))
+    given = np.zeros(z.shape, bool)
+    np.put_along_axis(given, ids.astype(np.int64), True, 1)
+    a = np.abs(dl).sum(-1, keepdims=True)
+    size = p * (a + (np.abs(de)[:, None] * (np.abs(r["lp"]) + r["entropy"][:, None] + 1) if ent else 0.0))
+    # the result's rounding, that of dL/dz beside the given tokens, the logits' own error (theirs and lse's: 2 zerr in
+    # log p, as much again in log p + entropy times its spread), fp32 sums over the vocabulary
+    z2 = (2 * zerr * (2 + r["spread"]))[:, None]
+    tol = (H16 * (np.abs(dz @ W) + np.where(given, 0.0, np.abs(dz)) @ aw) * 1.01 + (tol + size * np.expm1(z2) * 2) @ aw
+           + (V / 64 + 64) * H32 * ((np.abs(dz) + size) @ aw))
+    bad = ~(np.abs(got - dz @ W) <= tol)
+    assert not bad.any(), ((T, H), np.argwhere(bad)[:6], got[bad][:6], (dz @ W)[bad][:6], tol[bad][:6])
