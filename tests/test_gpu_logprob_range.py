@@ -439,3 +439,17 @@ def test_hidden_states_gradient_on_no_grid(T, H, m, ent):
            + (V / 64 + 64) * H32 * ((np.abs(dz) + size) @ aw))
     bad = ~(np.abs(got - dz @ W) <= tol)
     assert not bad.any(), ((T, H), np.argwhere(bad)[:6], got[bad][:6], (dz @ W)[bad][:6], tol[bad][:6])
+
+
+@pytest.mark.parametrize("far", [3e4, 1e30, np.inf])
+def test_a_tokens_sums_do_not_depend_on_its_neighbours(far):
+    """Bitwise the same beside tokens whose logits are far from 0 or infinite."""
+    T, H, V = 300, 128, 5003
+    h, w, ids, _ = _hidden(5, T, H, V, 1)
+    h[:, 3], w[:, 3] = 0.0, 1.0
+    alone = _head_fwd(h, w, ids, 5)
+    there = np.random.default_rng(1).random(T) < 0.3
+    h[there, 3] = _bf(far)
+    got = _head_fwd(h, w, ids, 5)
+    for n in alone:
+        assert np.array_equal(from_dev(got[n])[~there], from_dev(alone[n])[~there]), n
