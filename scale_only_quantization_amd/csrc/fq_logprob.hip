@@ -67,6 +67,12 @@ __device__ __forceinline__ uint64_t key_of(float z, int64_t col) {
 __device__ __forceinline__ int32_t key_id(uint64_t key) { return (int32_t)~(uint32_t)key; }
 __device__ __forceinline__ float key_z(uint64_t key) { return value_of((uint32_t)(key >> 32)); }
 
+// of s and u; a sum of one entry may be rounded below 1
+__device__ __forceinline__ float entropy_of(float s, float u) {
+    const float h = logf(s) - u / s;
+    return h < 0.0f ? 0.0f : h;                                    // (a NaN stays one)
+}
+
 // lanes below this one in a mask, and `from`
 __device__ __forceinline__ int lanes_before(uint64_t mask, int from) {
     return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, from));
@@ -526,7 +532,7 @@ __global__ __launch_bounds__(TPB) void k_rows_join(RowsArgs a) {
     const float ls = logf(s), lse = none ? -INFINITY : f + ls;
     if (threadIdx.x == 0) {
         if (a.lse) a.lse[t] = lse;
-        if (a.entropy) a.entropy[t] = none ? 0.0f : ls - u / s;
+        if (a.entropy) a.entropy[t] = none ? 0.0f : entropy_of(s, u);
     }
     auto logp = [&](float z) {                                     // z - f first: lse may be far from 0
         const float q = none ? -INFINITY : z - f - ls;
@@ -1133,7 +1139,7 @@ __global__ __launch_bounds__(64 * WPT * TOK) __attribute__((amdgpu_waves_per_eu(
     if (live && a.last && sub == 0) {
         if (lane == 0) {
             if (a.lse) a.lse[t] = lse;
-            if (ent) a.entropy[t] = none ? 0.0f : ls - u / s;
+            if (ent) a.entropy[t] = none ? 0.0f : entropy_of(s, u);
         }
     }
     if (live && a.last)

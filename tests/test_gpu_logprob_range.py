@@ -453,3 +453,22 @@ def test_a_tokens_sums_do_not_depend_on_its_neighbours(far):
     got = _head_fwd(h, w, ids, 5)
     for n in alone:
         assert np.array_equal(from_dev(got[n])[~there], from_dev(alone[n])[~there]), n
+
+
+@pytest.mark.parametrize("T", [12, 300])
+def test_entropies_are_never_negative(T):
+    """Rows that are sure of one entry: a sum of 1 and little else."""
+    rng = np.random.default_rng(T)
+    z = np.full((T, 300), -np.inf)
+    z[np.arange(T), rng.integers(0, 300, T)] = rng.standard_normal(T) * np.exp(rng.random(T) * 8)
+    got = _logits_fwd(_bf(z), None, 0)
+    assert np.all(from_dev(got["entropy"]) >= 0.0) and np.all(from_dev(got["entropy"]) <= 2 * H32)
+    assert np.all(np.abs(from_dev(got["lse"]) - _bf(z).max(-1)) <= 4 * H32 * (1 + np.abs(_bf(z).max(-1))))
+    h, w, _, _ = _hidden(1, T, 64, 300, 0)
+    h[:] = 0.0
+    h[:, 0] = _bf(np.abs(rng.standard_normal(T)) * np.exp(rng.random(T) * 6) + 1)
+    w[:] = 0.0
+    w[7, 0], w[np.arange(300) != 7, 0] = 3.0, -256.0
+    got = _head_fwd(h, w, None, 0)
+    ent = from_dev(got["entropy"])
+    assert np.all(ent >= 0.0) and np.all(ent <= 2 * H32)
