@@ -22,11 +22,11 @@
 //       pieces before; k_logp_merge joins a piece's strips to the tokens' running
 //       sums and alternatives.  In the backward it leaves dL/dz in bf16, which the
 //       loss's second product multiplies with the weight.
-// 16384 tokens of hidden 2048, 151936 entries, 64 alternatives: 8.0-8.4 ms, of
-// which the products 7.4 (1380 TFLOP/s; a library product of that size 1357 to
-// 1398) and the 16 merges 0.6-0.75; 2048 tokens 1.05-1.10 ms; 333 x 1024 x 32003
-// 43-47 us, one tile per CU, 33 in the product, whose two stages leave each load's
-// latency bare.  The gradient of 2048 tokens 1.94-2.06 ms, half in each product.
+// 16384 tokens of hidden 2048, 151936 entries, 64 alternatives: 8.0-8.7 ms, of
+// which the products 7.5-7.6 (1340 to 1355 TFLOP/s; a library product of that size
+// 1357 to 1398) and the 16 merges 0.75; 2048 tokens 1.05-1.10 ms; 333 x 1024 x 32003
+// 42-45 us, one tile per CU, 34 in the product, whose two stages leave each load's
+// latency bare.  The gradient of 2048 tokens 1.93-2.06 ms, half in each product.
 #include <algorithm>
 
 #include "fq_head_product.h"
@@ -294,7 +294,10 @@ __device__ __forceinline__ void opaque(uint4 (&v)[N]) {
 // unsorted, at most rows_keys(k) of them.  Bound by the vector unit: 8 operations
 // an element, one of them an exponential: 2048 rows of 151936 with 64 alternatives
 // 110-120 us and 12.5 for the join, 98 without alternatives (with 512 threads and
-// 32768 columns a block 9 more).
+// 32768 columns a block 9 more).  A chunk where more than rows_keys(k) entries reach
+// the bound (all equal; finite masks with fewer than k entries above them; the end
+// of a row with entries for fewer than k threads) reads itself again and cuts its
+// list on the way: such rows throughout take 930-990 us, masks of -inf 110-120.
 template <typename IN, int NL, bool ENT>
 __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
     constexpr int VEC = Vec<IN>::N, THREADS = TPB, CH = NL * VEC * THREADS, WAVES = THREADS / 64;
@@ -861,7 +864,11 @@ __device__ __forceinline__ float log2_p(float z, float lse) {
 //         with ENT u = sum e^(z - m) (z - m)
 //   TOP   these, and the 64 logits themselves where m is above the token's bound,
 //         the k-th best logit of the pieces before: of a long row that is seldom
-//   GRAD  P = -p (A + b (log p + entropy)) in bf16
+//   GRAD  P = -p (A + b (log p + entropy)) in bf16, for the matrix units: half a bf16
+//         step of each entry, of which a row of the gradient sums many, beside the
+//         half step of the result.  The gradient's distance from 64 bits is 0.0016 to
+//         0.0017 so and with P in fp32, the two forms 5e-4 to 7e-4 apart.  The given
+//         tokens' entries stay out of it: a - p A may cancel.
 enum : int { SUMS = 0, TOP = 1, GRAD = 2 };
 template <int MODE, bool ENT>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k_head_z(HeadLogpArgs a) {

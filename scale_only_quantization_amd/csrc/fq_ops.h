@@ -143,12 +143,12 @@ struct HeadLogpArgs {
     // workspace
     float* zs;             // [T, m] the given tokens' logits
     float* thr;            // forward [T]: the k-th best logit so far
-    float4* run;           // forward [T]: maximum in base 2, s and u so far; few tokens: of the chunks
+    float4* run;           // forward [T]: maximum, s and u so far (frames of z itself); few tokens: of the chunks
     uint64_t* keys;        // few tokens: of the chunks
     float* best_z;         // forward [T, k]: the best so far
     int32_t* best_i;
-    float2* stats;         // forward [vc / 64, T]: maximum and s of each strip
-    float* ustats;         // forward [vc / 64, T], with the entropy: u
+    float2* stats;         // forward [vc / 64, T]: maximum m and s = sum e^(z - m) of each strip
+    float* ustats;         // forward [vc / 64, T], with the entropy: u = sum e^(z - m) (z - m)
     float* z;              // forward [T, vc], with k: logits of a piece's strips above thr
     float4* rowc;          // backward [T]: lse, A + b entropy, b (0 of a row of masks); the bits of the one given id or of -1
     uint16_t* p;           // backward [T, vc]
