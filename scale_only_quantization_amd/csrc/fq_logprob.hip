@@ -25,7 +25,7 @@
 // 16384 tokens of hidden 2048, 151936 entries, 64 alternatives: 8.0-8.7 ms, of
 // which the products 7.5-7.6 (1340 to 1355 TFLOP/s; a library product of that size
 // 1357 to 1398) and the 16 merges 0.75; 2048 tokens 1.05-1.10 ms; 333 x 1024 x 32003
-// 42-45 us, one tile per CU, 34 in the product, whose two stages leave each load's
+// 42-48 us, one tile per CU, 34 in the product, whose two stages leave each load's
 // latency bare.  The gradient of 2048 tokens 1.93-2.06 ms, half in each product.
 #include <algorithm>
 
@@ -376,7 +376,7 @@ __global__ __launch_bounds__(TPB) void k_rows_chunk(RowsArgs a) {
             s += red[0][i];
             u += red[1][i];
         }
-        // terms 2^(l + d') and their l: both sums times 2^-d, and the second's frame moved by d
+        // the terms are 2^l with l = (z - M) log2 e + d: both sums by 2^-d, and d off the second's l
         const float g = __builtin_fmaf(-d, LN2, 1.0f);
         a.part[t * a.nc + c] = make_float4(M, g * s, g * LN2 * __builtin_fmaf(-d, s, u), 0.0f);
     }
@@ -714,7 +714,7 @@ __global__ __launch_bounds__(ROW_TPB) void k_head_rows(HeadLogpArgs a) {
     auto multiply = [&](const u32x4 (&v)[ROW_GO][ROW_N]) {
 #pragma unroll
         for (int j = 0; j < ROW_GO; ++j) {
-            if ((c + j) * 512 + lane * 8 >= H) break;              // (past the row the weight's may be infinite)
+            if ((c + j) * 512 + lane * 8 >= H) break;              // (past the row's end are its first columns again)
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
                 const u32x4 x = *reinterpret_cast<const u32x4*>(sh + t * Hp + (c + j) * 512 + lane * 8);
@@ -1334,7 +1334,8 @@ __global__ __launch_bounds__(256) void k_logp_out(HeadLogpArgs a, int splits) {
         const float4 rc = a.rowc[t];
         const float l = log2_p(a.zs[t * a.m + j], rc.x);
         sid[j] = in ? id : 0;
-        scoef[j] = in && !(a.lse[t] <= MASKS) ? a.dlogp[t * a.m + j] - (first ? exp2_hw(l) * __builtin_fmaf(rc.z * LN2, l, rc.y) : 0.0f) : 0.0f;
+        const float own = first ? exp2_hw(l) * __builtin_fmaf(rc.z * LN2, l, rc.y) : 0.0f;
+        scoef[j] = in && !(a.lse[t] <= MASKS) ? a.dlogp[t * a.m + j] - own : 0.0f;
     }
     __syncthreads();
     typedef uint32_t words __attribute__((ext_vector_type(VEC / 2)));

@@ -150,7 +150,7 @@ struct HeadLogpArgs {
     float2* stats;         // forward [vc / 64, T]: maximum m and s = sum e^(z - m) of each strip
     float* ustats;         // forward [vc / 64, T], with the entropy: u = sum e^(z - m) (z - m)
     float* z;              // forward [T, vc], with k: logits of a piece's strips above thr
-    float4* rowc;          // backward [T]: lse, A + b entropy, b (0 of a row of masks); the bits of the one given id or of -1
+    float4* rowc;          // backward [T]: lse, A + b entropy, b (0 of a row of masks); the one given id's bits or -1's
     uint16_t* p;           // backward [T, vc]
     float* g;              // backward [splits, T, H]
     float* ones;           // backward [T]

@@ -472,3 +472,68 @@ def test_entropies_are_never_negative(T):
     got = _head_fwd(h, w, None, 0)
     ent = from_dev(got["entropy"])
     assert np.all(ent >= 0.0) and np.all(ent <= 2 * H32)
+
+
+@pytest.mark.parametrize("T", [12, 300])
+@pytest.mark.parametrize("k", [0, 20])
+def test_logits_without_the_entropy(T, k):
+    """The same bits with and without it, near 0 and far."""
+    F, T_ = _F(), torch()
+    V = 9001
+    rng = np.random.default_rng(T)
+    z = _bf(np.concatenate([_masked(s, V, rng) for s in (1e4, 1e9, 1e30, LOWEST)] * 11)[:T])
+    ids = rng.integers(0, V, (T, 2)).astype(np.int32)
+    want = _logits_fwd(z, ids, k)
+    got = {n: None if v is None or n == "entropy" else T_.full_like(v, 9) for n, v in want.items()}
+    d = F.logprob_desc(T, V, given=2, top=k)
+    F.logprob_fwd(d, _padded(z, 0, np.nan)[1], ids=to_dev(ids), workspace=_workspace(F.logprob_workspace_size(d)), **got)
+    T_.cuda.synchronize()
+    for n, v in got.items():
+        assert v is None or T_.equal(v, want[n]), n
+
+
+def test_as_many_rows_as_the_contract_takes():
+    """2^24 - 1 rows, from logits and from hidden states, forward and backward: rows of the same kind, at every place,
+    equal the first of their kind."""
+    F, T_ = _F(), torch()
+    T, V, H, kinds = (1 << 24) - 1, 40, 64, 5
+
+    def spread(x):
+        return to_dev_bf16(x)[T_.arange(T, device="cuda") % kinds].contiguous()
+
+    def same(x):
+        n = T // kinds * kinds
+        assert bool((x[:n].reshape(n // kinds, kinds, -1) == x[:kinds].reshape(1, kinds, -1)).all())
+        assert T_.equal(x[n:], x[:T - n])
+
+    h, w, _, z = _hidden(3, kinds, H, V, 0)
+    at = (T_.arange(T, device="cuda") % kinds).int()
+    ids = (at * 7)[:, None].contiguous()
+    dl, de = (at.float() - 1.5)[:, None].contiguous(), (at.float() * 0.1)
+    for hidden in (0, H):
+        zz = z if hidden else _bf(z)
+        d = F.logprob_desc(T, V, given=1, top=3, hidden=hidden)
+        out = dict(lse=T_.empty(T, device="cuda"), entropy=T_.empty(T, device="cuda"), logp=T_.empty((T, 1), device="cuda"),
+                   top_ids=T_.empty((T, 3), dtype=T_.int32, device="cuda"), top_logp=T_.empty((T, 3), device="cuda"))
+        x = spread(h if hidden else zz)
+        if hidden:
+            wd = to_dev_bf16(w)
+            F.head_logprob_fwd(d, x, wd, ids=ids, workspace=_workspace(F.head_logprob_workspace_size(d)), **out)
+            F.head_logprob_bwd(d, x, wd, out["lse"], x, ids=ids, dlogp=dl, entropy=out["entropy"], dentropy=de,
+                               workspace=_workspace(F.head_logprob_workspace_size(d, True)))
+        else:
+            F.logprob_fwd(d, x, ids=ids, workspace=_workspace(F.logprob_workspace_size(d)), **out)
+            F.logprob_bwd(d, x, out["lse"], x, ids=ids, dlogp=dl, entropy=out["entropy"], dentropy=de)
+        T_.cuda.synchronize()
+        first = np.arange(kinds)
+        _check({n: v[:kinds] for n, v in out.items()}, zz, (first * 7).astype(np.int32)[:, None], 3, what=hidden)
+        for v in out.values():
+            same(v)
+        same(x)
+        _, dz, p, tol = _grad_ref(zz.astype(np.float64), (first * 7)[:, None], from_dev(dl[:kinds]), from_dev(de[:kinds]))
+        aw = np.abs(w.astype(np.float64)) if hidden else np.eye(V)
+        ref = dz @ w.astype(np.float64) if hidden else dz
+        tol = H16 * (np.abs(ref) + (np.abs(dz) @ aw if hidden else 0.0)) * 1.001 + tol @ aw + 64 * H32 * (np.abs(dz) @ aw)
+        assert np.all(np.abs(from_dev(x[:kinds]) - ref) <= tol)
+        del x, out
+        T_.cuda.empty_cache()
